@@ -23,6 +23,9 @@
  *      its sequence selects, through sel_slot.
  *   6. ech_kv_append: each sequence's decoded token joins the host pool and
  *      the key cache (growing contexts).
+ * Next to it, layers that keep their rows resident (contexts below k tokens,
+ * windowed layers, budgeted caches) hold them in pages of a device pool:
+ * ech_paged_append, ech_paged_attn, ech_paged_weight, ech_paged_evict.
  *
  * Conventions
  *  - Ownership: the caller owns every buffer (device memory, the pinned host
@@ -92,11 +95,11 @@ extern "C" {
 #define ECH_CTR_EARLY_WALK 15 /* ring positions the last EARLY phase walked, head to last slot it allocated (0: none) */
 #define ECH_CTR_LEN      16
 
-/* ---- sticky status bits in ctr[ECH_CTR_STATUS] */
+/* ---- sticky status bits in ctr[ECH_CTR_STATUS] (and in ech_paged_append's status word) */
 #define ECH_ST_OVERFLOW   1   /* a FINAL/PREFILL phase found fewer unpinned slots than misses */
 #define ECH_ST_BADTOK     2   /* a selected token offset was outside [0, len) */
 #define ECH_ST_BADMISS    4   /* ech_recall saw a miss entry with g >= P or slot >= C */
-#define ECH_ST_FULL       8   /* ech_kv_append found a sequence at its capacity */
+#define ECH_ST_FULL       8   /* ech_kv_append found a sequence at its capacity; ech_paged_append a position without a page */
 #define ECH_ST_TIMEOUT   16   /* a bounded wait inside ech_index_logits_early ran out (results invalid) */
 
 /* Human-readable name of a return code. */
@@ -443,6 +446,119 @@ int ech_sparse_attn(const void* q, const void* dev_cache, int32_t C, const int32
 int ech_kv_append(void* host_pool, int64_t P, int64_t row_bytes, void* kcache, int kdtype, float* kscale,
                   int32_t* tok2slot, const int64_t* seq_tok0, int32_t* seq_len, const int32_t* seq_cap, int B,
                   const void* new_rows, const void* new_keys, const float* new_scales, int32_t* ctr, void* stream);
+
+/*
+ * The resident paged cache. A layer whose rows stay on the device keeps them
+ * in pages of a pool [n_slots, row]: token t of sequence b is pool row
+ *     page_table[b*pt_ld + t / page_size] * page_size + t % page_size.
+ * A pool may hold many layers' or sequences' pages in any order, sequences may
+ * share pages that are only read (a common prompt), and with page_size 1 the
+ * table is a list of slots like sel_slot. A step brings T new rows, those of
+ * sequence b being row0[b] .. row0[b+1]-1 (none, one, or a prompt's chunk);
+ * seq_len[b] counts the sequence's tokens with them, so its i-th of n new rows
+ * is the token at position seq_len[b] - n + i. Common arguments:
+ *  page_table [B, pt_ld] int32, device; page_size 1 .. 2^20 (any, not only
+ *             powers of two). An entry outside the pool (negative, or a slot
+ *             past n_slots) is no page: its tokens are not written, not read
+ *             and count as absent, as entries of sel_slot do.
+ *  row0       [B+1] int32, device, ascending, 0 <= row0[0], row0[B] <= T. Rows
+ *             of no sequence (before row0[0], from row0[B] on) are ignored and
+ *             their outputs left as they were.
+ *  seq_len    [B] int32, device. max_rows >= every row0[b+1] - row0[b] and
+ *             max_len >= every seq_len[b] are host bounds that size the grids;
+ *             lengths beyond max_len or the table are cut there, and of a
+ *             sequence with more than max_rows new rows only the first
+ *             max_rows are computed.
+ *  B 1 .. 65535; T*H < 2^30; n_slots < 2^31 (offsets are 64-bit). All four
+ *  calls may be captured; replays follow row0, seq_len and the table in place.
+ */
+
+/*
+ * ech_paged_append - a step's new rows go into their sequences' pages.
+ * Row r of sequence b lands in the slot of its position (above), row_bytes
+ * each. A row whose position has no page (or is negative) is not written and
+ * sets ECH_ST_FULL in *status (int32, device; NULL: no word). Page tables must
+ * not give two of the step's positions the same slot.
+ *  rows [T, row_bytes], row_stride bytes apart, 16-byte aligned; row_bytes and
+ *  row_stride multiples of 16, row_bytes <= row_stride. pool 16-byte aligned.
+ */
+int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, int page_size, const int32_t* page_table,
+                     int64_t pt_ld, const int32_t* row0, const int32_t* seq_len, int B, int T, const void* rows,
+                     int64_t row_stride, int32_t* status, void* stream);
+
+/*
+ * ech_paged_attn - attention of a step's new rows over their sequences' pages
+ * (their own rows included: append first). Rows are absorbed-MLA rows of 576
+ * bf16 values, all of them the key and the first 512 the value, shared by all
+ * heads. The row at position p sees token t iff t <= p, and with window > 0
+ * only if also t > p - window or t < n_sink (a sliding window, with the first
+ * n_sink tokens always visible; window 0: no limit). For new row r, head h:
+ *   s_t = sm_scale * q[r,h,:] . pool[slot_t, :]        (visible t with a page)
+ *   out[r,h,:] = sum_t softmax(s)_t * pool[slot_t, 0:512]
+ *   lse[r,h] = log sum_t exp(s_t)
+ * A row that sees nothing gets out = 0 and lse = -inf. Infinities and NaN in
+ * rows that a query does not see do not reach its output. Scores, maxima and
+ * sums are fp32; the softmax weights enter the value product as bf16.
+ *  q     [T, H, 576] bf16; strides in values between rows and heads, multiples
+ *        of 8; 16-byte aligned. H 1 .. 128, any.
+ *  pool  [n_slots, 576] bf16, 16-byte aligned.
+ *  out   [T, H, 512] bf16, 16-byte aligned; lse [T, H] fp32 or NULL.
+ *  ws    ech_paged_attn_ws_bytes(...) bytes, 256-byte aligned, uninitialised
+ *        OK; may be NULL where that is 0. Calls that share it must be ordered.
+ */
+size_t ech_paged_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink);
+int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool, int64_t n_slots,
+                   int page_size, const int32_t* page_table, int64_t pt_ld, const int32_t* row0,
+                   const int32_t* seq_len, int B, int T, int H, int max_rows, int max_len, int window, int n_sink,
+                   float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ech_paged_weight - the attention weight each cached token received from a
+ * step's new rows, added to a decayed running sum. For t < seq_len[b]:
+ *   acc_out[b,t] = decay * acc_in[b,t] + sum over the new rows r of b that see
+ *                  t and heads h of exp(sm_scale * q[r,h,:] . pool[slot_t,:] - lse[r,h])
+ * with the masks, q, pool and lse of the step's ech_paged_attn call. Entries
+ * t >= seq_len[b] are neither read nor written, so a new token's acc_in entry
+ * must have been set (0) by the caller. A token without a page receives 0. The
+ * additions of a token have one order: the same call gives the same bits.
+ *  acc_in [B, acc_ld] fp32 or NULL (all 0); acc_out [B, acc_ld] fp32, may be
+ *  acc_in. acc_ld >= max_len.
+ *  ws ech_paged_weight_ws_bytes(...) bytes, as for ech_paged_attn.
+ */
+size_t ech_paged_weight_ws_bytes(int B, int T, int H, int max_rows, int max_len);
+int ech_paged_weight(const void* q, int64_t q_row_stride, int64_t q_head_stride, const float* lse, const void* pool,
+                     int64_t n_slots, int page_size, const int32_t* page_table, int64_t pt_ld, const int32_t* row0,
+                     const int32_t* seq_len, int B, int T, int H, int max_rows, int max_len, int window, int n_sink,
+                     float sm_scale, const float* acc_in, float* acc_out, int64_t acc_ld, float decay, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * ech_paged_evict - eviction from a budgeted cache by accumulated weight. A
+ * sequence of n = seq_len[b] > keep tokens keeps its first n_sink tokens, its
+ * last n_recent, and of those between the keep - n_sink - n_recent with the
+ * largest acc[b,t] (equal weights: the lower t; -0 equals +0; NaN counts as
+ * larger than anything). A sequence of n <= keep keeps all of them.
+ *   kept    [B, keep] int32: the kept tokens, ascending, -1 from len_out[b] on
+ *   len_out [B] int32 = min(n, keep); may be seq_len
+ *   acc_out [B, acc_ld] or NULL: the kept tokens' weights in the same order,
+ *           then 0 up to max_len; may be acc
+ * With pool != NULL the kept rows then move together: kept token j's row goes
+ * from its slot in src_table to the slot of token j in dst_table (both [B,
+ * pt_ld]). dst_table is either src_table itself (the same pointer: the cache
+ * is compacted in place, and pages from ceil(len_out / page_size) on are free)
+ * or names only pages that src_table does not; rows are then copied, the
+ * sequences that keep everything included. A row without a slot on either side
+ * is not moved. In place, no two sequences may share a page, and no page
+ * may occur twice.
+ *  keep >= 1, n_sink + n_recent <= keep, acc_ld >= max_len, row_bytes a
+ *  multiple of 16, pool 16-byte aligned.
+ *  ws ech_paged_evict_ws_bytes(...) bytes, as for ech_paged_attn.
+ */
+size_t ech_paged_evict_ws_bytes(int B, int max_len, int keep);
+int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* seq_len, int B, int max_len, int keep, int n_sink,
+                    int n_recent, int32_t* kept, float* acc_out, int32_t* len_out, void* pool, int64_t n_slots,
+                    int64_t row_bytes, int page_size, const int32_t* src_table, const int32_t* dst_table,
+                    int64_t pt_ld, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

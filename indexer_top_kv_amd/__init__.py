@@ -23,8 +23,9 @@ from ._native import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, ECH_KEY_BF16, ECH_KEY_F
 
 __all__ = ['ech_kv_append', 'ech_sparse_attn', 'ech_sparse_attn_ws_bytes', 'ech_index_logits', 'ech_index_logits_causal', 'ech_topk', 'ech_topk_noalloc', 'ech_topk_ws_bytes', 'ech_cache_reset',
            'ech_cache_step', 'ech_cache_step_ws_bytes', 'ech_recall', 'ech_index_logits_early',
-           'ech_index_logits_early_ws_bytes', 'ech_recall_early_live', 'ech_recall_rest', 'ech_topk_early', 'EchError', 'LayerState',
-           'lib']
+           'ech_index_logits_early_ws_bytes', 'ech_recall_early_live', 'ech_recall_rest', 'ech_topk_early', 'ech_paged_append',
+           'ech_paged_attn', 'ech_paged_attn_ws_bytes', 'ech_paged_weight', 'ech_paged_weight_ws_bytes',
+           'ech_paged_evict', 'ech_paged_evict_ws_bytes', 'EchError', 'LayerState', 'lib']
 
 
 class EchError(RuntimeError):
@@ -260,3 +261,170 @@ def ech_kv_append(host_pool, kcache, kscale, state: LayerState, seq_tok0, seq_le
         _ptr(host_pool), host_pool.shape[0], row_bytes, _ptr(kcache), _key_dtype(kcache), _ptr(kscale),
         _ptr(state.tok2slot), _ptr(seq_tok0), _ptr(seq_len), _ptr(seq_cap), seq_tok0.shape[0], _ptr(new_rows),
         _ptr(new_keys), _ptr(new_scales), _ptr(state.ctr), _stream(stream)))
+
+
+# ------------------------------------------------------------------ resident paged cache
+_BITS16 = (torch.int16, torch.uint16, torch.bfloat16)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+
+
+def _arg(name: str, t: torch.Tensor, dtypes, shape, device: torch.device, inner: int = 0) -> None:
+    """Refuse a tensor that the kernels would misread: its type, shape (None:
+    any), device, or strides (its last `inner` dimensions are dense; 0: all)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f'{name}: unsupported dtype {t.dtype}')
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f'{name}: shape {tuple(t.shape)}, expected {tuple("any" if w is None else w for w in shape)}')
+    if t.device != device or device.type != 'cuda':
+        raise ValueError(f'{name}: on {t.device}, expected a GPU tensor{"" if device.type != "cuda" else f" on {device}"}')
+    if not t.is_contiguous():
+        n, want = t.dim(), 1
+        for d in range(n - 1, (n - inner if inner else 0) - 1, -1):
+            if t.shape[d] != 1 and t.stride(d) != want:
+                raise ValueError(f'{name}: strides {t.stride()} of shape {tuple(t.shape)} are not supported')
+            want *= t.shape[d]
+
+
+def _ws_arg(ws: Optional[torch.Tensor], device: torch.device):
+    """(pointer, bytes) of a workspace, or (None, 0) without one."""
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f'ws: expected a contiguous tensor on {device}')
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+class _on:
+    """The device of a call's tensors made current for its launches, and the
+    stream they go to: the caller's, or that device's current one."""
+    __slots__ = ('device', 'stream', 'back')
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.back = device, stream, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if self.device.index is not None and self.device.index != cur:
+            self.back = cur
+            torch.cuda.set_device(self.device)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _paged_args(pool, page_table, row0, seq_len, dtypes):
+    """Checks shared by the paged calls; returns (device, B)."""
+    dev = pool.device
+    _arg('pool', pool, dtypes, (None, None), dev)
+    B = seq_len.shape[0] if seq_len.dim() == 1 else -1
+    _arg('seq_len', seq_len, _I32, (None,), dev)
+    _arg('row0', row0, _I32, (B + 1,), dev)
+    _arg('page_table', page_table, _I32, (B, None), dev)
+    return dev, B
+
+
+def ech_paged_append(pool, page_table, page_size: int, row0, seq_len, rows, status=None, stream=None) -> None:
+    """A step's new rows [T, row] go into their sequences' pages: pool [slots,
+    row] (any type of `rows`' element size), page_table [B, pages] i32, row0
+    [B+1] i32, seq_len [B] i32 (with the new rows), status [1] i32 or None."""
+    dev, B = _paged_args(pool, page_table, row0, seq_len, (pool.dtype,))
+    _arg('rows', rows, (pool.dtype,), (None, pool.shape[1]), dev, inner=1)
+    if status is not None:
+        _arg('status', status, _I32, (1,), dev)
+    T, es = rows.shape[0], pool.element_size()
+    with _on(dev, stream) as s:
+        _check('ech_paged_append', lib().ech_paged_append(
+            _ptr(pool), pool.shape[0], pool.shape[1] * es, int(page_size), _ptr(page_table), page_table.shape[1],
+            _ptr(row0), _ptr(seq_len), B, T, _ptr(rows), (rows.stride(0) if T > 1 else rows.shape[1]) * es,
+            _ptr(status), s))
+
+
+def ech_paged_attn_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int, window: int = 0,
+                            n_sink: int = 0) -> int:
+    return int(lib().ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink))
+
+
+def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows: int, max_len: int, sm_scale: float,
+                   out, lse=None, window: int = 0, n_sink: int = 0, ws=None, stream=None) -> None:
+    """Causal attention of a step's new rows over their sequences' pages, with
+    an optional sliding window and n_sink first tokens that stay visible: q
+    [T, H, 576] bf16 (or its bits; rows and heads may be strided), pool [slots,
+    576] bf16 -> out [T, H, 512] bf16, lse [T, H] fp32 (optional)."""
+    dev, B = _paged_args(pool, page_table, row0, seq_len, _BITS16)
+    _arg('pool', pool, _BITS16, (None, 576), dev)
+    _arg('q', q, _BITS16, (None, None, 576), dev, inner=1)
+    T, H = q.shape[0], q.shape[1]
+    _arg('out', out, _BITS16, (T, H, 512), dev)
+    if lse is not None:
+        _arg('lse', lse, _F32, (T, H), dev)
+    wp, wb = _ws_arg(ws, dev)
+    with _on(dev, stream) as s:
+        _check('ech_paged_attn', lib().ech_paged_attn(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(pool), pool.shape[0], int(page_size), _ptr(page_table),
+            page_table.shape[1], _ptr(row0), _ptr(seq_len), B, T, H, int(max_rows), int(max_len), int(window),
+            int(n_sink), float(sm_scale), _ptr(out), _ptr(lse), wp, wb, s))
+
+
+def ech_paged_weight_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int) -> int:
+    return int(lib().ech_paged_weight_ws_bytes(B, T, H, max_rows, max_len))
+
+
+def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, max_rows: int, max_len: int,
+                     sm_scale: float, acc_in, acc_out, decay: float = 1.0, window: int = 0, n_sink: int = 0, ws=None,
+                     stream=None) -> None:
+    """The attention weight each cached token received from the step's rows
+    and heads (lse: that of ech_paged_attn), added to decay * acc_in: acc_in
+    [B, >= max_len] fp32 or None, acc_out like it (may be acc_in)."""
+    dev, B = _paged_args(pool, page_table, row0, seq_len, _BITS16)
+    _arg('pool', pool, _BITS16, (None, 576), dev)
+    _arg('q', q, _BITS16, (None, None, 576), dev, inner=1)
+    T, H = q.shape[0], q.shape[1]
+    _arg('lse', lse, _F32, (T, H), dev)
+    _arg('acc_out', acc_out, _F32, (B, None), dev)
+    if acc_in is not None:
+        _arg('acc_in', acc_in, _F32, (B, acc_out.shape[1]), dev)
+    wp, wb = _ws_arg(ws, dev)
+    with _on(dev, stream) as s:
+        _check('ech_paged_weight', lib().ech_paged_weight(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(lse), _ptr(pool), pool.shape[0], int(page_size),
+            _ptr(page_table), page_table.shape[1], _ptr(row0), _ptr(seq_len), B, T, H, int(max_rows), int(max_len),
+            int(window), int(n_sink), float(sm_scale), _ptr(acc_in), _ptr(acc_out), acc_out.shape[1], float(decay),
+            wp, wb, s))
+
+
+def ech_paged_evict_ws_bytes(B: int, max_len: int, keep: int) -> int:
+    return int(lib().ech_paged_evict_ws_bytes(B, max_len, keep))
+
+
+def ech_paged_evict(acc, seq_len, max_len: int, keep: int, n_sink: int, n_recent: int, kept, len_out, acc_out=None,
+                    pool=None, src_table=None, dst_table=None, page_size: int = 1, ws=None, stream=None) -> None:
+    """Keep `keep` tokens of each longer sequence: the first n_sink, the last
+    n_recent and the heaviest between (acc [B, >= max_len] fp32). kept [B,
+    keep] i32 (ascending, -1 padded), len_out [B] i32, acc_out like acc or
+    None. With a pool the kept rows move from src_table's pages to dst_table's
+    (src_table itself: compacted in place)."""
+    dev, B = acc.device, (seq_len.shape[0] if seq_len.dim() == 1 else -1)
+    _arg('seq_len', seq_len, _I32, (None,), dev)
+    _arg('acc', acc, _F32, (B, None), dev)
+    _arg('kept', kept, _I32, (B, int(keep)), dev)
+    _arg('len_out', len_out, _I32, (B,), dev)
+    if acc_out is not None:
+        _arg('acc_out', acc_out, _F32, (B, acc.shape[1]), dev)
+    n_slots = row_bytes = ld = 0
+    if pool is not None:
+        _arg('pool', pool, (pool.dtype,), (None, None), dev)
+        if src_table is None or dst_table is None:
+            raise ValueError('src_table and dst_table are needed to move the rows of a pool')
+        _arg('src_table', src_table, _I32, (B, None), dev)
+        _arg('dst_table', dst_table, _I32, (B, src_table.shape[1]), dev)
+        n_slots, row_bytes, ld = pool.shape[0], pool.shape[1] * pool.element_size(), src_table.shape[1]
+    wp, wb = _ws_arg(ws, dev)
+    with _on(dev, stream) as s:
+        _check('ech_paged_evict', lib().ech_paged_evict(
+            _ptr(acc), acc.shape[1], _ptr(seq_len), B, int(max_len), int(keep), int(n_sink), int(n_recent),
+            _ptr(kept), _ptr(acc_out), _ptr(len_out), _ptr(pool), n_slots, row_bytes, int(page_size),
+            _ptr(src_table) if pool is not None else None, _ptr(dst_table) if pool is not None else None, ld, wp, wb,
+            s))

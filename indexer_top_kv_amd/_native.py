@@ -72,6 +72,18 @@ SIGNATURES = {
     'ech_sparse_attn_ws_bytes': (_sz, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
     'ech_sparse_attn': (ctypes.c_int, [_p, _p, _i32, _p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
                                        _p, _p, _p, _sz, _p]),
+    'ech_paged_append': (ctypes.c_int, [_p, _i64, _i64, ctypes.c_int, _p, _i64, _p, _p, ctypes.c_int, ctypes.c_int, _p,
+                                        _i64, _p, _p]),
+    'ech_paged_attn_ws_bytes': (_sz, [ctypes.c_int] * 7),
+    'ech_paged_attn': (ctypes.c_int, [_p, _i64, _i64, _p, _i64, ctypes.c_int, _p, _i64, _p, _p, *[ctypes.c_int] * 7,
+                                      ctypes.c_float, _p, _p, _p, _sz, _p]),
+    'ech_paged_weight_ws_bytes': (_sz, [ctypes.c_int] * 5),
+    'ech_paged_weight': (ctypes.c_int, [_p, _i64, _i64, _p, _p, _i64, ctypes.c_int, _p, _i64, _p, _p,
+                                        *[ctypes.c_int] * 7, ctypes.c_float, _p, _p, _i64, ctypes.c_float, _p, _sz,
+                                        _p]),
+    'ech_paged_evict_ws_bytes': (_sz, [ctypes.c_int] * 3),
+    'ech_paged_evict': (ctypes.c_int, [_p, _i64, _p, *[ctypes.c_int] * 5, _p, _p, _p, _p, _i64, _i64, ctypes.c_int, _p,
+                                       _p, _i64, _p, _sz, _p]),
 }
 
 _lib = None

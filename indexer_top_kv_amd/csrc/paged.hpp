@@ -1,0 +1,98 @@
+// What the paged-cache kernels share: how a batch's new rows, positions and
+// pages are read, and which tokens a row sees.
+//
+// A resident layer keeps its rows in pages of a pool: token t of sequence b is
+// slot page_table[b][t / page_size] * page_size + t % page_size. A step brings
+// rows row0[b] .. row0[b+1]-1 of sequence b, the last ones of its seq_len[b]
+// tokens: its row i is at position seq_len[b] - n + i and sees tokens t <=
+// position (with a window: those with t > position - window, or t < n_sink).
+// Everything read from the device is clamped to the host's bounds, so no table
+// or length, however wrong, leads outside a buffer.
+#pragma once
+
+#include "common.hpp"
+
+namespace {
+
+constexpr int kPagedRow = 576;             // values per row (key width)
+constexpr int kPagedVal = 512;             // value width: the row's first values
+constexpr int kPagedChunks = kPagedRow * 2 / 16;   // 16-byte pieces of a row (72)
+
+struct Pages {
+  const int32_t* table;   // [B, ld]
+  int64_t ld;             // page-table entries per sequence
+  int64_t n_slots;        // rows in the pool
+  int size;               // tokens per page
+};
+
+// Slot of token t of the sequence whose page-table row is `row`, or -1 where
+// the table has no valid page for it.
+__device__ __forceinline__ int slot_of(const Pages& pg, const int32_t* row, int t) {
+  const uint32_t idx = (uint32_t)t / (uint32_t)pg.size;
+  if ((int64_t)idx >= pg.ld) return -1;
+  const int page = row[idx];
+  const int64_t s = (int64_t)page * pg.size + (t - (int)idx * pg.size);
+  return page >= 0 && s < pg.n_slots ? (int)s : -1;
+}
+
+// The new rows of one sequence, clamped: rows [first, first + n), row i at
+// position pos0 + i (negative: it sees nothing), tokens below len exist.
+struct SeqRows {
+  int first, n, pos0, len;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const int32_t* row0, const int32_t* seq_len, const Pages& pg, int b, int T,
+                                            int max_rows, int max_len) {
+  const int r0 = min(max(row0[b], 0), T), r1 = min(max(row0[b + 1], r0), T);
+  const int64_t cap = min((int64_t)max_len, pg.ld * (int64_t)pg.size);
+  const int len = (int)min((int64_t)max(seq_len[b], 0), cap);
+  return SeqRows{r0, min(r1 - r0, max_rows), len - (r1 - r0), len};
+}
+
+// Which sequence and which of its tiles `tile` is, when sequence b's n rows of
+// H heads make ceil(n H / per) tiles and the tiles are numbered through the
+// batch; b = -1 past the last one. Every lane of the wave takes part: 64
+// sequences a round.
+__device__ __forceinline__ void find_tile(const int32_t* row0, int B, int T, int max_rows, int H, int per, int tile,
+                                          int* b_out, int* t_out) {
+  const int lane = ech::lane_id();
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < B) {
+      const int r0 = min(max(row0[b], 0), T), r1 = min(max(row0[b + 1], r0), T);
+      n = min(r1 - r0, max_rows);
+    }
+    const int tiles = (int)(((int64_t)n * H + per - 1) / per);
+    const int incl = ech::wave_incl_scan(tiles);
+    const unsigned long long past = __ballot(base + incl > tile);
+    if (past != 0ull) {
+      const int l = __builtin_ctzll(past);
+      *b_out = b0 + l;
+      *t_out = tile - base - (__shfl(incl, l, 64) - __shfl(tiles, l, 64));
+      return;
+    }
+    base += __shfl(incl, 63, 64);
+  }
+  *b_out = -1;
+  *t_out = 0;
+}
+
+// Whether a row at position p sees token t (t < len is the caller's).
+__device__ __forceinline__ bool sees(int p, int t, int window, int n_sink) {
+  return t <= p && (window == 0 || t > p - window || t < n_sink);
+}
+
+inline bool aligned16_(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Host checks shared by the entry points.
+inline bool pages_ok(int64_t n_slots, int page_size, const int32_t* table, int64_t ld) {
+  return table && n_slots >= 1 && n_slots < (1ll << 31) && page_size >= 1 && page_size <= (1 << 20) && ld >= 1 &&
+         ld < (1ll << 31);
+}
+inline bool batch_ok(int B, int T, int max_rows, int max_len) {
+  return B >= 1 && B <= 65535 && T >= 0 && max_rows >= 0 && max_len >= 0 && max_len <= (1 << 30);
+}
+
+}  // namespace

@@ -1,0 +1,106 @@
+"""The resident paged cache without a GPU: refusals of the C ABI and of the
+binding, and the oracle against closed forms."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import indexer_top_kv_amd as ech
+import oracle
+import paged_abi_checks
+from oracle.numerics import bf16_to_f64
+from test_abi import ROOT, _clang_rt
+import workloads as wk
+
+
+@pytest.mark.parametrize('check', paged_abi_checks.CHECKS, ids=lambda f: f.__name__)
+def test_argument_checks(check):
+    check(ech.lib())
+
+
+def test_argument_checks_under_asan_ubsan():
+    from indexer_top_kv_amd import build as b
+    rt = _clang_rt('asan')
+    if rt is None or not os.path.exists(os.environ.get('HIPCC', '/opt/rocm/bin/hipcc')):
+        pytest.skip('no hipcc or sanitizer runtime')
+    lib = b.build_sanitized()
+    env = dict(os.environ, LD_PRELOAD=rt, ASAN_OPTIONS='detect_leaks=0:abort_on_error=1',
+               UBSAN_OPTIONS='halt_on_error=1:print_stacktrace=1',
+               LD_LIBRARY_PATH=os.path.dirname(rt) + ':' + os.environ.get('LD_LIBRARY_PATH', ''))
+    r = subprocess.run([sys.executable, os.path.join(ROOT, 'tests', 'paged_abi_checks.py'), lib], env=env,
+                       capture_output=True, text=True, timeout=300)
+    out = r.stdout + r.stderr
+    assert r.returncode == 0 and 'paged abi checks ok' in r.stdout, out[-4000:]
+    assert 'AddressSanitizer' not in out and 'runtime error' not in out, out[-4000:]
+
+
+def test_binding_refuses_host_tensors_types_and_shapes():
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)  # noqa: E731
+    pool, q = z(64, 576, dt=torch.bfloat16), z(2, 4, 576, dt=torch.bfloat16)
+    table, row0, n = z(1, 4), z(2), z(1)
+    out = z(2, 4, 512, dt=torch.bfloat16)
+    with pytest.raises(ValueError):                       # host tensors
+        ech.ech_paged_attn(q, pool, table, 16, row0, n, 2, 64, 0.1, out)
+    with pytest.raises(TypeError):
+        ech.ech_paged_attn(q, pool.float(), table, 16, row0, n, 2, 64, 0.1, out)
+    with pytest.raises(ValueError):
+        ech.ech_paged_append(pool, table, 16, row0, n, z(2, 576, dt=torch.bfloat16))
+    with pytest.raises(ValueError):
+        ech.ech_paged_weight(q, z(2, 4, dt=torch.float32), pool, table, 16, row0, n, 2, 64, 0.1, None,
+                             z(1, 64, dt=torch.float32))
+    with pytest.raises(ValueError):
+        ech.ech_paged_evict(z(1, 64, dt=torch.float32), n, 64, 8, 0, 0, z(1, 8), z(1))
+    with pytest.raises(TypeError):
+        ech.ech_paged_evict(z(1, 64, dt=torch.float32), z(1, dt=torch.int64), 64, 8, 0, 0, z(1, 8), z(1))
+
+
+def test_oracle_attention_closed_forms():
+    """One visible token: its value row; equal scores: the mean; the window and
+    the first tokens by hand."""
+    r = np.random.default_rng(1)
+    pool = wk.to_bf16_bits(r.standard_normal((40, 576)).astype(np.float32))
+    table = np.array([[3, 1, 0, 4]])
+    v = bf16_to_f64(pool)[:, :512]
+    sl = oracle.paged.slots(table[0], 8, 40, 20)
+    np.testing.assert_array_equal(sl[:10], [24, 25, 26, 27, 28, 29, 30, 31, 8, 9])
+    q = np.zeros((3, 2, 576), np.uint16)
+    out, lse, _, _ = oracle.paged.attention(q, pool, table, 8, [0, 3], [20], 1.0)
+    np.testing.assert_allclose(out[2, 1], v[sl].mean(0))
+    np.testing.assert_allclose(lse[:, 0], np.log([18, 19, 20]))
+    out, lse, _, _ = oracle.paged.attention(q, pool, table, 8, [0, 3], [20], 1.0, window=2, n_sink=1)
+    np.testing.assert_allclose(out[1, 0], v[sl[[0, 17, 18]]].mean(0))
+    out, lse, _, _ = oracle.paged.attention(q, pool, table, 8, [0, 3], [20], 1.0, window=1)
+    np.testing.assert_allclose(out[:, 0], v[sl[17:20]])
+    out, lse, _, _ = oracle.paged.attention(q, pool, np.full((1, 4), -1), 8, [0, 3], [20], 1.0)
+    assert np.all(out == 0) and np.all(np.isneginf(lse))
+
+
+def test_oracle_received_weight_hands_out_one():
+    r = np.random.default_rng(2)
+    pool = wk.to_bf16_bits(r.standard_normal((64, 576)).astype(np.float32))
+    q = wk.to_bf16_bits(r.standard_normal((5, 3, 576)).astype(np.float32))
+    table, row0, n = np.arange(8).reshape(2, 4), [0, 2, 5], [30, 17]
+    _, lse, _, _ = oracle.paged.attention(q, pool, table, 8, row0, n, 0.07, 6, 2)
+    acc = oracle.paged.received(q, lse, pool, table, 8, row0, n, 0.07, np.zeros((2, 32)), 1.0, 6, 2)
+    np.testing.assert_allclose(acc.sum(1), [2 * 3, 3 * 3])
+    assert acc[0, 2:23].sum() == 0 and np.all(acc[0, :2] > 0)
+
+
+def test_oracle_evict_by_brute_force():
+    r = np.random.default_rng(3)
+    for _ in range(200):
+        n, keep = int(r.integers(0, 12)), int(r.integers(1, 9))
+        sink = int(r.integers(0, keep + 1))
+        recent = int(r.integers(0, keep - sink + 1))
+        acc = r.integers(0, 3, (1, 12)).astype(np.float32)
+        got = oracle.paged.evict(acc, [n], keep, sink, recent)[0]
+        assert len(got) == min(n, keep) and np.all(np.diff(got) > 0)
+        if n > keep:
+            assert set(range(sink)) <= set(got) and set(range(n - recent, n)) <= set(got)
+            mid = [t for t in range(sink, n - recent)]
+            inn = [t for t in mid if t in got]
+            for t in set(mid) - set(got):
+                assert all((acc[0, u], -u) > (acc[0, t], -t) for u in inn)
