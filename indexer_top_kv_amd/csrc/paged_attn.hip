@@ -21,6 +21,7 @@
 // of each weight at most; the output is rounded to bf16 as well), while the
 // sum that divides them is fp32 over the unrounded weights.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "paged.hpp"
@@ -37,12 +38,13 @@ typedef short v8s_t __attribute__((ext_vector_type(8)));
 constexpr int kMT = 128;                     // queries per workgroup
 constexpr int kStepTok = 32;                 // tokens per step
 constexpr int kKs16 = kPagedRow / 16;        // contraction steps of the scores (36)
-constexpr int kPitchC = 73;                  // 16-byte pieces per token row in LDS (one spare: bank spread)
-constexpr int kPitch = kPitchC * 16;
-constexpr int kPos = kStepTok * kPitchC;     // piece positions of a step
-constexpr int kTileB = ((kPos + 63) / 64) * 1024;   // bytes of a step's buffer (whole load instructions)
-constexpr int kInstr = (kPos + 63) / 64;
+constexpr int kVPitch = kPagedVal * 2 + 32;  // bytes per token of the value part in LDS (two spare pieces: banks)
+constexpr int kTailAt = kStepTok * kVPitch;  // the rows' last 64 values (rotary part), 128 bytes a token
+constexpr int kTileB = kTailAt + kStepTok * 128;
+constexpr int kBufs = 3;
 constexpr int kPPitch = 80;                  // bytes per query of P in LDS (64 + 16: bank spread)
+constexpr int kKD = 4;                       // key fragments in flight
+constexpr int kQReg = 32;                    // query fragments in registers; the others wait in LDS
 
 #define ECH_LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -95,17 +97,29 @@ __device__ __forceinline__ Ranges ranges_of(int p_lo, int p_hi, int window, int 
 // grid (tiles x spans): workgroup = (tile of 128 queries of one sequence, span
 // of its steps). With one span it writes out and lse; with several the span's
 // maximum, sum and unnormalised output go to the workspace.
+//
+// One wave per SIMD, so a step's phases overlap inside the wave: while the
+// matrix cores form the scores of step i + 1, the vector unit turns those of
+// step i into weights (the scheduler is told to put a few of its instructions
+// behind each product); then a barrier, the value product of step i, and a
+// barrier. Three step buffers: i (values), i + 1 (keys), i + 2 (loading, with
+// a whole step's time to arrive). Rows arrive by direct-to-LDS loads: one
+// instruction brings the 1024 bytes of a token's value part (the slot is
+// scalar), one the last 128 bytes of eight tokens, in an order that spreads
+// them over the banks. They are issued from inline asm, so that the compiler
+// does not wait for them before every LDS read; they write no register, and a
+// wave waits for all of its loads before the barrier that opens their step.
 __global__ void __launch_bounds__(256, 1)
-    paged_attn_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint4* __restrict__ pool, Pages pg,
+    paged_attn_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool, Pages pg,
                       const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B, int T, int H,
                       int max_rows, int max_len, int window, int n_sink, float scale2, int nsp,
                       uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
                       float2* __restrict__ part_ml) {
-  __shared__ __align__(16) uint8_t tiles[2][kTileB];
+  __shared__ __align__(16) uint8_t tiles[kBufs * kTileB];
   __shared__ __align__(16) uint8_t ps[kMT * kPPitch];
+  __shared__ __align__(16) uint8_t qls[(kKs16 - kQReg) * 4096];   // [fragment][wave][lane] 16 bytes
   __shared__ float s_alpha[kMT], s_m[kMT], s_l[kMT];
-  __shared__ int s_grow[4], s_poison[4];
-  __shared__ int slots[3][kStepTok];
+  __shared__ int s_flag[4];   // per row tile: 1 = its maximum grew, 2 = a score that does not count is not finite
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
@@ -116,27 +130,19 @@ __global__ void __launch_bounds__(256, 1)
   mt = __builtin_amdgcn_readfirstlane(mt);
   const int sp = blockIdx.x % nsp;
   const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
-  const int M = sr.n * H;                                  // fits: T H < 2^31 (checked on the host)
+  const int M = sr.n * H;                                  // fits: T H < 2^30 (checked on the host)
   const int m0 = mt * kMT;
   const int r_lo = m0 / H, r_hi = (min(m0 + kMT, M) - 1) / H;
-  const Ranges rg = ranges_of(sr.pos0 + r_lo, sr.pos0 + r_hi, window, n_sink);
+  const int p_lo = sr.pos0 + r_lo, p_hi = sr.pos0 + r_hi;
+  const Ranges rg = ranges_of(p_lo, p_hi, window, n_sink);
   const int per = (rg.steps + nsp - 1) / nsp;
   const int step0 = min(sp * per, rg.steps), nsteps = min(step0 + per, rg.steps) - step0;
 
   // this lane's query of row tile `wave`
   const int m = m0 + wave * 32 + col;
   const bool live = m < M;
-  const int mr = live ? m / H : 0, mh = live ? m - mr * H : 0;
-  const int p_row = live ? sr.pos0 + mr : -1;
-  bf16x8_t qf[kKs16];
-  {
-    const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + g * 16;
-#pragma unroll
-    for (int s = 0; s < kKs16; ++s) {
-      qf[s] = __builtin_bit_cast(bf16x8_t, u32x4_t{0, 0, 0, 0});
-      if (live) qf[s] = ld_bf16x8(qp + s * 32);
-    }
-  }
+  const int mr = min(m, M - 1) / H, mh = min(m, M - 1) - mr * H;   // past the end: the last one again, never written
+  const int p_row = sr.pos0 + mr;
   const int32_t* trow = pg.table + (int64_t)b * pg.ld;
 
   // tokens of step i: [t0, t0 + count)
@@ -146,32 +152,51 @@ __global__ void __launch_bounds__(256, 1)
     *count = min(kStepTok, (st < rg.s0 ? rg.n0 : rg.w1) - t0);
     return t0;
   };
+  // slot of the step's token `col` in lanes 0..31 (-1: none), and the bits of those that have one
   auto fetch_slot = [&](int i) -> int {
     int cnt;
     const int t0 = step_tok(i, &cnt);
     return lane < cnt ? slot_of(pg, trow, t0 + lane) : -1;
   };
-  // Rows of a step whose slots are in slots[si]: direct loads into LDS, one
-  // 1 KiB instruction per 64 piece positions; a token without a slot brings
-  // slot 0's row, which no query weighs.
-  auto issue = [&](int si, int buf) {
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(&tiles[0][0]))) +
-                          static_cast<uint32_t>(buf * kTileB);
+  // This wave's eight tokens of a step: 8 wave .. +7. A token without a slot
+  // brings slot 0's row, which no query weighs.
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(&tiles[0])));
+  auto issue = [&](int slot, int buf) {
+    const uint32_t base = lds0 + static_cast<uint32_t>(buf * kTileB);
+    const uint32_t voff = lane * 16;
 #pragma unroll
-    for (int j = 0; j < (kInstr + 3) / 4; ++j) {
-      const int ins = j * 4 + wave;
-      const int p = ins * 64 + ln;
-      const int t = p / kPitchC, c = p - t * kPitchC;
-      if (ins < kInstr && p < kPos && c < kPagedChunks) {
-        const uint4* src = pool + (int64_t)max(slots[si][t], 0) * kPagedChunks + c;
-        const uint32_t lds = lds0 + static_cast<uint32_t>(ins * 1024);
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int tok = wave * 8 + j;
+      const int sl = max(__builtin_amdgcn_readlane(slot, tok), 0);
+      const uint8_t* src = pool + (int64_t)sl * (kPagedRow * 2);
+      const uint32_t lds = base + static_cast<uint32_t>(tok * kVPitch);
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src) : "memory", "m0");
+    }
+    {
+      const int k = lane >> 3, tok = wave * 8 + k;
+      const int sl = max(__shfl(slot, tok, 64), 0);
+      const uint8_t* src = pool + (int64_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16);
+      const uint32_t lds = base + static_cast<uint32_t>(kTailAt + wave * 1024);
+      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
     }
   };
+  // key fragment s of the token `col` of a buffer
+  auto kload = [&](const uint8_t* buf, int s) -> bf16x8_t {
+    return s < 32 ? ld_bf16x8(buf + col * kVPitch + g * 16 + s * 32)
+                  : ld_bf16x8(buf + kTailAt + col * 128 + (((2 * (s - 32) + g) ^ (col & 7)) * 16));
+  };
 
+  bf16x8_t qr[kQReg];
+  uint8_t* const qmine = qls + wave * 1024 + lane * 16;
+  {
+    const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + g * 16;
+#pragma unroll
+    for (int s = 0; s < kQReg; ++s) qr[s] = ld_bf16x8(qp + s * 32);
+#pragma unroll
+    for (int s = kQReg; s < kKs16; ++s)
+      *reinterpret_cast<u32x4_t*>(qmine + (s - kQReg) * 4096) = *reinterpret_cast<const u32x4_t*>(qp + s * 32);
+  }
+  auto qf = [&](int s) -> bf16x8_t { return s < kQReg ? qr[s] : ld_bf16x8(qmine + (s - kQReg) * 4096); };
   f32x16_t acc[4][4];   // [column tile][row tile]
 #pragma unroll
   for (int c = 0; c < 4; ++c)
@@ -181,111 +206,177 @@ __global__ void __launch_bounds__(256, 1)
       for (int v = 0; v < 16; ++v) acc[c][r][v] = 0.f;
   float mx = -__builtin_inff(), l = 0.f;   // running maximum of the query, this lane's part of its sum
 
+  // Weights of step i from its scores st (lane: query col, tokens t0 + 8 (v / 4)
+  // + 4 g + v % 4), with the scores of the next step formed meanwhile.
+  auto weigh = [&](auto has_next, auto whole, f32x16_t& st, f32x16_t& nx, const uint8_t* kbuf, uint32_t bits) {
+    constexpr bool NEXT = decltype(has_next)::value, FULL = decltype(whole)::value;
+    bf16x8_t kb[kKD];
+    if constexpr (NEXT) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) nx[v] = 0.f;
+#pragma unroll
+      for (int s = 0; s < kKD; ++s) kb[s] = kload(kbuf, s);
+#pragma unroll
+      for (int s = 0; s < kKs16; ++s) {
+        nx = mfma32(kb[s % kKD], qf(s), nx);
+        if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
+      }
+    }
+    float tmax = -__builtin_inff();
+    bool poison = false;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      float x = st[v] * scale2;
+      if constexpr (!FULL) {
+        const bool ok = (bits >> (8 * (v >> 2) + (v & 3))) & 1;
+        poison |= !ok && !(fabsf(x) < __builtin_inff());
+        x = ok ? x : -__builtin_inff();
+      }
+      st[v] = x;
+      tmax = fmaxf(tmax, x);
+    }
+    tmax = pair_max(tmax);
+    // the maximum moves only when a step's exceeds it by more than 8: a
+    // weight may reach 2^8, and bf16 and fp32 keep their relative precision
+    const bool grow = __any(tmax > mx + 8.f);
+    const float mn = grow ? fmaxf(mx, tmax) : mx;
+    const float ref = mn == -__builtin_inff() ? 0.f : mn;
+    const float alpha = grow ? __builtin_amdgcn_exp2f(mx - ref) : 1.f;   // 0 while nothing was seen
+    float psum = 0.f;
+    bf16x8_t pb[2];
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const float p = __builtin_amdgcn_exp2f(st[v] - ref);
+      psum += p;
+      pb[v >> 3][v & 7] = (__bf16)p;
+    }
+    l = l * alpha + psum;
+    mx = mn;
+    uint8_t* pw = ps + (wave * 32 + col) * kPPitch + g * 16;
+    *reinterpret_cast<u32x4_t*>(pw) = __builtin_bit_cast(u32x4_t, pb[0]);
+    *reinterpret_cast<u32x4_t*>(pw + 32) = __builtin_bit_cast(u32x4_t, pb[1]);
+    s_alpha[wave * 32 + col] = alpha;
+    int flag = grow ? 1 : 0;
+    if constexpr (!FULL) flag |= __any(poison) ? 2 : 0;
+    s_flag[wave] = flag;
+    if constexpr (NEXT) {
+      __builtin_amdgcn_sched_group_barrier(0x100, kKD, 0);   // LDS reads
+#pragma unroll
+      for (int s = 0; s < kKs16 - kKD; ++s) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // product
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);   // vector instructions
+      }
+    }
+  };
+
   if (nsteps > 0) {
-    if (wave == 0 && lane < kStepTok) slots[0][lane] = fetch_slot(0);
+    int s_nxt;                       // slots of the step to load next
+    uint32_t ok0, ok1 = 0, ok2 = 0;  // tokens with a slot of steps i, i + 1, i + 2
+    {
+      const int s0 = fetch_slot(0), s1 = nsteps > 1 ? fetch_slot(1) : -1;
+      s_nxt = nsteps > 2 ? fetch_slot(2) : -1;
+      ok0 = (uint32_t)__ballot(s0 >= 0);
+      ok1 = (uint32_t)__ballot(s1 >= 0);
+      issue(s0, 0);
+      if (nsteps > 1) issue(s1, 1);
+    }
+    __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
     __syncthreads();
-    issue(0, 0);
-    int nxt = wave == 0 && nsteps > 1 ? fetch_slot(1) : -1;
+    f32x16_t st, nx;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) st[v] = 0.f;
+#pragma unroll
+    for (int s = 0; s < kKs16; ++s) st = mfma32(kload(tiles, s), qf(s), st);
+
+    int cur = 0, nxt = 1, far = 2;   // buffers of steps i, i + 1, i + 2
     for (int i = 0; i < nsteps; ++i) {
-      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads of step i have landed
-      if (wave == 0 && lane < kStepTok && i + 1 < nsteps) slots[(i + 1) % 3][lane] = nxt;
-      __syncthreads();
-      if (i + 1 < nsteps) issue((i + 1) % 3, (i + 1) & 1);
-      if (wave == 0 && i + 2 < nsteps) nxt = fetch_slot(i + 2);
-      const uint8_t* cur = &tiles[i & 1][0];
+      if (i + 2 < nsteps) {
+        ok2 = (uint32_t)__ballot(s_nxt >= 0);
+        issue(s_nxt, far);
+        if (i + 3 < nsteps) s_nxt = fetch_slot(i + 3);
+      }
       int cnt;
       const int t0 = step_tok(i, &cnt);
-
-      // scores of 32 tokens x this wave's 32 queries
-      f32x16_t st;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) st[v] = 0.f;
-      const uint8_t* kr = cur + col * kPitch + g * 16;
-#pragma unroll
-      for (int s = 0; s < kKs16; ++s) st = mfma32(ld_bf16x8(kr + s * 32), qf[s], st);
-
-      // lane: query col, tokens t0 + 8 (v / 4) + 4 g + v % 4
-      float sv[16];
-      float tmax = -__builtin_inff();
-      bool poison = false;   // a score that does not count is not finite: its row holds infinities or NaN
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int tt = 8 * (v >> 2) + 4 * g + (v & 3);
-        const bool ok = slots[i % 3][tt] >= 0 && sees(p_row, t0 + tt, window, n_sink);
-        const float x = st[v] * scale2;
-        poison |= !ok && !(fabsf(x) < __builtin_inff());
-        sv[v] = ok ? x : -__builtin_inff();
-        tmax = fmaxf(tmax, sv[v]);
-      }
-      tmax = pair_max(tmax);
-      // the maximum moves only when a step's exceeds it by more than 8: a
-      // weight may reach 2^8, and bf16 and fp32 keep their relative precision
-      const bool grow = __any(tmax > mx + 8.f);
-      const float mn = grow ? fmaxf(mx, tmax) : mx;
-      const float ref = mn == -__builtin_inff() ? 0.f : mn;
-      const float alpha = exp2f(mx - ref);                  // 0 while nothing was seen
-      float psum = 0.f;
-      bf16x8_t pb[2];
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const float p = exp2f(sv[v] - ref);
-        psum += p;
-        pb[v >> 3][v & 7] = (__bf16)p;
-      }
-      l = l * (grow ? alpha : 1.f) + psum;
-      mx = mn;
-      uint8_t* pw = ps + (wave * 32 + col) * kPPitch + g * 16;
-      *reinterpret_cast<u32x4_t*>(pw) = __builtin_bit_cast(u32x4_t, pb[0]);
-      *reinterpret_cast<u32x4_t*>(pw + 32) = __builtin_bit_cast(u32x4_t, pb[1]);
-      if (g == 0) s_alpha[wave * 32 + col] = alpha;
-      const bool any_poison = __any(poison);
-      if (lane == 0) {
-        s_grow[wave] = grow;
-        s_poison[wave] = any_poison;
+      const bool full = ok0 == 0xffffffffu && t0 + kStepTok - 1 <= p_lo &&
+                        (window == 0 || t0 > p_hi - window || t0 + kStepTok <= n_sink);
+      const uint8_t* vbuf = tiles + cur * kTileB;
+      const uint8_t* kbuf = tiles + nxt * kTileB;
+      if (full) {
+        if (i + 1 < nsteps) weigh(std::true_type{}, std::true_type{}, st, nx, kbuf, 0);
+        else weigh(std::false_type{}, std::true_type{}, st, nx, kbuf, 0);
+      } else {
+        // the tokens this lane's query sees: bit t
+        const int d = p_row - t0;    // last visible, relative
+        uint32_t bits = d < 0 ? 0u : (d >= 31 ? 0xffffffffu : (2u << d) - 1u);
+        if (window != 0) {
+          const int lo = d - window + 1, sk = n_sink - t0;
+          const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
+          const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
+          bits &= win | first;
+        }
+        bits = (bits & ok0) >> (4 * g);
+        if (i + 1 < nsteps) weigh(std::true_type{}, std::false_type{}, st, nx, kbuf, bits);
+        else weigh(std::false_type{}, std::false_type{}, st, nx, kbuf, bits);
       }
       __syncthreads();
 
+      int flags[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (s_grow[r]) {
-          const float a = s_alpha[r * 32 + col];
+      for (int r = 0; r < 4; ++r) flags[r] = __builtin_amdgcn_readfirstlane(s_flag[r]);
+      if (flags[0] | flags[1] | flags[2] | flags[3]) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            asm volatile("" : "+a"(acc[c][r]));
+        for (int r = 0; r < 4; ++r) {
+          if (flags[r] & 1) {
+            const float a = s_alpha[r * 32 + col];
 #pragma unroll
-            for (int v = 0; v < 16; ++v) acc[c][r][v] *= a;
-            asm volatile("" : "+a"(acc[c][r]));
+            for (int c = 0; c < 4; ++c) {
+              asm volatile("" : "+a"(acc[c][r]));   // one accumulator at a time leaves its registers
+#pragma unroll
+              for (int v = 0; v < 16; ++v) acc[c][r][v] *= a;
+              asm volatile("" : "+a"(acc[c][r]));
+            }
           }
         }
-      }
-      if (s_poison[0] | s_poison[1] | s_poison[2] | s_poison[3]) {
-        // A weight of zero must add nothing, but 0 x inf is NaN: values that
-        // are not finite become 0 in this wave's columns of the step. A query
-        // that sees such a row has a score, so a weight, that is NaN already.
-        for (int x = lane; x < kStepTok * 16; x += 64) {
-          uint16_t* e = reinterpret_cast<uint16_t*>(&tiles[i & 1][0] + (x >> 4) * kPitch + wave * 256 + (x & 15) * 16);
+        if ((flags[0] | flags[1] | flags[2] | flags[3]) & 2) {
+          // A weight of zero must add nothing, but 0 x inf is NaN: values that
+          // are not finite become 0 in this wave's columns of the step. A query
+          // that sees such a row has a score, so a weight, that is NaN already.
+          for (int x = lane; x < kStepTok * 16; x += 64) {
+            uint16_t* e = reinterpret_cast<uint16_t*>(tiles + cur * kTileB + (x >> 4) * kVPitch + wave * 256 + (x & 15) * 16);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+            for (int j = 0; j < 8; ++j)
+              if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
       // O^T += V^T P^T, contraction order of a lane's 16 scores: tokens
       // {16 c + 4 g .. +3, 16 c + 8 + 4 g .. +3} for half c
-      bf16x8_t pf[2][4];
+      const uint8_t* vb = vbuf + (4 * g + ((lane & 15) >> 2)) * kVPitch + wave * 256 + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c) {
+        bf16x8_t pf[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) pf[c][r] = ld_bf16x8(ps + (r * 32 + col) * kPPitch + c * 32 + g * 16);
-      const uint8_t* vb = cur + (4 * g + ((lane & 15) >> 2)) * kPitch + wave * 256 + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
+        for (int r = 0; r < 4; ++r) pf[r] = ld_bf16x8(ps + (r * 32 + col) * kPPitch + c * 32 + g * 16);
 #pragma unroll
-      for (int ct = 0; ct < 4; ++ct)
+        for (int ct = 0; ct < 4; ++ct) {
+          const bf16x8_t vf = ld_tr8(vb + 16 * c * kVPitch + ct * 64, vb + (16 * c + 8) * kVPitch + ct * 64);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const bf16x8_t vf = ld_tr8(vb + 16 * c * kPitch + ct * 64, vb + (16 * c + 8) * kPitch + ct * 64);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[ct][r] = mfma32(vf, pf[c][r], acc[ct][r]);
+          for (int r = 0; r < 4; ++r) acc[ct][r] = mfma32(vf, pf[r], acc[ct][r]);
         }
+      }
+      st = nx;
+      ok0 = ok1;
+      ok1 = ok2;
+      const int t = cur;
+      cur = nxt;
+      nxt = far;
+      far = t;
+      if (i + 1 < nsteps) {
+        __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads of step i + 2 have landed
+        __syncthreads();
+      }
     }
   }
 
@@ -416,6 +507,8 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   const size_t need = ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink);
   if (ws_bytes < need || (need && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)))) return ECH_EINVAL;
   if (T == 0 || max_rows == 0) return ECH_OK;
+  if (window >= max_len) window = 0;                       // no position has more tokens behind it
+  n_sink = std::min(n_sink, max_len);
   const int nsp = spans_of(B, T, H, max_rows, max_len, window, n_sink);
   const int64_t tiles = tiles_of(B, T, H, max_rows);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -423,7 +516,7 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)nsp * T * H * kPagedVal);
   const Pages pg{page_table, pt_ld, n_slots, page_size};
   hipLaunchKernelGGL(paged_attn_kernel, dim3((unsigned)(tiles * nsp)), dim3(256), 0, s, static_cast<const uint16_t*>(q),
-                     q_row_stride, q_head_stride, static_cast<const uint4*>(pool), pg, row0, seq_len, B, T, H, max_rows,
+                     q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg, row0, seq_len, B, T, H, max_rows,
                      max_len, window, n_sink, sm_scale * 1.4426950408889634f, nsp, static_cast<uint16_t*>(out), lse,
                      part_o, part_ml);
   ECH_LAUNCH_CHECK();
