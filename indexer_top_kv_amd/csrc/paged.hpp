@@ -21,18 +21,37 @@ constexpr int kPagedChunks = kPagedRow * 2 / 16;   // 16-byte pieces of a row (7
 struct Pages {
   const int32_t* table;   // [B, ld]
   int64_t ld;             // page-table entries per sequence
-  int64_t n_slots;        // rows in the pool
+  uint32_t n_slots;       // rows in the pool
+  uint32_t n_pages;       // pages that begin in the pool
   int size;               // tokens per page
+  uint32_t mul;           // t / size = (mulhi(t, mul) + t) >> shift for t < 2^31
+  int shift;
 };
+
+inline Pages make_pages(const int32_t* table, int64_t ld, int64_t n_slots, int size) {
+  int l = 0;
+  while ((1u << l) < (uint32_t)size) ++l;                  // ceil(log2 size), size <= 2^20
+  const uint64_t mul = (((1ull << l) - (uint64_t)size) << 32) / (uint64_t)size + 1;
+  return Pages{table, ld, (uint32_t)n_slots, (uint32_t)((n_slots + size - 1) / size), size, (uint32_t)mul, l};
+}
+
+__device__ __forceinline__ uint32_t page_index(const Pages& pg, int t) {
+  return (__umulhi((uint32_t)t, pg.mul) + (uint32_t)t) >> pg.shift;
+}
+
+// Slot of the token `off` tokens into page `page`, or -1 where that is none of
+// the pool's.
+__device__ __forceinline__ int slot_in(const Pages& pg, int page, int off) {
+  const uint32_t s = (uint32_t)page * (uint32_t)pg.size + (uint32_t)off;   // < 2^31 + 2^20 for a page of the pool
+  return (uint32_t)page < pg.n_pages && s < pg.n_slots ? (int)s : -1;
+}
 
 // Slot of token t of the sequence whose page-table row is `row`, or -1 where
 // the table has no valid page for it.
 __device__ __forceinline__ int slot_of(const Pages& pg, const int32_t* row, int t) {
-  const uint32_t idx = (uint32_t)t / (uint32_t)pg.size;
+  const uint32_t idx = page_index(pg, t);
   if ((int64_t)idx >= pg.ld) return -1;
-  const int page = row[idx];
-  const int64_t s = (int64_t)page * pg.size + (t - (int)idx * pg.size);
-  return page >= 0 && s < pg.n_slots ? (int)s : -1;
+  return slot_in(pg, row[idx], t - (int)idx * pg.size);
 }
 
 // The new rows of one sequence, clamped: rows [first, first + n), row i at

@@ -44,7 +44,6 @@ constexpr int kTileB = kTailAt + kStepTok * 128;
 constexpr int kBufs = 3;
 constexpr int kPPitch = 80;                  // bytes per query of P in LDS (64 + 16: bank spread)
 constexpr int kKD = 4;                       // key fragments in flight
-constexpr int kQReg = 32;                    // query fragments in registers; the others wait in LDS
 
 #define ECH_LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -55,6 +54,18 @@ __device__ __forceinline__ bf16x8_t ld_bf16x8(const uint8_t* p) {
 __device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+
+// The same with the sums in vector registers, which the weights are computed
+// from (the builtin's go to accumulation registers, all of which the output
+// takes). The compiler does not see that these are matrix instructions, so
+// mfma32_v_done stands between the last of them and any other use.
+__device__ __forceinline__ void mfma32_v_first(f32x16_t& d, bf16x8_t a, bf16x8_t b) {
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma32_v(f32x16_t& d, bf16x8_t a, bf16x8_t b) {
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void mfma32_v_done(f32x16_t& d) { asm volatile("s_nop 15" : "+v"(d)); }
 
 // 8 tokens x this lane's column, from two transposed reads of 4 tokens.
 __device__ __forceinline__ bf16x8_t ld_tr8(const uint8_t* p0, const uint8_t* p1) {
@@ -117,7 +128,6 @@ __global__ void __launch_bounds__(256, 1)
                       float2* __restrict__ part_ml) {
   __shared__ __align__(16) uint8_t tiles[kBufs * kTileB];
   __shared__ __align__(16) uint8_t ps[kMT * kPPitch];
-  __shared__ __align__(16) uint8_t qls[(kKs16 - kQReg) * 4096];   // [fragment][wave][lane] 16 bytes
   __shared__ float s_alpha[kMT], s_m[kMT], s_l[kMT];
   __shared__ int s_flag[4];   // per row tile: 1 = its maximum grew, 2 = a score that does not count is not finite
 
@@ -152,11 +162,19 @@ __global__ void __launch_bounds__(256, 1)
     *count = min(kStepTok, (st < rg.s0 ? rg.n0 : rg.w1) - t0);
     return t0;
   };
-  // slot of the step's token `col` in lanes 0..31 (-1: none), and the bits of those that have one
-  auto fetch_slot = [&](int i) -> int {
+  // The page of the step's token `lane` (lanes past the count: its last one),
+  // and the slot it makes once the load is in.
+  auto fetch_page = [&](int i, int& off) -> int {
     int cnt;
-    const int t0 = step_tok(i, &cnt);
-    return lane < cnt ? slot_of(pg, trow, t0 + lane) : -1;
+    const int t = step_tok(i, &cnt) + min(lane, cnt - 1);
+    const uint32_t idx = page_index(pg, t);
+    off = t - (int)idx * pg.size;
+    return trow[idx];
+  };
+  auto slot_at = [&](int i, int page, int off) -> int {
+    int cnt;
+    step_tok(i, &cnt);
+    return lane < cnt ? slot_in(pg, page, off) : -1;
   };
   // This wave's eight tokens of a step: 8 wave .. +7. A token without a slot
   // brings slot 0's row, which no query weighs.
@@ -186,17 +204,12 @@ __global__ void __launch_bounds__(256, 1)
                   : ld_bf16x8(buf + kTailAt + col * 128 + (((2 * (s - 32) + g) ^ (col & 7)) * 16));
   };
 
-  bf16x8_t qr[kQReg];
-  uint8_t* const qmine = qls + wave * 1024 + lane * 16;
+  bf16x8_t qf[kKs16];
   {
     const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + g * 16;
 #pragma unroll
-    for (int s = 0; s < kQReg; ++s) qr[s] = ld_bf16x8(qp + s * 32);
-#pragma unroll
-    for (int s = kQReg; s < kKs16; ++s)
-      *reinterpret_cast<u32x4_t*>(qmine + (s - kQReg) * 4096) = *reinterpret_cast<const u32x4_t*>(qp + s * 32);
+    for (int s = 0; s < kKs16; ++s) qf[s] = ld_bf16x8(qp + s * 32);
   }
-  auto qf = [&](int s) -> bf16x8_t { return s < kQReg ? qr[s] : ld_bf16x8(qmine + (s - kQReg) * 4096); };
   f32x16_t acc[4][4];   // [column tile][row tile]
 #pragma unroll
   for (int c = 0; c < 4; ++c)
@@ -206,76 +219,87 @@ __global__ void __launch_bounds__(256, 1)
       for (int v = 0; v < 16; ++v) acc[c][r][v] = 0.f;
   float mx = -__builtin_inff(), l = 0.f;   // running maximum of the query, this lane's part of its sum
 
-  // Weights of step i from its scores st (lane: query col, tokens t0 + 8 (v / 4)
-  // + 4 g + v % 4), with the scores of the next step formed meanwhile.
+  const uint8_t* const vlane = tiles + (4 * g + ((lane & 15) >> 2)) * kVPitch + wave * 256 + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
+  // value fragment (V^T) of token half c, column tile ct: the contraction order
+  // of a lane's 16 scores, tokens {16 c + 4 g .. +3, 16 c + 8 + 4 g .. +3}
+  auto vload = [&](int buf, int c, int ct) -> bf16x8_t {
+    const uint8_t* v = vlane + buf * kTileB + 16 * c * kVPitch + ct * 64;
+    return ld_tr8(v, v + 8 * kVPitch);
+  };
+  uint8_t* const pmine = ps + (wave * 32 + col) * kPPitch + g * 16;
+  const uint8_t* const pall = ps + col * kPPitch + g * 16;
+
+  // One step: the weights of step i from its scores st (lane: query col, tokens
+  // t0 + 8 (v / 4) + 4 g + v % 4), a few instructions behind each product of
+  // the next step's scores nx. The order is the one written: a group per
+  // product, closed by a scheduling barrier, key fragments kKD products ahead.
   auto weigh = [&](auto has_next, auto whole, f32x16_t& st, f32x16_t& nx, const uint8_t* kbuf, uint32_t bits) {
     constexpr bool NEXT = decltype(has_next)::value, FULL = decltype(whole)::value;
     bf16x8_t kb[kKD];
     if constexpr (NEXT) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) nx[v] = 0.f;
-#pragma unroll
       for (int s = 0; s < kKD; ++s) kb[s] = kload(kbuf, s);
-#pragma unroll
-      for (int s = 0; s < kKs16; ++s) {
-        nx = mfma32(kb[s % kKD], qf(s), nx);
-        if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
-      }
     }
-    float tmax = -__builtin_inff();
-    bool poison = false;
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      float x = st[v] * scale2;
-      if constexpr (!FULL) {
-        const bool ok = (bits >> (8 * (v >> 2) + (v & 3))) & 1;
-        poison |= !ok && !(fabsf(x) < __builtin_inff());
-        x = ok ? x : -__builtin_inff();
-      }
-      st[v] = x;
-      tmax = fmaxf(tmax, x);
-    }
-    tmax = pair_max(tmax);
-    // the maximum moves only when a step's exceeds it by more than 8: a
-    // weight may reach 2^8, and bf16 and fp32 keep their relative precision
-    const bool grow = __any(tmax > mx + 8.f);
-    const float mn = grow ? fmaxf(mx, tmax) : mx;
-    const float ref = mn == -__builtin_inff() ? 0.f : mn;
-    const float alpha = grow ? __builtin_amdgcn_exp2f(mx - ref) : 1.f;   // 0 while nothing was seen
-    float psum = 0.f;
+    float tmax = -__builtin_inff(), ref = 0.f, alpha = 1.f, psum = 0.f;
+    bool poison = false, grow = false;
     bf16x8_t pb[2];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const float p = __builtin_amdgcn_exp2f(st[v] - ref);
-      psum += p;
-      pb[v >> 3][v & 7] = (__bf16)p;
-    }
-    l = l * alpha + psum;
-    mx = mn;
-    uint8_t* pw = ps + (wave * 32 + col) * kPPitch + g * 16;
-    *reinterpret_cast<u32x4_t*>(pw) = __builtin_bit_cast(u32x4_t, pb[0]);
-    *reinterpret_cast<u32x4_t*>(pw + 32) = __builtin_bit_cast(u32x4_t, pb[1]);
-    s_alpha[wave * 32 + col] = alpha;
-    int flag = grow ? 1 : 0;
-    if constexpr (!FULL) flag |= __any(poison) ? 2 : 0;
-    s_flag[wave] = flag;
-    if constexpr (NEXT) {
-      __builtin_amdgcn_sched_group_barrier(0x100, kKD, 0);   // LDS reads
-#pragma unroll
-      for (int s = 0; s < kKs16 - kKD; ++s) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // product
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);   // vector instructions
+    for (int s = 0; s < kKs16; ++s) {
+      if constexpr (NEXT) {
+        if (s == 0) mfma32_v_first(nx, kb[0], qf[0]);
+        else mfma32_v(nx, kb[s % kKD], qf[s]);
+        if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
       }
+      if (s < 8) {
+#pragma unroll
+        for (int v = 2 * s; v < 2 * s + 2; ++v) {
+          float x = st[v] * scale2;
+          if constexpr (!FULL) {
+            const bool ok = (bits >> (8 * (v >> 2) + (v & 3))) & 1;
+            poison |= !ok && !(fabsf(x) < __builtin_inff());
+            x = ok ? x : -__builtin_inff();
+          }
+          st[v] = x;
+          tmax = fmaxf(tmax, x);
+        }
+      } else if (s == 8) {
+        tmax = pair_max(tmax);
+      } else if (s == 9) {
+        // the maximum moves only when a step's exceeds it by more than 8: a
+        // weight may reach 2^8, and bf16 and fp32 keep their relative precision
+        grow = __any(tmax > mx + 8.f);
+        const float mn = grow ? fmaxf(mx, tmax) : mx;
+        ref = mn == -__builtin_inff() ? 0.f : mn;
+        alpha = grow ? __builtin_amdgcn_exp2f(mx - ref) : 1.f;   // 0 while nothing was seen
+        mx = mn;
+      } else if (s < 26) {
+        const int v = s - 10;
+        const float p = __builtin_amdgcn_exp2f(st[v] - ref);
+        psum += p;
+        pb[v >> 3][v & 7] = (__bf16)p;
+        if (v == 7) *reinterpret_cast<u32x4_t*>(pmine) = __builtin_bit_cast(u32x4_t, pb[0]);
+        if (v == 15) *reinterpret_cast<u32x4_t*>(pmine + 32) = __builtin_bit_cast(u32x4_t, pb[1]);
+      } else if (s == 26) {
+        l = l * alpha + psum;
+        s_alpha[wave * 32 + col] = alpha;
+        int flag = grow ? 1 : 0;
+        if constexpr (!FULL) flag |= __any(poison) ? 2 : 0;
+        s_flag[wave] = flag;
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (NEXT) mfma32_v_done(nx);
   };
 
   if (nsteps > 0) {
-    int s_nxt;                       // slots of the step to load next
+    int page, off;                   // of the step to load next
     uint32_t ok0, ok1 = 0, ok2 = 0;  // tokens with a slot of steps i, i + 1, i + 2
     {
-      const int s0 = fetch_slot(0), s1 = nsteps > 1 ? fetch_slot(1) : -1;
-      s_nxt = nsteps > 2 ? fetch_slot(2) : -1;
+      int off0, off1;
+      const int i1 = min(1, nsteps - 1);
+      const int page0 = fetch_page(0, off0), page1 = fetch_page(i1, off1);
+      page = fetch_page(min(2, nsteps - 1), off);
+      const int s0 = slot_at(0, page0, off0), s1 = slot_at(i1, page1, off1);
       ok0 = (uint32_t)__ballot(s0 >= 0);
       ok1 = (uint32_t)__ballot(s1 >= 0);
       issue(s0, 0);
@@ -284,24 +308,34 @@ __global__ void __launch_bounds__(256, 1)
     __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
     __syncthreads();
     f32x16_t st, nx;
+    {
+      bf16x8_t kb[kKD];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) st[v] = 0.f;
+      for (int s = 0; s < kKD; ++s) kb[s] = kload(tiles, s);
 #pragma unroll
-    for (int s = 0; s < kKs16; ++s) st = mfma32(kload(tiles, s), qf(s), st);
+      for (int s = 0; s < kKs16; ++s) {
+        if (s == 0) mfma32_v_first(st, kb[0], qf[0]);
+        else mfma32_v(st, kb[s % kKD], qf[s]);
+        if (s + kKD < kKs16) kb[s % kKD] = kload(tiles, s + kKD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      mfma32_v_done(st);
+    }
 
     int cur = 0, nxt = 1, far = 2;   // buffers of steps i, i + 1, i + 2
     for (int i = 0; i < nsteps; ++i) {
       if (i + 2 < nsteps) {
-        ok2 = (uint32_t)__ballot(s_nxt >= 0);
-        issue(s_nxt, far);
-        if (i + 3 < nsteps) s_nxt = fetch_slot(i + 3);
+        const int slot = slot_at(i + 2, page, off);
+        ok2 = (uint32_t)__ballot(slot >= 0);
+        page = fetch_page(min(i + 3, nsteps - 1), off);   // read in the next round, after this round's wait
+        issue(slot, far);
       }
       int cnt;
       const int t0 = step_tok(i, &cnt);
       const bool full = ok0 == 0xffffffffu && t0 + kStepTok - 1 <= p_lo &&
                         (window == 0 || t0 > p_hi - window || t0 + kStepTok <= n_sink);
-      const uint8_t* vbuf = tiles + cur * kTileB;
       const uint8_t* kbuf = tiles + nxt * kTileB;
+      __builtin_amdgcn_sched_barrier(0);
       if (full) {
         if (i + 1 < nsteps) weigh(std::true_type{}, std::true_type{}, st, nx, kbuf, 0);
         else weigh(std::false_type{}, std::true_type{}, st, nx, kbuf, 0);
@@ -319,8 +353,14 @@ __global__ void __launch_bounds__(256, 1)
         if (i + 1 < nsteps) weigh(std::true_type{}, std::false_type{}, st, nx, kbuf, bits);
         else weigh(std::false_type{}, std::false_type{}, st, nx, kbuf, bits);
       }
+      bf16x8_t vf[2], pf[2][4];
+      vf[0] = vload(cur, 0, 0);
+      vf[1] = vload(cur, 0, 1);
+      __builtin_amdgcn_sched_barrier(0);
       __syncthreads();
 
+#pragma unroll
+      for (int r = 0; r < 4; ++r) pf[0][r] = ld_bf16x8(pall + r * 32 * kPPitch);
       int flags[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) flags[r] = __builtin_amdgcn_readfirstlane(s_flag[r]);
@@ -349,22 +389,23 @@ __global__ void __launch_bounds__(256, 1)
               if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
           }
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          vf[0] = vload(cur, 0, 0);
+          vf[1] = vload(cur, 0, 1);
         }
       }
-      // O^T += V^T P^T, contraction order of a lane's 16 scores: tokens
-      // {16 c + 4 g .. +3, 16 c + 8 + 4 g .. +3} for half c
-      const uint8_t* vb = vbuf + (4 * g + ((lane & 15) >> 2)) * kVPitch + wave * 256 + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
+      __builtin_amdgcn_sched_barrier(0);
+      // O^T += V^T P^T: a group per value fragment, two fragments ahead
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        bf16x8_t pf[4];
+      for (int x = 0; x < 8; ++x) {
+        const int c = x >> 2, ct = x & 3;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) pf[r] = ld_bf16x8(ps + (r * 32 + col) * kPPitch + c * 32 + g * 16);
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct) {
-          const bf16x8_t vf = ld_tr8(vb + 16 * c * kVPitch + ct * 64, vb + (16 * c + 8) * kVPitch + ct * 64);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[ct][r] = mfma32(vf, pf[r], acc[ct][r]);
+        for (int r = 0; r < 4; ++r) acc[ct][r] = mfma32(vf[x & 1], pf[c][r], acc[ct][r]);
+        if (x + 2 < 8) vf[x & 1] = vload(cur, (x + 2) >> 2, (x + 2) & 3);
+        if (x < 2) {
+          pf[1][2 * x] = ld_bf16x8(pall + 2 * x * 32 * kPPitch + 32);
+          pf[1][2 * x + 1] = ld_bf16x8(pall + (2 * x + 1) * 32 * kPPitch + 32);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       st = nx;
       ok0 = ok1;
@@ -514,7 +555,7 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   float* part_o = static_cast<float*>(ws);
   float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)nsp * T * H * kPagedVal);
-  const Pages pg{page_table, pt_ld, n_slots, page_size};
+  const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
   hipLaunchKernelGGL(paged_attn_kernel, dim3((unsigned)(tiles * nsp)), dim3(256), 0, s, static_cast<const uint16_t*>(q),
                      q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg, row0, seq_len, B, T, H, max_rows,
                      max_len, window, n_sink, sm_scale * 1.4426950408889634f, nsp, static_cast<uint16_t*>(out), lse,

@@ -167,7 +167,7 @@ extern "C" int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, 
       !aligned16_(pool) || !aligned16_(rows))
     return ECH_EINVAL;
   if (T == 0) return ECH_OK;
-  const Pages pg{page_table, pt_ld, n_slots, page_size};
+  const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
   hipLaunchKernelGGL(paged_append_kernel, dim3((T + 3) / 4), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
                      static_cast<uint4*>(pool), (int)(row_bytes / 16), pg, row0, seq_len, B, T,
                      static_cast<const uint4*>(rows), row_stride / 16, status);
@@ -203,7 +203,7 @@ extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* 
   ECH_LAUNCH_CHECK();
   if (!pool) return ECH_OK;
   const int row16 = (int)(row_bytes / 16);
-  const Pages a{src_table, pt_ld, n_slots, page_size}, d{dst_table, pt_ld, n_slots, page_size};
+  const Pages a = make_pages(src_table, pt_ld, n_slots, page_size), d = make_pages(dst_table, pt_ld, n_slots, page_size);
   if (src_table == dst_table)
     hipLaunchKernelGGL(paged_move_within_kernel, dim3((row16 + 3) / 4, B), dim3(1024), 0, s, static_cast<uint4*>(pool),
                        row16, a, kept, keep);

@@ -147,7 +147,7 @@ extern "C" int ech_paged_weight(const void* q, int64_t q_row_stride, int64_t q_h
   if (ws_bytes < need || (need && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)))) return ECH_EINVAL;
   if (max_len == 0) return ECH_OK;
   const int parts = parts_of(B, T, H, max_rows, max_len);
-  const Pages pg{page_table, pt_ld, n_slots, page_size};
+  const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(paged_weight_kernel, dim3((max_len + kTokWg - 1) / kTokWg, B, parts), dim3(256), 0, s,
                      static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, lse, static_cast<const uint4*>(pool),
