@@ -28,9 +28,8 @@ def sources():
 
 # Sources built without -amdgpu-mfma-vgpr-form: their MFMA accumulators
 # outgrow the 256 architectural VGPRs and must live in accumulation
-# registers (the sparse attention keeps 32 heads x 512 values per wave, the
-# paged one 128 queries x 128 values).
-ACC_REG_SOURCES = {'attn.hip', 'paged_attn.hip'}
+# registers (the sparse attention keeps 32 heads x 512 values per wave).
+ACC_REG_SOURCES = {'attn.hip'}
 
 
 def _flags(src: str):

@@ -43,7 +43,8 @@ constexpr int kTailAt = kStepTok * kVPitch;  // the rows' last 64 values (rotary
 constexpr int kTileB = kTailAt + kStepTok * 128;
 constexpr int kBufs = 3;
 constexpr int kPPitch = 80;                  // bytes per query of P in LDS (64 + 16: bank spread)
-constexpr int kKD = 4;                       // key fragments in flight
+constexpr int kKD = 3;                       // key fragments in flight
+constexpr int kSplit = 30;                   // products of a step's scores before the barrier that publishes P
 
 #define ECH_LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
 
@@ -55,17 +56,14 @@ __device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// The same with the sums in vector registers, which the weights are computed
-// from (the builtin's go to accumulation registers, all of which the output
-// takes). The compiler does not see that these are matrix instructions, so
-// mfma32_v_done stands between the last of them and any other use.
-__device__ __forceinline__ void mfma32_v_first(f32x16_t& d, bf16x8_t a, bf16x8_t b) {
-  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
+// The same onto an accumulator that stays in accumulation registers (the
+// output takes all 256 of them, so none is left for the compiler to choose).
+// The compiler does not see that this is a matrix instruction, so other
+// instructions that touch the accumulator stand behind mfma32_acc_done.
+__device__ __forceinline__ void mfma32_acc(f32x16_t& d, bf16x8_t a, bf16x8_t b) {
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(d) : "v"(a), "v"(b));
 }
-__device__ __forceinline__ void mfma32_v(f32x16_t& d, bf16x8_t a, bf16x8_t b) {
-  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
-}
-__device__ __forceinline__ void mfma32_v_done(f32x16_t& d) { asm volatile("s_nop 15" : "+v"(d)); }
+__device__ __forceinline__ void mfma32_acc_done() { asm volatile("s_nop 15\n\ts_nop 7"); }
 
 // 8 tokens x this lane's column, from two transposed reads of 4 tokens.
 __device__ __forceinline__ bf16x8_t ld_tr8(const uint8_t* p0, const uint8_t* p1) {
@@ -148,6 +146,20 @@ __global__ void __launch_bounds__(256, 1)
   const int per = (rg.steps + nsp - 1) / nsp;
   const int step0 = min(sp * per, rg.steps), nsteps = min(step0 + per, rg.steps) - step0;
 
+  const int64_t mg0 = (int64_t)sr.first * H + m0;          // first query among the batch's (row, head) pairs
+  const int64_t MT_all = (int64_t)T * H;
+  if (nsteps <= 0) {
+    // nothing to see (a table without pages for it, a span past the end)
+    for (int x = threadIdx.x; x < min(kMT, M - m0); x += 256) {
+      if (nsp > 1) part_ml[sp * MT_all + mg0 + x] = make_float2(-__builtin_inff(), 0.f);
+      else if (lse) lse[mg0 + x] = -__builtin_inff();
+    }
+    if (nsp == 1)
+      for (int x = threadIdx.x; x < min(kMT, M - m0) * (kPagedVal / 8); x += 256)
+        reinterpret_cast<uint4*>(out + mg0 * kPagedVal)[x] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+
   // this lane's query of row tile `wave`
   const int m = m0 + wave * 32 + col;
   const bool live = m < M;
@@ -179,24 +191,25 @@ __global__ void __launch_bounds__(256, 1)
   // This wave's eight tokens of a step: 8 wave .. +7. A token without a slot
   // brings slot 0's row, which no query weighs.
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(&tiles[0])));
-  auto issue = [&](int slot, int buf) {
-    const uint32_t base = lds0 + static_cast<uint32_t>(buf * kTileB);
+  auto issue_row = [&](int slot, int buf, int j) {
     const uint32_t voff = lane * 16;
+    const int tok = wave * 8 + j;
+    const int sl = max(__builtin_amdgcn_readlane(slot, tok), 0);
+    const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2);
+    const uint32_t lds = lds0 + static_cast<uint32_t>(buf * kTileB + tok * kVPitch);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src) : "memory", "m0");
+  };
+  auto issue_tails = [&](int slot, int buf) {
+    const int k = lane >> 3, tok = wave * 8 + k;
+    const int sl = max(__shfl(slot, tok, 64), 0);
+    const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16);
+    const uint32_t lds = lds0 + static_cast<uint32_t>(buf * kTileB + kTailAt + wave * 1024);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+  };
+  auto issue = [&](int slot, int buf) {
+    issue_tails(slot, buf);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int tok = wave * 8 + j;
-      const int sl = max(__builtin_amdgcn_readlane(slot, tok), 0);
-      const uint8_t* src = pool + (int64_t)sl * (kPagedRow * 2);
-      const uint32_t lds = base + static_cast<uint32_t>(tok * kVPitch);
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src) : "memory", "m0");
-    }
-    {
-      const int k = lane >> 3, tok = wave * 8 + k;
-      const int sl = max(__shfl(slot, tok, 64), 0);
-      const uint8_t* src = pool + (int64_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16);
-      const uint32_t lds = base + static_cast<uint32_t>(kTailAt + wave * 1024);
-      asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
-    }
+    for (int j = 0; j < 8; ++j) issue_row(slot, buf, j);
   };
   // key fragment s of the token `col` of a buffer
   auto kload = [&](const uint8_t* buf, int s) -> bf16x8_t {
@@ -229,27 +242,22 @@ __global__ void __launch_bounds__(256, 1)
   uint8_t* const pmine = ps + (wave * 32 + col) * kPPitch + g * 16;
   const uint8_t* const pall = ps + col * kPPitch + g * 16;
 
-  // One step: the weights of step i from its scores st (lane: query col, tokens
-  // t0 + 8 (v / 4) + 4 g + v % 4), a few instructions behind each product of
-  // the next step's scores nx. The order is the one written: a group per
+  // The weights of a step from its scores st (lane: query col, tokens t0 + 8 (v
+  // / 4) + 4 g + v % 4), a few instructions behind each of the first products
+  // of the next step's scores nx. The order is the one written: a group per
   // product, closed by a scheduling barrier, key fragments kKD products ahead.
-  auto weigh = [&](auto has_next, auto whole, f32x16_t& st, f32x16_t& nx, const uint8_t* kbuf, uint32_t bits) {
-    constexpr bool NEXT = decltype(has_next)::value, FULL = decltype(whole)::value;
-    bf16x8_t kb[kKD];
-    if constexpr (NEXT) {
+  bf16x8_t kb[kKD];
+  auto weigh = [&](auto whole, f32x16_t& st, f32x16_t& nx, const uint8_t* kbuf, uint32_t bits) {
+    constexpr bool FULL = decltype(whole)::value;
 #pragma unroll
-      for (int s = 0; s < kKD; ++s) kb[s] = kload(kbuf, s);
-    }
+    for (int v = 0; v < 16; ++v) nx[v] = 0.f;
     float tmax = -__builtin_inff(), ref = 0.f, alpha = 1.f, psum = 0.f;
     bool poison = false, grow = false;
     bf16x8_t pb[2];
 #pragma unroll
-    for (int s = 0; s < kKs16; ++s) {
-      if constexpr (NEXT) {
-        if (s == 0) mfma32_v_first(nx, kb[0], qf[0]);
-        else mfma32_v(nx, kb[s % kKD], qf[s]);
-        if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
-      }
+    for (int s = 0; s < kSplit; ++s) {
+      nx = mfma32(kb[s % kKD], qf[s], nx);
+      kb[s % kKD] = kload(kbuf, s + kKD);
       if (s < 8) {
 #pragma unroll
         for (int v = 2 * s; v < 2 * s + 2; ++v) {
@@ -288,145 +296,174 @@ __global__ void __launch_bounds__(256, 1)
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (NEXT) mfma32_v_done(nx);
   };
-
-  if (nsteps > 0) {
-    int page, off;                   // of the step to load next
-    uint32_t ok0, ok1 = 0, ok2 = 0;  // tokens with a slot of steps i, i + 1, i + 2
-    {
-      int off0, off1;
-      const int i1 = min(1, nsteps - 1);
-      const int page0 = fetch_page(0, off0), page1 = fetch_page(i1, off1);
-      page = fetch_page(min(2, nsteps - 1), off);
-      const int s0 = slot_at(0, page0, off0), s1 = slot_at(i1, page1, off1);
-      ok0 = (uint32_t)__ballot(s0 >= 0);
-      ok1 = (uint32_t)__ballot(s1 >= 0);
-      issue(s0, 0);
-      if (nsteps > 1) issue(s1, 1);
+  // the tokens of a step that this lane's query sees, as bits for its 16 scores
+  auto seen_bits = [&](int t0, uint32_t ok) -> uint32_t {
+    const int d = p_row - t0;    // last visible, relative
+    uint32_t bits = d < 0 ? 0u : (d >= 31 ? 0xffffffffu : (2u << d) - 1u);
+    if (window != 0) {
+      const int lo = d - window + 1, sk = n_sink - t0;
+      const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
+      const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
+      bits &= win | first;
     }
+    return (bits & ok) >> (4 * g);
+  };
+  auto whole_step = [&](int t0, uint32_t ok) -> bool {
+    return ok == 0xffffffffu && t0 + kStepTok - 1 <= p_lo &&
+           (window == 0 || t0 > p_hi - window || t0 + kStepTok <= n_sink);
+  };
+  // what the weights of a step change before its value product: accumulators of
+  // grown maxima, values that are not finite; true if values changed
+  auto adjust = [&](int cur) -> bool {
+    int flags[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) flags[r] = __builtin_amdgcn_readfirstlane(s_flag[r]);
+    const int any = flags[0] | flags[1] | flags[2] | flags[3];
+    if (any == 0) return false;
+    mfma32_acc_done();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (flags[r] & 1) {
+        const float a = s_alpha[r * 32 + col];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          asm volatile("" : "+a"(acc[c][r]));   // one accumulator at a time leaves its registers
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[c][r][v] *= a;
+          asm volatile("" : "+a"(acc[c][r]));
+        }
+      }
+    }
+    asm volatile("s_nop 7");
+    if (!(any & 2)) return false;
+    // A weight of zero must add nothing, but 0 x inf is NaN: values that
+    // are not finite become 0 in this wave's columns of the step. A query
+    // that sees such a row has a score, so a weight, that is NaN already.
+    for (int x = lane; x < kStepTok * 16; x += 64) {
+      uint16_t* e = reinterpret_cast<uint16_t*>(tiles + cur * kTileB + (x >> 4) * kVPitch + wave * 256 + (x & 15) * 16);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    return true;
+  };
+  auto pload = [&](int c, int r) -> bf16x8_t { return ld_bf16x8(pall + r * 32 * kPPitch + c * 32); };
+
+  int page, off;                   // of the step to load next
+  uint32_t ok0, ok1, ok2;          // tokens with a slot of steps i, i + 1, i + 2
+  {
+    // a span shorter than three steps loads its last one again
+    int off0, off1, off2;
+    const int i1 = min(1, nsteps - 1), i2 = min(2, nsteps - 1);
+    const int page0 = fetch_page(0, off0), page1 = fetch_page(i1, off1), page2 = fetch_page(i2, off2);
+    page = fetch_page(min(3, nsteps - 1), off);
+    const int s0 = slot_at(0, page0, off0), s1 = slot_at(i1, page1, off1), s2 = slot_at(i2, page2, off2);
+    ok0 = (uint32_t)__ballot(s0 >= 0);
+    ok1 = (uint32_t)__ballot(s1 >= 0);
+    ok2 = (uint32_t)__ballot(s2 >= 0);
+    issue(s0, 0);
+    issue(s1, 1);
     __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
     __syncthreads();
-    f32x16_t st, nx;
-    {
-      bf16x8_t kb[kKD];
+    issue(s2, 2);
+  }
+  f32x16_t st, nx;
 #pragma unroll
-      for (int s = 0; s < kKD; ++s) kb[s] = kload(tiles, s);
+  for (int v = 0; v < 16; ++v) st[v] = 0.f;
 #pragma unroll
-      for (int s = 0; s < kKs16; ++s) {
-        if (s == 0) mfma32_v_first(st, kb[0], qf[0]);
-        else mfma32_v(st, kb[s % kKD], qf[s]);
-        if (s + kKD < kKs16) kb[s % kKD] = kload(tiles, s + kKD);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      mfma32_v_done(st);
-    }
+  for (int s = 0; s < kKD; ++s) kb[s] = kload(tiles, s);
+#pragma unroll
+  for (int s = 0; s < kKs16; ++s) {
+    st = mfma32(kb[s % kKD], qf[s], st);
+    kb[s % kKD] = s + kKD < kKs16 ? kload(tiles, s + kKD) : kload(tiles + kTileB, s + kKD - kKs16);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
-    int cur = 0, nxt = 1, far = 2;   // buffers of steps i, i + 1, i + 2
-    for (int i = 0; i < nsteps; ++i) {
-      if (i + 2 < nsteps) {
-        const int slot = slot_at(i + 2, page, off);
-        ok2 = (uint32_t)__ballot(slot >= 0);
-        page = fetch_page(min(i + 3, nsteps - 1), off);   // read in the next round, after this round's wait
-        issue(slot, far);
-      }
-      int cnt;
-      const int t0 = step_tok(i, &cnt);
-      const bool full = ok0 == 0xffffffffu && t0 + kStepTok - 1 <= p_lo &&
-                        (window == 0 || t0 > p_hi - window || t0 + kStepTok <= n_sink);
-      const uint8_t* kbuf = tiles + nxt * kTileB;
+  // Every round forms the scores of the next step and loads the one three
+  // ahead; past the span's end these are repeats that nothing uses, which
+  // keeps the round one straight piece of code.
+  int cur = 0, nxt = 1, far = 2;   // buffers of steps i, i + 1, i + 2
+  int cnt, t0 = step_tok(0, &cnt);
+  auto round = [&](int i, f32x16_t& st, f32x16_t& nx) {
+    // scores of step i + 1 beside the weights of step i
+    const uint8_t* kbuf = tiles + nxt * kTileB;
+    if (whole_step(t0, ok0)) weigh(std::true_type{}, st, nx, kbuf, 0);
+    else weigh(std::false_type{}, st, nx, kbuf, seen_bits(t0, ok0));
+    bf16x8_t vf[2], pf[2][4];
+    vf[0] = vload(cur, 0, 0);
+    vf[1] = vload(cur, 0, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    // P and the flags cross while the last of those products run
+#pragma unroll
+    for (int r = 0; r < 4; ++r) pf[0][r] = pload(0, r);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = kSplit; s < kKs16; ++s) {
+      nx = mfma32(kb[s % kKD], qf[s], nx);
+      if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
       __builtin_amdgcn_sched_barrier(0);
-      if (full) {
-        if (i + 1 < nsteps) weigh(std::true_type{}, std::true_type{}, st, nx, kbuf, 0);
-        else weigh(std::false_type{}, std::true_type{}, st, nx, kbuf, 0);
-      } else {
-        // the tokens this lane's query sees: bit t
-        const int d = p_row - t0;    // last visible, relative
-        uint32_t bits = d < 0 ? 0u : (d >= 31 ? 0xffffffffu : (2u << d) - 1u);
-        if (window != 0) {
-          const int lo = d - window + 1, sk = n_sink - t0;
-          const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
-          const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
-          bits &= win | first;
-        }
-        bits = (bits & ok0) >> (4 * g);
-        if (i + 1 < nsteps) weigh(std::true_type{}, std::false_type{}, st, nx, kbuf, bits);
-        else weigh(std::false_type{}, std::false_type{}, st, nx, kbuf, bits);
-      }
-      bf16x8_t vf[2], pf[2][4];
+    }
+    if (adjust(cur)) {
       vf[0] = vload(cur, 0, 0);
       vf[1] = vload(cur, 0, 1);
-      __builtin_amdgcn_sched_barrier(0);
-      __syncthreads();
-
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // O^T += V^T P^T: a group per value fragment, two fragments ahead
 #pragma unroll
-      for (int r = 0; r < 4; ++r) pf[0][r] = ld_bf16x8(pall + r * 32 * kPPitch);
-      int flags[4];
+    for (int x = 0; x < 6; ++x) {
+      const int c = x >> 2, ct = x & 3;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) flags[r] = __builtin_amdgcn_readfirstlane(s_flag[r]);
-      if (flags[0] | flags[1] | flags[2] | flags[3]) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (flags[r] & 1) {
-            const float a = s_alpha[r * 32 + col];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              asm volatile("" : "+a"(acc[c][r]));   // one accumulator at a time leaves its registers
-#pragma unroll
-              for (int v = 0; v < 16; ++v) acc[c][r][v] *= a;
-              asm volatile("" : "+a"(acc[c][r]));
-            }
-          }
-        }
-        if ((flags[0] | flags[1] | flags[2] | flags[3]) & 2) {
-          // A weight of zero must add nothing, but 0 x inf is NaN: values that
-          // are not finite become 0 in this wave's columns of the step. A query
-          // that sees such a row has a score, so a weight, that is NaN already.
-          for (int x = lane; x < kStepTok * 16; x += 64) {
-            uint16_t* e = reinterpret_cast<uint16_t*>(tiles + cur * kTileB + (x >> 4) * kVPitch + wave * 256 + (x & 15) * 16);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
-          }
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          vf[0] = vload(cur, 0, 0);
-          vf[1] = vload(cur, 0, 1);
-        }
+      for (int r = 0; r < 4; ++r) mfma32_acc(acc[ct][r], vf[x & 1], pf[c][r]);
+      vf[x & 1] = vload(cur, (x + 2) >> 2, (x + 2) & 3);
+      if (x < 2) {
+        pf[1][2 * x] = pload(1, 2 * x);
+        pf[1][2 * x + 1] = pload(1, 2 * x + 1);
       }
       __builtin_amdgcn_sched_barrier(0);
-      // O^T += V^T P^T: a group per value fragment, two fragments ahead
+    }
+    const int slot = i + 3 < nsteps ? slot_at(i + 3, page, off) : -1;
+    // Every wave has read its values and weights of step i, and its loads of
+    // step i + 2 have landed.
+    __builtin_amdgcn_s_waitcnt(0x70);           // vmcnt(0), lgkmcnt(0)
+    __syncthreads();
+    const uint8_t* kfar = tiles + far * kTileB;
+    issue_tails(slot, cur);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int c = x >> 2, ct = x & 3;
+    for (int x = 6; x < 8; ++x) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[ct][r] = mfma32(vf[x & 1], pf[c][r], acc[ct][r]);
-        if (x + 2 < 8) vf[x & 1] = vload(cur, (x + 2) >> 2, (x + 2) & 3);
-        if (x < 2) {
-          pf[1][2 * x] = ld_bf16x8(pall + 2 * x * 32 * kPPitch + 32);
-          pf[1][2 * x + 1] = ld_bf16x8(pall + (2 * x + 1) * 32 * kPPitch + 32);
-        }
+      for (int r = 0; r < 4; ++r) {
+        mfma32_acc(acc[x & 3][r], vf[x & 1], pf[1][r]);
+        if (x == 6 && r < kKD) kb[r] = kload(kfar, r);
+        issue_row(slot, cur, (x - 6) * 4 + r);
         __builtin_amdgcn_sched_barrier(0);
       }
-      st = nx;
-      ok0 = ok1;
-      ok1 = ok2;
-      const int t = cur;
-      cur = nxt;
-      nxt = far;
-      far = t;
-      if (i + 1 < nsteps) {
-        __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads of step i + 2 have landed
-        __syncthreads();
-      }
     }
+    page = fetch_page(min(i + 4, nsteps - 1), off);   // in by the end of the next step
+    ok0 = ok1;
+    ok1 = ok2;
+    ok2 = (uint32_t)__ballot(slot >= 0);
+    t0 = step_tok(min(i + 1, nsteps - 1), &cnt);
+    const int t = cur;
+    cur = nxt;
+    nxt = far;
+    far = t;
+  };
+  for (int i = 0; i < nsteps; i += 2) {   // two at a time: the scores change places without a copy
+    round(i, st, nx);
+    if (i + 1 >= nsteps) break;
+    round(i + 1, nx, st);
   }
+  __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // no load of a repeat is under way when the workgroup ends
+  mfma32_acc_done();
 
   l = pair_sum(l);
   if (g == 0) {
     s_m[wave * 32 + col] = mx;
     s_l[wave * 32 + col] = l;
   }
-  const int64_t mg0 = (int64_t)sr.first * H + m0;          // first query among the batch's (row, head) pairs
   if (nsp == 1) {
     __syncthreads();
     if (lse && live && g == 0)
@@ -452,9 +489,7 @@ __global__ void __launch_bounds__(256, 1)
     }
     return;
   }
-  const int64_t MT_all = (int64_t)T * H;
   if (live && g == 0) part_ml[sp * MT_all + mg0 + wave * 32 + col] = make_float2(mx, l);
-  if (nsteps == 0) return;                                  // its (-inf, 0) says so
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int mm = r * 32 + col;
