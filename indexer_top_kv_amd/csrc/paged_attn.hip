@@ -103,9 +103,90 @@ __device__ __forceinline__ Ranges ranges_of(int p_lo, int p_hi, int window, int 
   return r;
 }
 
-// grid (tiles x spans): workgroup = (tile of 128 queries of one sequence, span
-// of its steps). With one span it writes out and lse; with several the span's
-// maximum, sum and unnormalised output go to the workspace.
+// What a workgroup does: span sp of the n_span spans of tile mt of sequence b;
+// the tile's spans are workgroups base .. base + n_span - 1.
+struct Work {
+  int b, mt, sp, n_span, base;
+};
+
+constexpr int kCus = 256;
+constexpr int kMinSpan = 4;          // steps a span is worth its start and its partial
+constexpr int kPlanSeqs = 256;       // sequences a plan covers (four per lane)
+
+__device__ __forceinline__ int wave_max(int v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = max(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// The batch's tiles split over the card's CUs: every tile takes ceil(steps /
+// S) spans with one S for all, the smallest for which the spans are at most as
+// many as the CUs, so that a batch of unequal lengths ends at one time.
+// (Spans of equal number per sequence instead: 32 decoded tokens at 128 heads
+// over 8K to 16K tokens 165 us, with this 153 us.) All tiles of a sequence
+// count as its last and longest. Every wave computes it alike, a sequence (of
+// each 64) per lane.
+__device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* seq_len, const Pages& pg, int B, int T,
+                                          int H, int max_rows, int max_len, int window, int n_sink, int wg) {
+  const int lane = ech::lane_id();
+  int nt[kPlanSeqs / 64], st[kPlanSeqs / 64];
+  int tiles = 0, total = 0, longest = 1;
+#pragma unroll
+  for (int c = 0; c < kPlanSeqs / 64; ++c) {
+    nt[c] = 0;
+    st[c] = 1;
+    if (c * 64 < B) {
+      const int b = c * 64 + lane;
+      if (b < B) {
+        const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+        nt[c] = (sr.n * H + kMT - 1) / kMT;
+        if (nt[c] > 0)
+          st[c] = max(1, ranges_of(sr.pos0 + (nt[c] - 1) * kMT / H, sr.pos0 + sr.n - 1, window, n_sink).steps);
+      }
+      tiles += nt[c];
+      total += nt[c] * st[c];
+      if (nt[c] > 0) longest = max(longest, st[c]);
+    }
+  }
+  tiles = ech::wave_sum(tiles);
+  total = ech::wave_sum(total);
+  longest = wave_max(longest);
+  auto spans = [&](int S) -> int {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < kPlanSeqs / 64; ++c)
+      if (c * 64 < B) n += nt[c] * ((st[c] + S - 1) / S);
+    return ech::wave_sum(n);
+  };
+  int lo = max(kMinSpan, (total + kCus - 1) / kCus), hi = max(lo, longest);   // spans(hi) = tiles <= kCus
+  if (tiles < kCus) hi = min(hi, max(lo, total / (kCus - tiles) + 1));         // sum ceil(x) < sum x + tiles
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (spans(mid) <= kCus) hi = mid;
+    else lo = mid + 1;
+  }
+  int base = 0;
+#pragma unroll
+  for (int c = 0; c < kPlanSeqs / 64; ++c) {
+    if (c * 64 < B) {
+      const int n = (st[c] + hi - 1) / hi, mine = nt[c] * n;
+      const int incl = ech::wave_incl_scan(mine);
+      const unsigned long long past = __ballot(base + incl > wg);
+      if (past != 0ull) {
+        const int l = __builtin_ctzll(past);
+        const int first = base + __shfl(incl, l, 64) - __shfl(mine, l, 64), ns = __shfl(n, l, 64);
+        const int mt = (wg - first) / ns, at = first + mt * ns;
+        return Work{c * 64 + l, mt, wg - at, ns, at};
+      }
+      base += __shfl(incl, 63, 64);
+    }
+  }
+  return Work{-1, 0, 0, 1, 0};
+}
+
+// Workgroup = (tile of 128 queries of one sequence, span of its steps). With
+// one span it writes out and lse; with several the span's maximum, sum and
+// unnormalised output go to the workspace, and where its spans are to `info`.
 //
 // One wave per SIMD, so a step's phases overlap inside the wave: while the
 // matrix cores form the scores of step i + 1, the vector unit turns those of
@@ -121,22 +202,27 @@ __device__ __forceinline__ Ranges ranges_of(int p_lo, int p_hi, int window, int 
 __global__ void __launch_bounds__(256, 1)
     paged_attn_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool, Pages pg,
                       const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B, int T, int H,
-                      int max_rows, int max_len, int window, int n_sink, float scale2, int nsp,
+                      int max_rows, int max_len, int window, int n_sink, float scale2, int planned, int rows_per,
                       uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
-                      float2* __restrict__ part_ml) {
-  __shared__ __align__(16) uint8_t tiles[kBufs * kTileB];
+                      float2* __restrict__ part_ml, int2* __restrict__ info) {
+  __shared__ __align__(128) uint8_t tiles[kBufs * kTileB];
   __shared__ __align__(16) uint8_t ps[kMT * kPPitch];
   __shared__ float s_alpha[kMT], s_m[kMT], s_l[kMT];
   __shared__ int s_flag[4];   // per row tile: 1 = its maximum grew, 2 = a score that does not count is not finite
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
-  int b, mt;
-  find_tile(row0, B, T, max_rows, H, kMT, blockIdx.x / nsp, &b, &mt);
-  b = __builtin_amdgcn_readfirstlane(b);
+  Work wk;
+  if (planned) {
+    wk = plan_work(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
+  } else {
+    // more tiles than CUs: a tile each, the last (and in a chunk longest) first
+    wk = Work{-1, 0, 0, 1, 0};
+    find_tile(row0, B, T, max_rows, H, kMT, (int)(gridDim.x - 1 - blockIdx.x), &wk.b, &wk.mt);
+  }
+  const int b = __builtin_amdgcn_readfirstlane(wk.b), mt = __builtin_amdgcn_readfirstlane(wk.mt);
+  const int sp = __builtin_amdgcn_readfirstlane(wk.sp), nsp = __builtin_amdgcn_readfirstlane(wk.n_span);
   if (b < 0) return;
-  mt = __builtin_amdgcn_readfirstlane(mt);
-  const int sp = blockIdx.x % nsp;
   const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
   const int M = sr.n * H;                                  // fits: T H < 2^30 (checked on the host)
   const int m0 = mt * kMT;
@@ -147,11 +233,13 @@ __global__ void __launch_bounds__(256, 1)
   const int step0 = min(sp * per, rg.steps), nsteps = min(step0 + per, rg.steps) - step0;
 
   const int64_t mg0 = (int64_t)sr.first * H + m0;          // first query among the batch's (row, head) pairs
-  const int64_t MT_all = (int64_t)T * H;
+  float2* const my_ml = part_ml + (int64_t)blockIdx.x * rows_per;
+  if (planned && sp == 0)
+    for (int x = threadIdx.x; x < min(kMT, M - m0); x += 256) info[mg0 + x] = make_int2(wk.base * kMT + x, nsp);
   if (nsteps <= 0) {
     // nothing to see (a table without pages for it, a span past the end)
     for (int x = threadIdx.x; x < min(kMT, M - m0); x += 256) {
-      if (nsp > 1) part_ml[sp * MT_all + mg0 + x] = make_float2(-__builtin_inff(), 0.f);
+      if (nsp > 1) my_ml[x] = make_float2(-__builtin_inff(), 0.f);
       else if (lse) lse[mg0 + x] = -__builtin_inff();
     }
     if (nsp == 1)
@@ -162,7 +250,6 @@ __global__ void __launch_bounds__(256, 1)
 
   // this lane's query of row tile `wave`
   const int m = m0 + wave * 32 + col;
-  const bool live = m < M;
   const int mr = min(m, M - 1) / H, mh = min(m, M - 1) - mr * H;   // past the end: the last one again, never written
   const int p_row = sr.pos0 + mr;
   const int32_t* trow = pg.table + (int64_t)b * pg.ld;
@@ -212,17 +299,11 @@ __global__ void __launch_bounds__(256, 1)
     for (int j = 0; j < 8; ++j) issue_row(slot, buf, j);
   };
   // key fragment s of the token `col` of a buffer
+  const uint32_t k_off = col * kVPitch + g * 16, k_tail = kTailAt + col * 128 + ((g ^ (col & 7)) * 16);
   auto kload = [&](const uint8_t* buf, int s) -> bf16x8_t {
-    return s < 32 ? ld_bf16x8(buf + col * kVPitch + g * 16 + s * 32)
-                  : ld_bf16x8(buf + kTailAt + col * 128 + (((2 * (s - 32) + g) ^ (col & 7)) * 16));
+    return ld_bf16x8(buf + (s < 32 ? k_off + s * 32 : k_tail ^ ((s - 32) * 32)));   // tail pieces 2 (s - 32) + g, xor-ed
   };
-
-  bf16x8_t qf[kKs16];
-  {
-    const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + g * 16;
-#pragma unroll
-    for (int s = 0; s < kKs16; ++s) qf[s] = ld_bf16x8(qp + s * 32);
-  }
+  bf16x8_t qf[kKs16];   // the query, loaded behind the first rows
   f32x16_t acc[4][4];   // [column tile][row tile]
 #pragma unroll
   for (int c = 0; c < 4; ++c)
@@ -365,10 +446,15 @@ __global__ void __launch_bounds__(256, 1)
     ok2 = (uint32_t)__ballot(s2 >= 0);
     issue(s0, 0);
     issue(s1, 1);
-    __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
-    __syncthreads();
     issue(s2, 2);
   }
+  {
+    const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + g * 16;
+#pragma unroll
+    for (int s = 0; s < kKs16; ++s) qf[s] = ld_bf16x8(qp + s * 32);
+  }
+  __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
+  __syncthreads();
   f32x16_t st, nx;
 #pragma unroll
   for (int v = 0; v < 16; ++v) st[v] = 0.f;
@@ -460,21 +546,25 @@ __global__ void __launch_bounds__(256, 1)
   mfma32_acc_done();
 
   l = pair_sum(l);
-  if (g == 0) {
-    s_m[wave * 32 + col] = mx;
-    s_l[wave * 32 + col] = l;
+  int tid = threadIdx.x;             // recomputed: held across the loop these would take registers it needs
+  asm volatile("" : "+v"(tid));
+  const int ecol = tid & 31, eg = (tid >> 5) & 1;
+  const bool elive = m0 + wave * 32 + ecol < M;
+  if (eg == 0) {
+    s_m[wave * 32 + ecol] = mx;
+    s_l[wave * 32 + ecol] = l;
   }
   if (nsp == 1) {
     __syncthreads();
-    if (lse && live && g == 0)
-      lse[mg0 + wave * 32 + col] = l == 0.f ? -__builtin_inff() : (mx + log2f(l)) * 0.69314718055994531f;
+    if (lse && elive && eg == 0)
+      lse[mg0 + wave * 32 + ecol] = l == 0.f ? -__builtin_inff() : (mx + log2f(l)) * 0.69314718055994531f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int mm = r * 32 + col;
+      const int mm = r * 32 + ecol;
       const float sl = s_l[mm];
       const float inv = sl == 0.f ? 0.f : 1.f / sl;
       if (m0 + mm < M) {
-        uint16_t* o = out + (mg0 + mm) * kPagedVal + wave * 128 + 4 * g;
+        uint16_t* o = out + (mg0 + mm) * kPagedVal + wave * 128 + 4 * eg;
 #pragma unroll
         for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
@@ -489,12 +579,12 @@ __global__ void __launch_bounds__(256, 1)
     }
     return;
   }
-  if (live && g == 0) part_ml[sp * MT_all + mg0 + wave * 32 + col] = make_float2(mx, l);
+  if (elive && eg == 0) my_ml[wave * 32 + ecol] = make_float2(mx, l);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const int mm = r * 32 + col;
+    const int mm = r * 32 + ecol;
     if (m0 + mm < M) {
-      float* o = part_o + (sp * MT_all + mg0 + mm) * kPagedVal + wave * 128 + 4 * g;
+      float* o = part_o + ((int64_t)blockIdx.x * rows_per + mm) * kPagedVal + wave * 128 + 4 * eg;
 #pragma unroll
       for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
@@ -505,29 +595,53 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
-// out and lse of every query from its spans' partials, in span order.
-// grid (T H), 128 threads: four value columns each.
+// out and lse of every query that took several spans, from their partials in
+// span order. grid (T H), 128 threads: four value columns each; the spans'
+// loads go out kG at a time before the first is waited for.
+constexpr int kG = 8;
 __global__ void __launch_bounds__(128)
     paged_attn_merge_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                            const int32_t* __restrict__ row0, int B, int T, int H, int nsp, uint16_t* __restrict__ out,
-                            float* __restrict__ lse) {
+                            const int2* __restrict__ info, const int32_t* __restrict__ row0, int B, int T, int H,
+                            int rows_per, int n_wg, uint16_t* __restrict__ out, float* __restrict__ lse) {
   const int64_t mg = blockIdx.x;
   const int row = (int)(mg / H);
   if (row < row0[0] || row >= row0[B]) return;              // a row of no sequence stays as it was
-  const int64_t MT_all = (int64_t)T * H;
-  float mx = -__builtin_inff();
-  for (int s = 0; s < nsp; ++s) mx = fmaxf(mx, part_ml[s * MT_all + mg].x);
-  const float ref = mx == -__builtin_inff() ? 0.f : mx;
-  float den = 0.f;
+  const int2 in = info[mg];
+  const int n = in.y;
+  const int base = in.x / kMT, mm = in.x % kMT;
+  // one span wrote its output itself; a query past max_rows has no info
+  if (n <= 1 || in.x < 0 || n > n_wg || base > n_wg - n || mm >= rows_per) return;
+  const float2* ml = part_ml + (int64_t)base * rows_per + mm;
+  const float* po = part_o + ((int64_t)base * rows_per + mm) * kPagedVal + 4 * threadIdx.x;
+  float mx = -__builtin_inff(), den = 0.f;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < nsp; ++s) {
-    const float2 ml = part_ml[s * MT_all + mg];
-    if (ml.y == 0.f) continue;                              // saw nothing: no output was written
-    const float w = exp2f((ml.x == -__builtin_inff() ? 0.f : ml.x) - ref);
-    den += w * ml.y;
-    const f32x4_t x = *reinterpret_cast<const f32x4_t*>(part_o + (s * MT_all + mg) * kPagedVal + 4 * threadIdx.x);
+  for (int s0 = 0; s0 < n; s0 += kG) {
+    float2 a[kG];
+    f32x4_t x[kG];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += w * x[e];
+    for (int j = 0; j < kG; ++j) {
+      const int64_t s = min(s0 + j, n - 1);
+      a[j] = ml[s * rows_per];
+      x[j] = *reinterpret_cast<const f32x4_t*>(po + s * rows_per * kPagedVal);
+    }
+    float top = mx;
+#pragma unroll
+    for (int j = 0; j < kG; ++j) top = fmaxf(top, a[j].x);
+    const float ref = top == -__builtin_inff() ? 0.f : top;
+    const float r = exp2f((mx == -__builtin_inff() ? ref : mx) - ref);   // o and den are 0 before anything is seen
+    den *= r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= r;
+#pragma unroll
+    for (int j = 0; j < kG; ++j) {
+      if (s0 + j < n && a[j].y != 0.f) {                    // a span that saw nothing wrote no output
+        const float w = exp2f((a[j].x == -__builtin_inff() ? ref : a[j].x) - ref);
+        den += w * a[j].y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += w * x[j][e];
+      }
+    }
+    mx = top;
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
   typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
@@ -536,7 +650,7 @@ __global__ void __launch_bounds__(128)
   for (int e = 0; e < 4; ++e) y[e] = (__bf16)(o[e] * inv);
   *reinterpret_cast<uint2*>(out + mg * kPagedVal + 4 * threadIdx.x) = __builtin_bit_cast(uint2, y);
   if (lse && threadIdx.x == 0)
-    lse[mg] = den == 0.f ? -__builtin_inff() : (ref + log2f(den)) * 0.69314718055994531f;
+    lse[mg] = den == 0.f ? -__builtin_inff() : (mx + log2f(den)) * 0.69314718055994531f;
 }
 
 // Upper bound of the batch's tiles: every sequence rounds up once.
@@ -545,14 +659,26 @@ int64_t tiles_of(int B, int T, int H, int max_rows) {
   return std::min<int64_t>(B * per_seq, (int64_t)T * H / kMT + B);
 }
 
-// Spans per tile: enough workgroups for the 256 CUs, four steps each at least.
-int spans_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
-  const int64_t tiles = tiles_of(B, T, H, max_rows);
-  int64_t seen = max_len;
-  if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1);
-  const int64_t steps = (seen + kStepTok - 1) / kStepTok + 1;
-  const int64_t want = std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), steps / 4);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, 64));
+// Whether tiles are split over spans, and what the workspace holds then.
+struct Split {
+  bool planned;
+  int64_t tiles;
+  int rows_per;       // queries a partial holds
+  size_t part_o, part_ml, info, bytes;
+};
+Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
+  Split sp{};
+  sp.tiles = tiles_of(B, T, H, max_rows);
+  int64_t seen = max_len;                                  // tokens a tile can read
+  if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1 + kStepTok);
+  sp.planned = sp.tiles <= kCus && B <= kPlanSeqs && seen > kMinSpan * kStepTok;
+  if (!sp.planned) return sp;
+  sp.rows_per = (int)std::min<int64_t>(kMT, (int64_t)std::min(max_rows, T) * H);
+  auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  sp.part_ml = (size_t)kCus * sp.rows_per * kPagedVal * sizeof(float);
+  sp.info = sp.part_ml + up((size_t)kCus * sp.rows_per * sizeof(float2));
+  sp.bytes = sp.info + up((size_t)T * H * sizeof(int2));
+  return sp;
 }
 
 bool shape_ok(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
@@ -564,9 +690,7 @@ bool shape_ok(int B, int T, int H, int max_rows, int max_len, int window, int n_
 
 extern "C" size_t ech_paged_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
   if (!shape_ok(B, T, H, max_rows, max_len, window, n_sink)) return 0;
-  const size_t nsp = (size_t)spans_of(B, T, H, max_rows, max_len, window, n_sink);
-  if (nsp == 1) return 0;
-  return nsp * T * H * (kPagedVal * sizeof(float) + sizeof(float2));
+  return split_of(B, T, H, max_rows, max_len, window, n_sink).bytes;
 }
 
 extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool,
@@ -585,20 +709,21 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   if (T == 0 || max_rows == 0) return ECH_OK;
   if (window >= max_len) window = 0;                       // no position has more tokens behind it
   n_sink = std::min(n_sink, max_len);
-  const int nsp = spans_of(B, T, H, max_rows, max_len, window, n_sink);
-  const int64_t tiles = tiles_of(B, T, H, max_rows);
+  const Split sp = split_of(B, T, H, max_rows, max_len, window, n_sink);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  float* part_o = static_cast<float*>(ws);
-  float2* part_ml = reinterpret_cast<float2*>(part_o + (size_t)nsp * T * H * kPagedVal);
+  char* w = static_cast<char*>(ws);
+  float* part_o = reinterpret_cast<float*>(w);
+  float2* part_ml = sp.planned ? reinterpret_cast<float2*>(w + sp.part_ml) : nullptr;
+  int2* info = sp.planned ? reinterpret_cast<int2*>(w + sp.info) : nullptr;
   const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
-  hipLaunchKernelGGL(paged_attn_kernel, dim3((unsigned)(tiles * nsp)), dim3(256), 0, s, static_cast<const uint16_t*>(q),
-                     q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg, row0, seq_len, B, T, H, max_rows,
-                     max_len, window, n_sink, sm_scale * 1.4426950408889634f, nsp, static_cast<uint16_t*>(out), lse,
-                     part_o, part_ml);
+  hipLaunchKernelGGL(paged_attn_kernel, dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
+                     static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg,
+                     row0, seq_len, B, T, H, max_rows, max_len, window, n_sink, sm_scale * 1.4426950408889634f,
+                     (int)sp.planned, sp.rows_per, static_cast<uint16_t*>(out), lse, part_o, part_ml, info);
   ECH_LAUNCH_CHECK();
-  if (nsp > 1) {
+  if (sp.planned) {
     hipLaunchKernelGGL(paged_attn_merge_kernel, dim3((unsigned)((int64_t)T * H)), dim3(kPagedVal / 4), 0, s, part_o,
-                       part_ml, row0, B, T, H, nsp, static_cast<uint16_t*>(out), lse);
+                       part_ml, info, row0, B, T, H, sp.rows_per, kCus, static_cast<uint16_t*>(out), lse);
     ECH_LAUNCH_CHECK();
   }
   return ECH_OK;
