@@ -84,11 +84,12 @@ __device__ __forceinline__ float pair_sum(float x) {
 }
 
 // The tokens a tile of queries at positions [p_lo, p_hi] reads, as up to two
-// ranges: [0, n0) and [w0, w1). Steps of 32 tokens run through the first, then
-// the second.
+// ranges: [0, n0) and [w0, w1). Steps of STEP tokens run through the first,
+// then the second.
 struct Ranges {
   int n0, w0, w1, s0, steps;
 };
+template <int STEP>
 __device__ __forceinline__ Ranges ranges_of(int p_lo, int p_hi, int window, int n_sink) {
   const int end = p_hi + 1;                               // <= len
   const int w0 = window == 0 ? 0 : max(0, p_lo - window + 1);
@@ -98,9 +99,22 @@ __device__ __forceinline__ Ranges ranges_of(int p_lo, int p_hi, int window, int 
   } else {
     r = Ranges{min(n_sink, end), w0, end, 0, 0};
   }
-  r.s0 = (r.n0 + kStepTok - 1) / kStepTok;
-  r.steps = r.s0 + (r.w1 - r.w0 + kStepTok - 1) / kStepTok;
+  r.s0 = (r.n0 + STEP - 1) / STEP;
+  r.steps = r.s0 + (r.w1 - r.w0 + STEP - 1) / STEP;
   return r;
+}
+
+// Bits of the tokens t0 .. t0 + 31 that a query at position p sees.
+__device__ __forceinline__ uint32_t sees_bits(int p, int t0, int window, int n_sink) {
+  const int d = p - t0;    // last visible, relative
+  uint32_t bits = d < 0 ? 0u : (d >= 31 ? 0xffffffffu : (2u << d) - 1u);
+  if (window != 0) {
+    const int lo = d - window + 1, sk = n_sink - t0;
+    const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
+    const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
+    bits &= win | first;
+  }
+  return bits;
 }
 
 // What a workgroup does: span sp of the n_span spans of tile mt of sequence b;
@@ -126,6 +140,7 @@ __device__ __forceinline__ int wave_max(int v) {
 // over 8K to 16K tokens 165 us, with this 153 us.) All tiles of a sequence
 // count as its last and longest. Every wave computes it alike, a sequence (of
 // each 64) per lane.
+template <int PER, int STEP>
 __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* seq_len, const Pages& pg, int B, int T,
                                           int H, int max_rows, int max_len, int window, int n_sink, int wg) {
   const int lane = ech::lane_id();
@@ -139,9 +154,9 @@ __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* se
       const int b = c * 64 + lane;
       if (b < B) {
         const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
-        nt[c] = (sr.n * H + kMT - 1) / kMT;
+        nt[c] = (sr.n * H + PER - 1) / PER;
         if (nt[c] > 0)
-          st[c] = max(1, ranges_of(sr.pos0 + (nt[c] - 1) * kMT / H, sr.pos0 + sr.n - 1, window, n_sink).steps);
+          st[c] = max(1, ranges_of<STEP>(sr.pos0 + (nt[c] - 1) * PER / H, sr.pos0 + sr.n - 1, window, n_sink).steps);
       }
       tiles += nt[c];
       total += nt[c] * st[c];
@@ -158,7 +173,7 @@ __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* se
       if (c * 64 < B) n += nt[c] * ((st[c] + S - 1) / S);
     return ech::wave_sum(n);
   };
-  int lo = max(kMinSpan, (total + kCus - 1) / kCus), hi = max(lo, longest);   // spans(hi) = tiles <= kCus
+  int lo = max(kMinSpan * kStepTok / STEP, (total + kCus - 1) / kCus), hi = max(lo, longest);   // spans(hi) = tiles <= kCus
   if (tiles < kCus) hi = min(hi, max(lo, total / (kCus - tiles) + 1));         // sum ceil(x) < sum x + tiles
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -214,7 +229,7 @@ __global__ void __launch_bounds__(256, 1)
   const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
   Work wk;
   if (planned) {
-    wk = plan_work(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
+    wk = plan_work<kMT, kStepTok>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
   } else {
     // more tiles than CUs: a tile each, the last (and in a chunk longest) first
     wk = Work{-1, 0, 0, 1, 0};
@@ -228,7 +243,7 @@ __global__ void __launch_bounds__(256, 1)
   const int m0 = mt * kMT;
   const int r_lo = m0 / H, r_hi = (min(m0 + kMT, M) - 1) / H;
   const int p_lo = sr.pos0 + r_lo, p_hi = sr.pos0 + r_hi;
-  const Ranges rg = ranges_of(p_lo, p_hi, window, n_sink);
+  const Ranges rg = ranges_of<kStepTok>(p_lo, p_hi, window, n_sink);
   const int per = (rg.steps + nsp - 1) / nsp;
   const int step0 = min(sp * per, rg.steps), nsteps = min(step0 + per, rg.steps) - step0;
 
@@ -380,23 +395,16 @@ __global__ void __launch_bounds__(256, 1)
   };
   // the tokens of a step that this lane's query sees, as bits for its 16 scores
   auto seen_bits = [&](int t0, uint32_t ok) -> uint32_t {
-    const int d = p_row - t0;    // last visible, relative
-    uint32_t bits = d < 0 ? 0u : (d >= 31 ? 0xffffffffu : (2u << d) - 1u);
-    if (window != 0) {
-      const int lo = d - window + 1, sk = n_sink - t0;
-      const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
-      const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
-      bits &= win | first;
-    }
-    return (bits & ok) >> (4 * g);
+    return (sees_bits(p_row, t0, window, n_sink) & ok) >> (4 * g);
   };
   auto whole_step = [&](int t0, uint32_t ok) -> bool {
     return ok == 0xffffffffu && t0 + kStepTok - 1 <= p_lo &&
            (window == 0 || t0 > p_hi - window || t0 + kStepTok <= n_sink);
   };
   // what the weights of a step change before its value product: accumulators of
-  // grown maxima, values that are not finite; true if values changed
-  auto adjust = [&](int cur) -> bool {
+  // grown maxima (none in the first step, they are 0), values that are not
+  // finite; true if values changed
+  auto adjust = [&](int cur, bool first) -> bool {
     int flags[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) flags[r] = __builtin_amdgcn_readfirstlane(s_flag[r]);
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(256, 1)
     mfma32_acc_done();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if (flags[r] & 1) {
+      if ((flags[r] & 1) && !first) {
         const float a = s_alpha[r * 32 + col];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -492,7 +500,7 @@ __global__ void __launch_bounds__(256, 1)
       if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (adjust(cur)) {
+    if (adjust(cur, i == 0)) {
       vf[0] = vload(cur, 0, 0);
       vf[1] = vload(cur, 0, 1);
     }
@@ -595,6 +603,361 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
+// ------------------------------------------------------------------ few queries
+// The same for sequences of at most 32 queries (a decoded token of up to 32
+// heads, two of 16): bound by the rows it reads, not by the products. The four
+// waves of a workgroup are token lanes of their own: each takes every fourth
+// 16-token step of the span with all 32 queries and all 512 value columns (256
+// accumulators), its own maximum and sum, and two step buffers of its own, so
+// nothing waits for another wave until the span's end, where the waves' states
+// are joined through LDS. In a step, on v_mfma_f32_16x16x32_bf16,
+//   S^T[token][m] = K . Q^T       16 tokens x 2 x 16 queries
+// leaves a lane four tokens of two queries; two lane swaps of the packed
+// weights turn them into the operand of O^T[col][m] += V^T . P^T
+// (v_mfma_f32_32x32x16_bf16), so P needs no LDS.
+// With the 128-query kernel: 64 sequences, one token, 32 heads, window 1024 of
+// 100K 41 us, one token of 16 heads over 1000 21 us; with this 38 and 20 us.
+constexpr int kNM = 32;                      // queries per workgroup
+constexpr int kNTok = 16;                    // tokens per step of a wave
+constexpr int kNRound = 4 * kNTok;           // tokens per step of the four waves
+constexpr int kNTail = kNTok * kVPitch;
+constexpr int kNTile = kNTail + kNTok * 128;
+constexpr int kNKs = kPagedRow / 32;         // contraction steps of the scores (18)
+constexpr int kNKD = 6;                      // key fragments in flight
+constexpr int kNLoads = kNTok + 2;           // row loads per step
+
+__device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  typedef __attribute__((__vector_size__(4 * sizeof(float)))) float v4_t;
+  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, __builtin_bit_cast(v4_t, c), 0, 0, 0));
+}
+__device__ __forceinline__ float quad_max(float x) {   // over lanes l, l ^ 16, l ^ 32, l ^ 48
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return pair_max(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return pair_sum(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+}
+
+__global__ void __launch_bounds__(256, 1)
+    paged_attn_narrow_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool,
+                             Pages pg, const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B,
+                             int T, int H, int max_rows, int max_len, int window, int n_sink, float scale2, int planned,
+                             int rows_per, uint16_t* __restrict__ out, float* __restrict__ lse,
+                             float* __restrict__ part_o, float2* __restrict__ part_ml, int2* __restrict__ info) {
+  __shared__ __align__(128) uint8_t tiles[4 * 2 * kNTile];
+  __shared__ int s_page[4][2][64];   // per wave: page-table entries of two steps' tokens
+  __shared__ float2 s_ml[4][kNM];    // per wave: maximum and sum of each query
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, col = lane & 31, g = lane >> 5;
+  Work wk{-1, 0, 0, 1, 0};
+  if (planned) wk = plan_work<kNM, kNRound>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
+  else find_tile(row0, B, T, max_rows, H, kNM, (int)blockIdx.x, &wk.b, &wk.mt);
+  const int b = __builtin_amdgcn_readfirstlane(wk.b);
+  const int sp = __builtin_amdgcn_readfirstlane(wk.sp), nsp = __builtin_amdgcn_readfirstlane(wk.n_span);
+  if (b < 0) return;
+  const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+  const int M = sr.n * H;                                  // 1 .. 32
+  const int64_t mg0 = (int64_t)sr.first * H;
+  const Ranges rg = ranges_of<kNRound>(sr.pos0, sr.pos0 + sr.n - 1, window, n_sink);
+  const int per = (rg.steps + nsp - 1) / nsp;
+  const int round0 = min(sp * per, rg.steps), rounds = min(round0 + per, rg.steps) - round0;
+  if (planned && sp == 0 && threadIdx.x < M) info[mg0 + threadIdx.x] = make_int2(wk.base * kMT + threadIdx.x, nsp);
+
+  // tokens of this wave's step i (one per round): [t0, t0 + count), count <= 0: none
+  auto step_tok = [&](int i, int* count) -> int {
+    const int st = round0 + i;
+    const int t0 = (st < rg.s0 ? st * kNRound : rg.w0 + (st - rg.s0) * kNRound) + wave * kNTok;
+    *count = min(kNTok, (st < rg.s0 ? rg.n0 : rg.w1) - t0);
+    return t0;
+  };
+  const int32_t* trow = pg.table + (int64_t)b * pg.ld;
+  // entry and slot of the step's token c16 (past the count: its last, or token 0's)
+  auto entry_of = [&](int i, int& off) -> const int32_t* {
+    int cnt;
+    const int t0 = step_tok(i, &cnt);
+    const int t = cnt > 0 ? t0 + min(c16, cnt - 1) : 0;
+    const uint32_t idx = page_index(pg, t);
+    off = t - (int)idx * pg.size;
+    return trow + idx;
+  };
+  auto slot_at = [&](int i, int page, int off) -> int {
+    int cnt;
+    step_tok(i, &cnt);
+    const int sl = slot_in(pg, page, off);
+    return c16 < cnt ? sl : -1;
+  };
+  uint8_t* const mine = tiles + wave * 2 * kNTile;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(mine)));
+  const uint32_t page0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(&s_page[wave][0][0])));
+  auto issue_pages = [&](int i) {
+    int off;
+    const int32_t* e = entry_of(min(i, rounds - 1), off);
+    const uint32_t lds = page0 + (i & 1) * 256u;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(e) : "memory", "m0");
+  };
+  auto issue = [&](int slot, int buf) {
+    const uint32_t base = lds0 + static_cast<uint32_t>(buf * kNTile), voff = lane * 16;
+#pragma unroll
+    for (int j = 0; j < kNTok; ++j) {
+      const int sl = max(__builtin_amdgcn_readlane(slot, j), 0);
+      const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2);
+      const uint32_t lds = base + static_cast<uint32_t>(j * kVPitch);
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src)
+                   : "memory", "m0");
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = lane >> 3;
+      const int sl = max(__shfl(slot, j * 8 + k, 64), 0);
+      const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16);
+      const uint32_t lds = base + static_cast<uint32_t>(kNTail + j * 1024);
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+    }
+  };
+  // key fragment s (32 values) of token c16: its piece 4 s + grp
+  auto kload = [&](const uint8_t* buf, int s) -> bf16x8_t {
+    return s < 16 ? ld_bf16x8(buf + c16 * kVPitch + s * 64 + grp * 16)
+                  : ld_bf16x8(buf + kNTail + c16 * 128 + (((4 * (s - 16) + grp) ^ (c16 & 7)) * 16));
+  };
+  // value fragment (V^T) of column tile ct: tokens 8 g .. +7
+  const uint32_t v_off = (8 * g + (c16 >> 2)) * kVPitch + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
+  auto vload = [&](const uint8_t* buf, int ct) -> bf16x8_t {
+    const uint8_t* v = buf + v_off + ct * 64;
+    return ld_tr8(v, v + 4 * kVPitch);
+  };
+
+  f32x16_t acc[16];   // [column tile]: O^T[col][query col]
+  float mx[2] = {-__builtin_inff(), -__builtin_inff()}, l[2] = {0.f, 0.f};   // of queries c16, 16 + c16
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[c][v] = 0.f;
+
+  if (rounds > 0) {
+    int p_row[2];
+    bf16x8_t qf[2][kNKs];
+    int slot;
+    uint32_t ok;
+    bool any_before = false;           // the accumulators hold something
+    {
+      int off0;
+      const int page = *entry_of(0, off0);
+      slot = slot_at(0, page, off0);
+      issue_pages(1);
+      issue(slot, 0);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int m = min(16 * h + c16, M - 1), mr = m / H, mh = m - mr * H;   // past the end: the last one again
+      p_row[h] = sr.pos0 + mr;
+      const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + grp * 16;
+#pragma unroll
+      for (int s = 0; s < kNKs; ++s) qf[h][s] = ld_bf16x8(qp + s * 64);
+    }
+    __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): step 0, the entries of step 1, the queries
+    for (int i = 0; i < rounds; ++i) {
+      const uint8_t* buf = mine + (i & 1) * kNTile;
+      int cnt;
+      const int t0 = step_tok(i, &cnt);
+      ok = (uint32_t)__ballot(slot >= 0) & 0xffffu;
+      // step i + 1 starts loading (its buffer's step is done), its entries are in
+      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00 | (kNLoads & 15) | ((kNLoads >> 4) << 14));
+      asm volatile("" ::: "memory");
+      {
+        int off;
+        const int j = min(i + 1, rounds - 1);
+        entry_of(j, off);
+        const int sl = slot_at(j, s_page[wave][(i + 1) & 1][lane], off);
+        slot = i + 1 < rounds ? sl : -1;
+      }
+      issue_pages(i + 2);
+      issue(slot, (i + 1) & 1);
+      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00 | ((kNLoads + 1) & 15) | (((kNLoads + 1) >> 4) << 14));   // step i is in
+      asm volatile("" ::: "memory");
+      if (cnt <= 0) continue;
+
+      f32x4_t st[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+      bf16x8_t kb[kNKD];
+#pragma unroll
+      for (int s = 0; s < kNKD; ++s) kb[s] = kload(buf, s);
+#pragma unroll
+      for (int s = 0; s < kNKs; ++s) {
+        st[0] = mfma16(kb[s % kNKD], qf[0][s], st[0]);
+        st[1] = mfma16(kb[s % kNKD], qf[1][s], st[1]);
+        if (s + kNKD < kNKs) kb[s % kNKD] = kload(buf, s + kNKD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      bf16x8_t vf[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) vf[c] = vload(buf, c);
+      const bool full = ok == 0xffffu && t0 + kNTok - 1 <= sr.pos0 &&
+                        (window == 0 || t0 > sr.pos0 + sr.n - 1 - window || t0 + kNTok <= n_sink);
+      bool poison = false;
+      float alpha[2];
+      uint32_t pk[2][2];
+      bool grown = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t bits = full ? 0xffffu : (sees_bits(p_row[h], t0, window, n_sink) & ok);
+        float x[4], tmax = -__builtin_inff();
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float sc = st[h][v] * scale2;
+          const bool seen = (bits >> (4 * grp + v)) & 1;
+          poison |= !seen && !(fabsf(sc) < __builtin_inff());
+          x[v] = seen ? sc : -__builtin_inff();
+          tmax = fmaxf(tmax, x[v]);
+        }
+        tmax = quad_max(tmax);
+        const bool grow = __any(tmax > mx[h] + 8.f);   // as in the 128-query kernel
+        const float mn = grow ? fmaxf(mx[h], tmax) : mx[h];
+        const float ref = mn == -__builtin_inff() ? 0.f : mn;
+        alpha[h] = grow ? __builtin_amdgcn_exp2f(mx[h] - ref) : 1.f;
+        grown |= grow;
+        float psum = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          x[v] = __builtin_amdgcn_exp2f(x[v] - ref);
+          psum += x[v];
+        }
+        typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
+        const bf16x4_t pb = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        const uint2 u = __builtin_bit_cast(uint2, pb);
+        pk[h][0] = u.x;
+        pk[h][1] = u.y;
+        l[h] = l[h] * alpha[h] + psum;
+        mx[h] = mn;
+      }
+      // Lane group r holds tokens 4 r .. +3 of queries c16 and 16 + c16; after
+      // the swaps lane l holds tokens 8 g .. +7 of query l % 32.
+      const auto s01 = __builtin_amdgcn_permlane16_swap(pk[0][0], pk[1][0], false, false);
+      const auto s23 = __builtin_amdgcn_permlane16_swap(pk[0][1], pk[1][1], false, false);
+      const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, u32x4_t{s01[0], s23[0], s01[1], s23[1]});
+      if (grown && any_before) {
+        mfma32_acc_done();
+        const float a = (lane & 16) ? alpha[1] : alpha[0];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          asm volatile("" : "+a"(acc[c]));   // one accumulator at a time leaves its registers
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[c][v] *= a;
+          asm volatile("" : "+a"(acc[c]));
+        }
+        asm volatile("s_nop 7");
+      }
+      if (__any(poison)) {
+        // as in the 128-query kernel: values that are not finite become 0
+        uint8_t* wbuf = mine + (i & 1) * kNTile;
+        for (int y = lane; y < kNTok * 64; y += 64) {
+          uint16_t* e = reinterpret_cast<uint16_t*>(wbuf + (y >> 6) * kVPitch + (y & 63) * 16);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < 4; ++c) vf[c] = vload(buf, c);
+      }
+      any_before = true;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        mfma32_acc(acc[c], vf[c & 3], pf);
+        if (c + 4 < 16) vf[c & 3] = vload(buf, c + 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // no load is under way when the buffers change hands
+  mfma32_acc_done();
+
+  // the four waves' states: query l % 32 of every lane
+  {
+    const float l0 = quad_sum(l[0]), l1 = quad_sum(l[1]);
+    const bool hi = (lane & 16) != 0;
+    if (lane < kNM) s_ml[wave][lane] = make_float2(hi ? mx[1] : mx[0], hi ? l1 : l0);
+  }
+  __syncthreads();
+  float top = -__builtin_inff(), den = 0.f, f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w][col].x);
+  const float ref = top == -__builtin_inff() ? 0.f : top;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float2 ml = s_ml[w][col];
+    den += ml.y == 0.f ? 0.f : exp2f(ml.x - ref) * ml.y;   // a wave that saw nothing: (-inf, 0)
+  }
+  f = s_ml[wave][col].y == 0.f ? 0.f : exp2f(s_ml[wave][col].x - ref);
+  // wave w ends up with value columns 128 w .. +127 of all waves: two quarters
+  // cross at a time (128 KiB of the buffers)
+  f32x16_t res[4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int quarter = half * 2 + u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f32x16_t x = acc[quarter * 4 + c];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) x[v] *= f;
+        if (wave == quarter) {
+          res[c] = x;
+        } else {
+          f32x4_t* to = reinterpret_cast<f32x4_t*>(tiles + ((wave * 2 + u) * 4 + c) * 4096 + lane * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) to[j * 64] = f32x4_t{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+        }
+      }
+    }
+    __syncthreads();
+    if ((wave >> 1) == half) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {   // the others in ring order
+          const f32x4_t* from =
+              reinterpret_cast<const f32x4_t*>(tiles + ((((wave + w) & 3) * 2 + (wave & 1)) * 4 + c) * 4096 + lane * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4_t x = from[j * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) res[c][4 * j + e] += x[e];
+          }
+        }
+    }
+    __syncthreads();
+  }
+  if (col >= M) return;
+  if (nsp == 1) {
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    if (lse && wave == 0 && g == 0)
+      lse[mg0 + col] = den == 0.f ? -__builtin_inff() : (top + log2f(den)) * 0.69314718055994531f;
+    uint16_t* o = out + (mg0 + col) * kPagedVal + wave * 128 + 4 * g;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
+        bf16x4_t x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = (__bf16)(res[c][4 * j + e] * inv);
+        *reinterpret_cast<uint2*>(o + c * 32 + 8 * j) = __builtin_bit_cast(uint2, x);
+      }
+    return;
+  }
+  if (wave == 0 && g == 0) part_ml[(int64_t)blockIdx.x * rows_per + col] = make_float2(top, den);
+  float* o = part_o + ((int64_t)blockIdx.x * rows_per + col) * kPagedVal + wave * 128 + 4 * g;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<f32x4_t*>(o + c * 32 + 8 * j) =
+          f32x4_t{res[c][4 * j], res[c][4 * j + 1], res[c][4 * j + 2], res[c][4 * j + 3]};
+}
+
 // out and lse of every query that took several spans, from their partials in
 // span order. grid (T H), 128 threads: four value columns each; the spans'
 // loads go out kG at a time before the first is waited for.
@@ -654,13 +1017,14 @@ __global__ void __launch_bounds__(128)
 }
 
 // Upper bound of the batch's tiles: every sequence rounds up once.
-int64_t tiles_of(int B, int T, int H, int max_rows) {
-  const int64_t per_seq = ((int64_t)std::min(max_rows, T) * H + kMT - 1) / kMT;
-  return std::min<int64_t>(B * per_seq, (int64_t)T * H / kMT + B);
+int64_t tiles_of(int B, int T, int H, int max_rows, int per) {
+  const int64_t per_seq = ((int64_t)std::min(max_rows, T) * H + per - 1) / per;
+  return std::min<int64_t>(B * per_seq, (int64_t)T * H / per + B);
 }
 
 // Whether tiles are split over spans, and what the workspace holds then.
 struct Split {
+  bool narrow;        // at most 32 queries a sequence
   bool planned;
   int64_t tiles;
   int rows_per;       // queries a partial holds
@@ -668,12 +1032,14 @@ struct Split {
 };
 Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
   Split sp{};
-  sp.tiles = tiles_of(B, T, H, max_rows);
+  sp.narrow = (int64_t)std::min(max_rows, T) * H <= kNM;
+  const int per = sp.narrow ? kNM : kMT;
+  sp.tiles = tiles_of(B, T, H, max_rows, per);
   int64_t seen = max_len;                                  // tokens a tile can read
   if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1 + kStepTok);
   sp.planned = sp.tiles <= kCus && B <= kPlanSeqs && seen > kMinSpan * kStepTok;
   if (!sp.planned) return sp;
-  sp.rows_per = (int)std::min<int64_t>(kMT, (int64_t)std::min(max_rows, T) * H);
+  sp.rows_per = (int)std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H);
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   sp.part_ml = (size_t)kCus * sp.rows_per * kPagedVal * sizeof(float);
   sp.info = sp.part_ml + up((size_t)kCus * sp.rows_per * sizeof(float2));
@@ -716,7 +1082,7 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   float2* part_ml = sp.planned ? reinterpret_cast<float2*>(w + sp.part_ml) : nullptr;
   int2* info = sp.planned ? reinterpret_cast<int2*>(w + sp.info) : nullptr;
   const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
-  hipLaunchKernelGGL(paged_attn_kernel, dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
+  hipLaunchKernelGGL((sp.narrow ? paged_attn_narrow_kernel : paged_attn_kernel), dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
                      static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg,
                      row0, seq_len, B, T, H, max_rows, max_len, window, n_sink, sm_scale * 1.4426950408889634f,
                      (int)sp.planned, sp.rows_per, static_cast<uint16_t*>(out), lse, part_o, part_ml, info);
