@@ -550,8 +550,8 @@ int ech_paged_weight(const void* q, int64_t q_row_stride, int64_t q_head_stride,
  * sequences that keep everything included. A row without a slot on either side
  * is not moved. In place, no two sequences may share a page, and no page
  * may occur twice.
- *  keep >= 1, n_sink + n_recent <= keep, acc_ld >= max_len, row_bytes a
- *  multiple of 16, pool 16-byte aligned.
+ *  keep >= 1, n_sink + n_recent <= keep, max_len <= 2^24, acc_ld >= max_len,
+ *  row_bytes a multiple of 16, pool 16-byte aligned.
  *  ws ech_paged_evict_ws_bytes(...) bytes, as for ech_paged_attn.
  */
 size_t ech_paged_evict_ws_bytes(int B, int max_len, int keep);

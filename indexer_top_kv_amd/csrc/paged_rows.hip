@@ -34,102 +34,357 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ eviction
+// A sequence of n > keep tokens keeps its first n_sink, its last n_recent, and
+// of the tokens between the `want` = keep - n_sink - n_recent with the largest
+// weights, ties to the lower index. The want-th largest key is found digit by
+// digit (11, 11 and 10 bits of an order-preserving 32-bit key) from
+// histograms; what is above it and the first `ties` of its equals stay. The
+// weights are read once (the one-workgroup form) or once per digit from L2
+// (the form for long rows); a wave owns consecutive tokens, 64 per register,
+// so ranks come from ballots.
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kBins = 2048;
+
 // Order of a weight: larger first; NaN above everything, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float x) { return x != x ? 0xffffffffu : ech::ord_key(x); }
 
-// One workgroup per sequence. A sequence of n > keep tokens keeps its first
-// n_sink, its last n_recent, and of the tokens between the `want` = keep -
-// n_sink - n_recent with the largest weights, ties to the lower index: the
-// want-th largest key is found digit by digit (four of 8 bits) from
-// histograms in LDS, then one ordered pass writes the kept tokens. acc_out may
-// be acc: a kept token's place is never behind it, and a round's weights are
-// read before any are written.
-__global__ void __launch_bounds__(1024)
-    paged_evict_select_kernel(const float* __restrict__ acc, int64_t acc_ld, const int32_t* __restrict__ seq_len,
-                              int max_len, int keep, int n_sink, int n_recent, int32_t* __restrict__ kept,
-                              float* __restrict__ acc_out, int32_t* __restrict__ len_out) {
-  __shared__ int hist[256];
-  __shared__ int scratch[16];
-  __shared__ int s_digit, s_rest;
-  const int b = blockIdx.x, tid = threadIdx.x;
+__device__ __forceinline__ int digit_shift(int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; }
+
+struct Row {
+  int n, lo, hi, want;   // tokens; those between are [lo, hi); how many of them stay (0 also where all stay)
+  bool cut;              // n > keep
+};
+__device__ __forceinline__ Row row_of(const int32_t* seq_len, int b, int max_len, int keep, int n_sink, int n_recent) {
   const int n = min(max(seq_len[b], 0), max_len);
+  const bool cut = n > keep;
+  return Row{n, cut ? n_sink : 0, cut ? n - n_recent : 0, cut ? keep - n_sink - n_recent : 0, cut};
+}
+
+// The digit d of descending bins that holds the want-th entry, and how many of
+// that bin are wanted. Thread t brings the counts of bins 2047 - 2t and 2046 -
+// 2t; out[0] = d, out[1] = rest. Call from all threads.
+__device__ __forceinline__ void find_digit(int c0, int c1, int want, int* scratch, int* out) {
+  int tot;
+  const int before = ech::block_excl_scan<kThreads>(c0 + c1, scratch, &tot);
+  const int d0 = kBins - 1 - 2 * (int)threadIdx.x;
+  if (before < want && want <= before + c0) {
+    out[0] = d0;
+    out[1] = want - before;
+  } else if (before + c0 < want && want <= before + c0 + c1) {
+    out[0] = d0 - 1;
+    out[1] = want - before - c0;
+  }
+  __syncthreads();
+}
+
+// This thread's tokens of a block of KPT * 1024 starting at t0: wave w owns
+// KPT * 64 consecutive ones, register j 64 of them.
+template <int KPT>
+__device__ __forceinline__ int token_of(int t0, int j) {
+  return t0 + (int)(threadIdx.x >> 6) * (KPT * 64) + j * 64 + (int)(threadIdx.x & 63);
+}
+
+// Ranks and writes of one block: its tokens above thr, its protected ones, and
+// its equals of thr while `ties` (less those before the block, ties0) last go
+// to places at0, at0 + 1, ... in token order.
+template <int KPT>
+__device__ __forceinline__ void write_kept(const float (&x)[KPT], const Row& r, int t0, uint32_t thr, int ties, int ties0,
+                                           int at0, int keep, int32_t* kb, float* ao, int (*s_cnt)[2]) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int gt = 0, eq = 0;
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t = token_of<KPT>(t0, j);
+    const bool mid = r.cut && t >= r.lo && t < r.hi;
+    const uint32_t k = weight_key(x[j]);
+    gt += (int)__popcll(__ballot(t < r.n && (!mid || k > thr)));
+    eq += (int)__popcll(__ballot(t < r.n && mid && k == thr));
+  }
+  if (lane == 0) {
+    s_cnt[wave][0] = gt;
+    s_cnt[wave][1] = eq;
+  }
+  __syncthreads();
+  int at = at0, seen = ties0;
+  for (int w = 0; w < wave; ++w) {
+    at += s_cnt[w][0] + min(max(ties - seen, 0), s_cnt[w][1]);
+    seen += s_cnt[w][1];
+  }
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t = token_of<KPT>(t0, j);
+    const bool mid = r.cut && t >= r.lo && t < r.hi;
+    const uint32_t k = weight_key(x[j]);
+    const bool tie = t < r.n && mid && k == thr;
+    const unsigned long long below = (1ull << lane) - 1ull, tm = __ballot(tie);
+    const bool take = (t < r.n && (!mid || k > thr)) || (tie && seen + (int)__popcll(tm & below) < ties);
+    const unsigned long long m = __ballot(take);
+    const int place = at + (int)__popcll(m & below);
+    if (take && place < keep) {
+      kb[place] = t;
+      if (ao) ao[place] = x[j];
+    }
+    at += (int)__popcll(m);
+    seen += (int)__popcll(tm);
+  }
+}
+
+// Rows of at most KPT * 1024 tokens: one workgroup per sequence, its weights in
+// registers from the first read on, so acc_out may be acc and len_out seq_len.
+// 32 sequences of 8K-16K tokens (KPT 16) 12 us; the form for long rows 22 us.
+template <int KPT>
+__global__ void __launch_bounds__(kThreads)
+    paged_evict_row_kernel(const float* acc, int64_t acc_ld, const int32_t* seq_len, int max_len, int keep, int n_sink,
+                           int n_recent, int32_t* __restrict__ kept, float* acc_out, int32_t* len_out) {
+  __shared__ int hist[kBins];
+  __shared__ int scratch[kWaves], s_found[2];
+  __shared__ int s_cnt[kWaves][2];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
   const float* a = acc + (int64_t)b * acc_ld;
+  float x[KPT];
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t = token_of<KPT>(0, j);
+    x[j] = t < r.n ? a[t] : 0.f;
+  }
+  uint32_t thr = 0xffffffffu;
+  int ties = 0;
+  if (r.want > 0) {
+    int want = r.want;
+    uint32_t prefix = 0;
+    for (int level = 0; level < 3; ++level) {
+      const int shift = digit_shift(level), width = level == 2 ? 10 : 11;
+      hist[tid] = 0;
+      hist[tid + kThreads] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < KPT; ++j) {
+        const int t = token_of<KPT>(0, j);
+        const uint32_t k = weight_key(x[j]);
+        if (t >= r.lo && t < r.hi && (level == 0 || (k >> (shift + width)) == prefix))
+          atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
+      }
+      __syncthreads();
+      find_digit(hist[kBins - 1 - 2 * tid], hist[kBins - 2 - 2 * tid], want, scratch, s_found);
+      prefix = (prefix << width) | (uint32_t)s_found[0];
+      want = s_found[1];
+      __syncthreads();
+    }
+    thr = prefix;
+    ties = want;
+  }
+  const int nk = min(r.n, keep);
   int32_t* kb = kept + (int64_t)b * keep;
   float* ao = acc_out ? acc_out + (int64_t)b * acc_ld : nullptr;
-  const int nk = min(n, keep);
-  uint32_t thr = 0;        // tokens between with a key above thr stay,
-  int ties = 0;            // and the first `ties` of those equal to it
-  const int lo = n_sink, hi = n - n_recent;
-  if (n > keep) {
-    int want = keep - n_sink - n_recent;
-    uint32_t prefix = 0;
-    if (want == 0) {
-      thr = 0xffffffffu;
-    } else {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int t = lo + tid; t < hi; t += 1024) {
-          const uint32_t k = weight_key(a[t]);
-          if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (tid == 0) {
-          int rest = want, d = 255;
-          while (d > 0 && hist[d] < rest) rest -= hist[d--];
-          s_digit = d;
-          s_rest = rest;
-        }
-        __syncthreads();
-        prefix = (prefix << 8) | (uint32_t)s_digit;
-        want = s_rest;
-        __syncthreads();
-      }
-      thr = prefix;
-      ties = want;
-    }
-  }
-  int out = 0, seen = 0;   // kept so far, ties seen so far
-  for (int t0 = 0; t0 < n; t0 += 1024) {
-    const int t = t0 + tid;
-    const float x = t < n ? a[t] : 0.f;
-    bool take = t < n, tie = false;
-    if (n > keep && t < n && t >= lo && t < hi) {
-      const uint32_t k = weight_key(x);
-      take = k > thr;
-      tie = k == thr;
-    }
-    int tot;
-    const int rank = ech::block_excl_scan<1024>(tie ? 1 : 0, scratch, &tot);
-    take = take || (tie && seen + rank < ties);
-    seen += tot;
-    const int at = out + ech::block_excl_scan<1024>(take ? 1 : 0, scratch, &tot);
-    out += tot;
-    if (take && at < keep) {
-      kb[at] = t;
-      if (ao) ao[at] = x;
-    }
-  }
-  for (int j = nk + tid; j < keep; j += 1024) kb[j] = -1;
-  __syncthreads();
+  write_kept<KPT>(x, r, 0, thr, ties, 0, 0, keep, kb, ao, s_cnt);
+  for (int j = nk + tid; j < keep; j += kThreads) kb[j] = -1;
   if (ao)
-    for (int j = nk + tid; j < max_len; j += 1024) ao[j] = 0.f;
+    for (int j = nk + tid; j < max_len; j += kThreads) ao[j] = 0.f;
   if (tid == 0) len_out[b] = nk;
 }
 
-// Rows of kept tokens to the pages of another table. grid (ceil(keep / 4), B),
-// one wave per row.
+// Longer rows: blocks of 8192 tokens, a launch per digit and one that writes.
+// ws per sequence: what is found so far {digit 0, rest, digit 1, rest}, and per
+// block its counts above the digits found so far, then every block's histogram
+// of each level. Nothing needs to start at zero.
+constexpr int kBlockKpt = 8, kBlock = kBlockKpt * kThreads;
+struct LongWs {
+  int32_t* found;   // [B][4]
+  int32_t* above;   // [B][2][blocks]
+  int32_t* hist;    // [3][B][blocks][kBins]
+  float* weight;    // [B][keep]: the kept weights, where acc_out is acc
+  int blocks, B;
+};
+__device__ __forceinline__ int32_t* hist_of(const LongWs& w, int level, int b, int blk) {
+  return w.hist + (((int64_t)level * w.B + b) * w.blocks + blk) * kBins;
+}
+// The sequence's digit of `level` from its blocks' histograms; thread t also
+// gets, in before[0..1], what blocks before `blk` hold in its two bins.
+__device__ __forceinline__ void find_in_blocks(const LongWs& w, int level, int b, int blk, int n_blk, int want,
+                                               int* scratch, int* found, int (&before)[2]) {
+  const int32_t* h = hist_of(w, level, b, 0) + (kBins - 2 - 2 * (int)threadIdx.x);
+  int c0 = 0, c1 = 0;
+  before[0] = before[1] = 0;
+  constexpr int kAhead = 8;          // blocks whose loads are under way together
+  for (int i0 = 0; i0 < n_blk; i0 += kAhead) {
+    int2 v[kAhead];                  // bins 2046 - 2t, 2047 - 2t
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) v[u] = *reinterpret_cast<const int2*>(h + (int64_t)min(i0 + u, n_blk - 1) * kBins);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      c0 += i < n_blk ? v[u].y : 0;
+      c1 += i < n_blk ? v[u].x : 0;
+      before[0] += i < blk ? v[u].y : 0;
+      before[1] += i < blk ? v[u].x : 0;
+    }
+  }
+  find_digit(c0, c1, want, scratch, found);
+}
+
+template <int LEVEL>
+__global__ void __launch_bounds__(kThreads)
+    paged_evict_digit_kernel(const float* __restrict__ acc, int64_t acc_ld, const int32_t* __restrict__ seq_len,
+                             int max_len, int keep, int n_sink, int n_recent, LongWs w) {
+  __shared__ int hist[kBins];
+  __shared__ int scratch[kWaves], s_found[2];
+  const int b = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x, t0 = blk * kBlock;
+  const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
+  if (r.want == 0 || t0 >= r.n) return;
+  const int n_blk = (r.n + kBlock - 1) / kBlock;
+  const float* a = acc + (int64_t)b * acc_ld;
+  float x[kBlockKpt];
+#pragma unroll
+  for (int j = 0; j < kBlockKpt; ++j) {
+    const int t = token_of<kBlockKpt>(t0, j);
+    x[j] = t < r.n ? a[t] : 0.f;
+  }
+  hist[tid] = 0;
+  hist[tid + kThreads] = 0;
+  uint32_t prefix = 0;
+  if (LEVEL > 0) {
+    int want = r.want, before[2];
+    if (LEVEL > 1) {
+      prefix = (uint32_t)w.found[b * 4];
+      want = w.found[b * 4 + 1];
+    }
+    find_in_blocks(w, LEVEL - 1, b, blk, n_blk, want, scratch, s_found, before);
+    if (blk == 0 && tid < 2) w.found[b * 4 + (LEVEL - 1) * 2 + tid] = s_found[tid];
+    // this block's tokens above the digit just found, among those equal before it
+    int above = 0;
+    constexpr int up = LEVEL == 1 ? 21 : 10;
+#pragma unroll
+    for (int j = 0; j < kBlockKpt; ++j) {
+      const int t = token_of<kBlockKpt>(t0, j);
+      const uint32_t k = weight_key(x[j]) >> up;
+      above += t >= r.lo && t < r.hi && (LEVEL == 1 || (k >> 11) == prefix) && (k & (kBins - 1)) > (uint32_t)s_found[0];
+    }
+    above = ech::block_sum<kThreads>(above, scratch);
+    if (tid == 0) w.above[((int64_t)b * 2 + LEVEL - 1) * w.blocks + blk] = above;
+    prefix = (prefix << 11) | (uint32_t)s_found[0];
+  }
+  __syncthreads();
+  constexpr int shift = LEVEL == 0 ? 21 : LEVEL == 1 ? 10 : 0, width = LEVEL == 2 ? 10 : 11;
+#pragma unroll
+  for (int j = 0; j < kBlockKpt; ++j) {
+    const int t = token_of<kBlockKpt>(t0, j);
+    const uint32_t k = weight_key(x[j]);
+    if (t >= r.lo && t < r.hi && (LEVEL == 0 || (k >> ((shift + width) & 31)) == prefix))
+      atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
+  }
+  __syncthreads();
+  int32_t* h = hist_of(w, LEVEL, b, blk);
+  h[tid] = hist[tid];
+  h[tid + kThreads] = hist[tid + kThreads];
+}
+
+__global__ void __launch_bounds__(kThreads)
+    paged_evict_pick_kernel(const float* __restrict__ acc, int64_t acc_ld, const int32_t* __restrict__ seq_len,
+                            int max_len, int keep, int n_sink, int n_recent, int32_t* __restrict__ kept,
+                            float* __restrict__ weight, int64_t weight_ld, int ends, int32_t* __restrict__ len_out,
+                            LongWs w) {
+  __shared__ int scratch[kWaves], s_found[2];
+  __shared__ int s_cnt[kWaves][2], s_tie0;
+  const int b = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x, t0 = blk * kBlock;
+  const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
+  int32_t* kb = kept + (int64_t)b * keep;
+  const int nk = min(r.n, keep);
+  for (int j = max(nk, t0) + tid; j < min(keep, t0 + kBlock); j += kThreads) kb[j] = -1;
+  if (ends) {   // the outputs are not the inputs: what follows the kept weights, and the length
+    if (weight)
+      for (int j = max(nk, t0) + tid; j < min(max_len, t0 + kBlock); j += kThreads) weight[(int64_t)b * weight_ld + j] = 0.f;
+    if (blk == 0 && tid == 0) len_out[b] = nk;
+  }
+  if (t0 >= r.n) return;
+  const float* a = acc + (int64_t)b * acc_ld;
+  float x[kBlockKpt];
+#pragma unroll
+  for (int j = 0; j < kBlockKpt; ++j) {
+    const int t = token_of<kBlockKpt>(t0, j);
+    x[j] = t < r.n ? a[t] : 0.f;
+  }
+  uint32_t thr = 0xffffffffu;
+  int ties = 0, ties0 = 0, at0 = t0;
+  if (r.cut) at0 = min(t0, r.lo) + max(0, t0 - r.hi);       // protected tokens before the block
+  if (r.want > 0) {
+    const int n_blk = (r.n + kBlock - 1) / kBlock;
+    int before[2];
+    const int d0 = w.found[b * 4], d1 = w.found[b * 4 + 2], want = w.found[b * 4 + 3];
+    find_in_blocks(w, 2, b, blk, n_blk, want, scratch, s_found, before);
+    const int d2 = s_found[0], bin0 = kBins - 1 - 2 * tid;
+    thr = ((uint32_t)d0 << 21) | ((uint32_t)d1 << 10) | (uint32_t)d2;
+    ties = s_found[1];
+    if (bin0 == d2) s_tie0 = before[0];
+    if (bin0 - 1 == d2) s_tie0 = before[1];
+    int above = (bin0 > d2 ? before[0] : 0) + (bin0 - 1 > d2 ? before[1] : 0);
+    for (int i = tid; i < blk; i += kThreads)
+      above += w.above[(int64_t)b * 2 * w.blocks + i] + w.above[((int64_t)b * 2 + 1) * w.blocks + i];
+    above = ech::block_sum<kThreads>(above, scratch);       // its barriers publish s_tie0
+    ties0 = s_tie0;
+    at0 += above + min(ties, ties0);
+  }
+  write_kept<kBlockKpt>(x, r, t0, thr, ties, ties0, at0, keep, kb, weight ? weight + (int64_t)b * weight_ld : nullptr,
+                        s_cnt);
+}
+
+// What has to wait until every block has read acc and seq_len, where an output
+// is one of them: the weights (if acc_out is acc), the zeros behind them, the
+// lengths. grid (blocks, B).
+__global__ void __launch_bounds__(kThreads)
+    paged_evict_end_kernel(const int32_t* __restrict__ seq_len, int max_len, int keep, float* __restrict__ acc_out,
+                           int64_t acc_ld, const float* __restrict__ weight, int64_t weight_ld) {
+  const int b = blockIdx.y, nk = min(min(max(seq_len[b], 0), max_len), keep);
+  float* ao = acc_out + (int64_t)b * acc_ld;
+  for (int j = blockIdx.x * kThreads + threadIdx.x; j < max_len; j += gridDim.x * kThreads) {
+    if (j >= nk) ao[j] = 0.f;
+    else if (weight) ao[j] = weight[b * weight_ld + j];
+  }
+}
 __global__ void __launch_bounds__(256)
-    paged_move_kernel(uint4* __restrict__ pool, int row16, Pages src, Pages dst, const int32_t* __restrict__ kept,
+    paged_evict_len_kernel(const int32_t* seq_len, int B, int max_len, int keep, int32_t* len_out) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b < B) len_out[b] = min(min(max(seq_len[b], 0), max_len), keep);
+}
+
+// Rows of kept tokens to the pages of another table. grid (ceil(keep / 64),
+// B), 256 threads: 64 rows' slots, then their 16-byte pieces, kMovePieces of a
+// thread's loads under way at a time. ROW16: pieces per row (0: row16).
+constexpr int kMoveRows = 64, kMovePieces = 6;
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+template <int ROW16>
+__global__ void __launch_bounds__(256)
+    paged_move_kernel(u32x4_t* __restrict__ pool, int row16, Pages src, Pages dst, const int32_t* __restrict__ kept,
                       int keep) {
-  const int j = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63, b = blockIdx.y;
-  if (j >= keep) return;
-  const int t = kept[(int64_t)b * keep + j];
-  if (t < 0) return;
-  const int s = slot_of(src, src.table + (int64_t)b * src.ld, t);
-  const int d = slot_of(dst, dst.table + (int64_t)b * dst.ld, j);
-  if (s < 0 || d < 0) return;
-  for (int i = lane; i < row16; i += 64) pool[(int64_t)d * row16 + i] = pool[(int64_t)s * row16 + i];
+  __shared__ int s_src[kMoveRows], s_dst[kMoveRows];
+  const int b = blockIdx.y, j0 = blockIdx.x * kMoveRows, n16 = ROW16 ? ROW16 : row16;
+  if (threadIdx.x < kMoveRows) {
+    const int j = j0 + threadIdx.x, t = j < keep ? kept[(int64_t)b * keep + j] : -1;
+    int s = -1, d = -1;
+    if (t >= 0) {
+      s = slot_of(src, src.table + (int64_t)b * src.ld, t);
+      d = slot_of(dst, dst.table + (int64_t)b * dst.ld, j);
+    }
+    s_src[threadIdx.x] = d < 0 ? -1 : s;
+    s_dst[threadIdx.x] = d;
+  }
+  __syncthreads();
+  const int total = kMoveRows * n16;
+  for (int p0 = threadIdx.x; p0 < total; p0 += 256 * kMovePieces) {
+    u32x4_t v[kMovePieces];
+    int64_t to[kMovePieces];
+#pragma unroll
+    for (int u = 0; u < kMovePieces; ++u) {
+      // rows that do not move read slot 0, so that every load goes out at once
+      const int p = min(p0 + u * 256, total - 1), rw = p / n16, c = p - rw * n16;
+      const int s = s_src[rw];
+      to[u] = s < 0 || p0 + u * 256 >= total ? -1 : (int64_t)s_dst[rw] * n16 + c;
+      v[u] = pool[(int64_t)max(s, 0) * n16 + c];
+    }
+#pragma unroll
+    for (int u = 0; u < kMovePieces; ++u)
+      if (to[u] >= 0) pool[to[u]] = v[u];
+  }
 }
 
 // The same within one table. A kept token's place is never behind it, so
@@ -175,11 +430,39 @@ extern "C" int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, 
   return ECH_OK;
 }
 
+// Rows of at most 16384 tokens are one workgroup's work.
+constexpr int kRowMost = 16 * kThreads;
+
+static LongWs long_ws(char* ws, int B, int max_len, int keep, size_t* bytes) {
+  LongWs w{};
+  if (max_len <= kRowMost) {
+    *bytes = 0;
+    return w;
+  }
+  auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  w.B = B;
+  w.blocks = (max_len + kBlock - 1) / kBlock;
+  const size_t above = up((size_t)B * 4 * 4), hist = above + up((size_t)B * 2 * w.blocks * 4),
+               weight = hist + (size_t)3 * B * w.blocks * kBins * 4;
+  if (ws) {
+    w.found = reinterpret_cast<int32_t*>(ws);
+    w.above = reinterpret_cast<int32_t*>(ws + above);
+    w.hist = reinterpret_cast<int32_t*>(ws + hist);
+    w.weight = reinterpret_cast<float*>(ws + weight);
+  }
+  *bytes = weight + up((size_t)B * std::min(keep, max_len) * 4);
+  return w;
+}
+
+static bool evict_shape_ok(int B, int max_len, int keep) {
+  return B >= 1 && B <= 65535 && max_len >= 0 && max_len <= (1 << 24) && keep >= 1 && keep <= (1 << 30);
+}
+
 extern "C" size_t ech_paged_evict_ws_bytes(int B, int max_len, int keep) {
-  (void)B;
-  (void)max_len;
-  (void)keep;
-  return 0;
+  if (!evict_shape_ok(B, max_len, keep)) return 0;
+  size_t n;
+  (void)long_ws(nullptr, B, max_len, keep, &n);
+  return n;
 }
 
 extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* seq_len, int B, int max_len, int keep,
@@ -187,8 +470,8 @@ extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* 
                                int64_t n_slots, int64_t row_bytes, int page_size, const int32_t* src_table,
                                const int32_t* dst_table, int64_t pt_ld, void* ws, size_t ws_bytes, void* stream) {
   if (!acc || !seq_len || !kept || !len_out) return ECH_EINVAL;
-  if (B < 1 || B > 65535 || max_len < 0 || max_len > (1 << 30) || acc_ld < max_len || keep < 1 || keep > (1 << 30) ||
-      n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > keep)
+  if (!evict_shape_ok(B, max_len, keep) || acc_ld < max_len || n_sink < 0 || n_recent < 0 ||
+      (int64_t)n_sink + n_recent > keep)
     return ECH_EINVAL;
   if (pool) {
     if (!dst_table || !pages_ok(n_slots, page_size, src_table, pt_ld) || row_bytes < 16 || row_bytes % 16 ||
@@ -198,18 +481,56 @@ extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* 
   const size_t need = ech_paged_evict_ws_bytes(B, max_len, keep);
   if (ws_bytes < need || (need && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)))) return ECH_EINVAL;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(paged_evict_select_kernel, dim3(B), dim3(1024), 0, s, acc, acc_ld, seq_len, max_len, keep, n_sink,
-                     n_recent, kept, acc_out, len_out);
+#define ECH_EVICT_ROW(K)                                                                                             \
+  hipLaunchKernelGGL(paged_evict_row_kernel<K>, dim3(B), dim3(kThreads), 0, s, acc, acc_ld, seq_len, max_len, keep, \
+                     n_sink, n_recent, kept, acc_out, len_out)
+  if (max_len <= 4 * kThreads) {
+    ECH_EVICT_ROW(4);
+  } else if (max_len <= kRowMost) {
+    ECH_EVICT_ROW(16);
+  } else {
+    size_t n;
+    const LongWs w = long_ws(static_cast<char*>(ws), B, max_len, keep, &n);
+    const dim3 grid(w.blocks, B), block(kThreads);
+    hipLaunchKernelGGL(paged_evict_digit_kernel<0>, grid, block, 0, s, acc, acc_ld, seq_len, max_len, keep, n_sink,
+                       n_recent, w);
+    hipLaunchKernelGGL(paged_evict_digit_kernel<1>, grid, block, 0, s, acc, acc_ld, seq_len, max_len, keep, n_sink,
+                       n_recent, w);
+    hipLaunchKernelGGL(paged_evict_digit_kernel<2>, grid, block, 0, s, acc, acc_ld, seq_len, max_len, keep, n_sink,
+                       n_recent, w);
+    ECH_LAUNCH_CHECK();
+    const bool same = acc_out == acc || len_out == seq_len, tmp = acc_out == acc;
+    const int64_t tmp_ld = std::min(keep, max_len);
+    // the blocks past max_len mark unused places where keep is larger
+    const dim3 pgrid((std::max(keep, max_len) + kBlock - 1) / kBlock, B);
+    hipLaunchKernelGGL(paged_evict_pick_kernel, pgrid, block, 0, s, acc, acc_ld, seq_len, max_len, keep, n_sink, n_recent,
+                       kept, tmp ? w.weight : acc_out, tmp ? tmp_ld : acc_ld, (int)!same, len_out, w);
+    ECH_LAUNCH_CHECK();
+    if (same) {
+      if (acc_out) {
+        hipLaunchKernelGGL(paged_evict_end_kernel, grid, block, 0, s, seq_len, max_len, keep, acc_out, acc_ld,
+                           tmp ? w.weight : nullptr, tmp_ld);
+        ECH_LAUNCH_CHECK();
+      }
+      hipLaunchKernelGGL(paged_evict_len_kernel, dim3((B + 255) / 256), dim3(256), 0, s, seq_len, B, max_len, keep,
+                         len_out);
+    }
+  }
+#undef ECH_EVICT_ROW
   ECH_LAUNCH_CHECK();
   if (!pool) return ECH_OK;
   const int row16 = (int)(row_bytes / 16);
   const Pages a = make_pages(src_table, pt_ld, n_slots, page_size), d = make_pages(dst_table, pt_ld, n_slots, page_size);
+  const dim3 mgrid((std::min(keep, max_len) + kMoveRows - 1) / kMoveRows, B);
+  if (mgrid.x == 0) return ECH_OK;
   if (src_table == dst_table)
     hipLaunchKernelGGL(paged_move_within_kernel, dim3((row16 + 3) / 4, B), dim3(1024), 0, s, static_cast<uint4*>(pool),
                        row16, a, kept, keep);
+  else if (row16 == kPagedChunks)
+    hipLaunchKernelGGL(paged_move_kernel<kPagedChunks>, mgrid, dim3(256), 0, s, static_cast<u32x4_t*>(pool), row16, a, d, kept,
+                       keep);
   else
-    hipLaunchKernelGGL(paged_move_kernel, dim3((keep + 3) / 4, B), dim3(256), 0, s, static_cast<uint4*>(pool), row16, a,
-                       d, kept, keep);
+    hipLaunchKernelGGL(paged_move_kernel<0>, mgrid, dim3(256), 0, s, static_cast<u32x4_t*>(pool), row16, a, d, kept, keep);
   ECH_LAUNCH_CHECK();
   return ECH_OK;
 }

@@ -390,13 +390,13 @@ def test_weight_in_place_absent_pages_and_nan():
 
 
 # ------------------------------------------------------------------ eviction
-def run_evict(acc, lens, keep, sink, recent, pool=None, src=None, dst=None, page=1, in_place=False):
+def run_evict(acc, lens, keep, sink, recent, pool=None, src=None, dst=None, page=1, in_place=False, len_in_place=None):
     B, L = acc.shape
     kept = torch.full((B, keep), -9, dtype=torch.int32, device='cuda')
     a = dev(acc)
     n = dev(lens)
     ao = a if in_place else torch.full_like(a, 5.0)
-    lo = n if in_place else torch.full_like(n, -3)
+    lo = n if (in_place if len_in_place is None else len_in_place) else torch.full_like(n, -3)
     nb = ech.ech_paged_evict_ws_bytes(B, L, keep)
     ws = torch.full((nb,), 0xff, dtype=torch.uint8, device='cuda') if nb else None
     ech.ech_paged_evict(a, n, L, keep, sink, recent, kept, lo, acc_out=ao, pool=pool, src_table=src, dst_table=dst,
@@ -419,7 +419,8 @@ EVICT = [
     # lens, keep, sink, recent
     ([1], 1, 0, 0), ([0, 5, 3], 4, 0, 0), ([2], 1, 1, 0), ([2], 1, 0, 1), ([100, 64, 65], 64, 4, 16),
     ([1000, 1025, 3, 700], 512, 4, 100), ([5000], 17, 0, 0), ([5000, 4999], 4000, 1000, 1500),
-    ([20011], 9001, 16, 512), ([300], 200, 100, 100), ([70000, 131], 4096, 4, 0),
+    ([20011], 9001, 16, 512), ([300], 200, 100, 100), ([70000, 131], 4096, 4, 0), ([16384, 16385], 8192, 0, 0),
+    ([4096, 4097, 1], 1, 0, 0), ([24577, 8191, 8193], 30000, 9, 9), ([24577, 8191, 8193], 8192, 8000, 100),
 ]
 
 
@@ -445,6 +446,9 @@ def test_evict_selection(lens, keep, sink, recent, kind):
     acc = acc.astype(np.float32)
     check_evict(run_evict(acc, lens, keep, sink, recent), acc, lens, keep, sink, recent)
     check_evict(run_evict(acc, lens, keep, sink, recent, in_place=True), acc, lens, keep, sink, recent)
+    if max(lens) > 16384:                  # blocks of a long row: each output in place by itself
+        check_evict(run_evict(acc, lens, keep, sink, recent, in_place=True, len_in_place=False), acc, lens, keep, sink, recent)
+        check_evict(run_evict(acc, lens, keep, sink, recent, len_in_place=True), acc, lens, keep, sink, recent)
 
 
 @pytest.mark.parametrize('page,row', [(1, 576), (16, 576), (24, 576), (100, 24)])
