@@ -1,0 +1,179 @@
+// What the matrix-core kernels over paged rows share: operand types, the step
+// layout in LDS, the ranges of tokens that a tile of queries reads, and the
+// split of tiles over the CUs.
+#pragma once
+
+#include "paged.hpp"
+
+namespace {
+
+typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8_t;
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef short v4s_t __attribute__((ext_vector_type(4)));
+typedef short v8s_t __attribute__((ext_vector_type(8)));
+
+constexpr int kStepTok = 32;                 // tokens per step
+constexpr int kKs16 = kPagedRow / 16;        // contraction steps of the scores (36)
+constexpr int kVPitch = kPagedVal * 2 + 32;  // bytes per token of the value part in LDS (two spare pieces: banks)
+constexpr int kTailAt = kStepTok * kVPitch;  // the rows' last 64 values (rotary part), 128 bytes a token
+constexpr int kTileB = kTailAt + kStepTok * 128;
+#define ECH_LDS_PTR(p) ((__attribute__((address_space(3))) void*)(p))
+
+__device__ __forceinline__ bf16x8_t ld_bf16x8(const uint8_t* p) {
+  return __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(p));
+}
+
+__device__ __forceinline__ f32x16_t mfma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Maximum / sum over the two lanes (l, l ^ 32) that share a query.
+__device__ __forceinline__ float pair_max(float x) {
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
+// Direct-to-LDS loads of 1 KiB: lane l's 16 bytes go to lds + 16 l. From inline
+// asm, so that the compiler does not wait for them before other LDS reads; they
+// write no register, and the caller waits for them by count.
+__device__ __forceinline__ void lds_load_row(uint32_t lds, uint32_t voff, const uint8_t* src) {   // src uniform
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load_lanes(uint32_t lds, const uint8_t* src) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load_dwords(uint32_t lds, const void* src) {   // 4 bytes a lane
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(const_cast<void*>(p))));
+}
+
+// The tokens a tile of queries at positions [p_lo, p_hi] reads, as up to two
+// ranges: [0, n0) and [w0, w1). Steps of STEP tokens run through the first,
+// then the second.
+struct Ranges {
+  int n0, w0, w1, s0, steps;
+};
+template <int STEP>
+__device__ __forceinline__ Ranges ranges_of(int p_lo, int p_hi, int window, int n_sink) {
+  const int end = p_hi + 1;                               // <= len
+  const int w0 = window == 0 ? 0 : max(0, p_lo - window + 1);
+  Ranges r;
+  if (window == 0 || w0 <= n_sink) {                      // one range
+    r = Ranges{0, 0, max(end, 0), 0, 0};
+  } else {
+    r = Ranges{min(n_sink, end), w0, end, 0, 0};
+  }
+  r.s0 = (r.n0 + STEP - 1) / STEP;
+  r.steps = r.s0 + (r.w1 - r.w0 + STEP - 1) / STEP;
+  return r;
+}
+
+// Bits of the tokens t0 .. t0 + 31 that a query at position p sees.
+__device__ __forceinline__ uint32_t sees_bits(int p, int t0, int window, int n_sink) {
+  const int d = p - t0;    // last visible, relative
+  uint32_t bits = d < 0 ? 0u : (d >= 31 ? 0xffffffffu : (2u << d) - 1u);
+  if (window != 0) {
+    const int lo = d - window + 1, sk = n_sink - t0;
+    const uint32_t win = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
+    const uint32_t first = sk <= 0 ? 0u : (sk >= 32 ? 0xffffffffu : (1u << sk) - 1u);
+    bits &= win | first;
+  }
+  return bits;
+}
+
+// What a workgroup does: span sp of the n_span spans of tile mt of sequence b;
+// the tile's spans are workgroups base .. base + n_span - 1.
+struct Work {
+  int b, mt, sp, n_span, base;
+};
+
+constexpr int kCus = 256;
+constexpr int kMinSpan = 4;          // steps a span is worth its start and its partial
+constexpr int kPlanSeqs = 256;       // sequences a plan covers (four per lane)
+
+__device__ __forceinline__ int wave_max(int v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v = max(v, __shfl_xor(v, d, 64));
+  return v;
+}
+
+// The batch's tiles split over the card's CUs: every tile takes ceil(steps /
+// S) spans with one S for all, the smallest for which the spans are at most as
+// many as the CUs, so that a batch of unequal lengths ends at one time.
+// (Spans of equal number per sequence instead: 32 decoded tokens at 128 heads
+// over 8K to 16K tokens 165 us, with this 153 us.) All tiles of a sequence
+// count as its last and longest. Every wave computes it alike, a sequence (of
+// each 64) per lane. ALL: one tile per sequence, over all of its tokens, new
+// rows or none.
+template <int PER, int STEP, bool ALL = false>
+__device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* seq_len, const Pages& pg, int B, int T,
+                                          int H, int max_rows, int max_len, int window, int n_sink, int wg) {
+  const int lane = ech::lane_id();
+  int nt[kPlanSeqs / 64], st[kPlanSeqs / 64];
+  int tiles = 0, total = 0, longest = 1;
+#pragma unroll
+  for (int c = 0; c < kPlanSeqs / 64; ++c) {
+    nt[c] = 0;
+    st[c] = 1;
+    if (c * 64 < B) {
+      const int b = c * 64 + lane;
+      if (b < B) {
+        const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+        nt[c] = (sr.n * H + PER - 1) / PER;
+        if (ALL) {
+          nt[c] = sr.len > 0;
+          st[c] = max(1, (sr.len + STEP - 1) / STEP);
+        } else if (nt[c] > 0)
+          st[c] = max(1, ranges_of<STEP>(sr.pos0 + (nt[c] - 1) * PER / H, sr.pos0 + sr.n - 1, window, n_sink).steps);
+      }
+      tiles += nt[c];
+      total += nt[c] * st[c];
+      if (nt[c] > 0) longest = max(longest, st[c]);
+    }
+  }
+  tiles = ech::wave_sum(tiles);
+  total = ech::wave_sum(total);
+  longest = wave_max(longest);
+  auto spans = [&](int S) -> int {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < kPlanSeqs / 64; ++c)
+      if (c * 64 < B) n += nt[c] * ((st[c] + S - 1) / S);
+    return ech::wave_sum(n);
+  };
+  int lo = max(kMinSpan * kStepTok / STEP, (total + kCus - 1) / kCus), hi = max(lo, longest);   // spans(hi) = tiles <= kCus
+  if (tiles < kCus) hi = min(hi, max(lo, total / (kCus - tiles) + 1));         // sum ceil(x) < sum x + tiles
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (spans(mid) <= kCus) hi = mid;
+    else lo = mid + 1;
+  }
+  int base = 0;
+#pragma unroll
+  for (int c = 0; c < kPlanSeqs / 64; ++c) {
+    if (c * 64 < B) {
+      const int n = (st[c] + hi - 1) / hi, mine = nt[c] * n;
+      const int incl = ech::wave_incl_scan(mine);
+      const unsigned long long past = __ballot(base + incl > wg);
+      if (past != 0ull) {
+        const int l = __builtin_ctzll(past);
+        const int first = base + __shfl(incl, l, 64) - __shfl(mine, l, 64), ns = __shfl(n, l, 64);
+        const int mt = (wg - first) / ns, at = first + mt * ns;
+        return Work{c * 64 + l, mt, wg - at, ns, at};
+      }
+      base += __shfl(incl, 63, 64);
+    }
+  }
+  return Work{-1, 0, 0, 1, 0};
+}
+
+}  // namespace
