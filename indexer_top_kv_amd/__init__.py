@@ -267,60 +267,57 @@ def ech_kv_append(host_pool, kcache, kscale, state: LayerState, seq_tok0, seq_le
 _BITS16 = (torch.int16, torch.uint16, torch.bfloat16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, '_cuda_getCurrentRawStream') else None
 
 
-def _arg(name: str, t: torch.Tensor, dtypes, shape, device: torch.device, inner: int = 0) -> None:
+def _arg(name: str, t: torch.Tensor, dtypes, shape, device: int, rows: bool = False) -> None:
     """Refuse a tensor that the kernels would misread: its type, shape (None:
-    any), device, or strides (its last `inner` dimensions are dense; 0: all)."""
+    any), device, or strides (`rows`: only the last dimension is dense)."""
+    if (t.dtype in dtypes and t.dim() == len(shape) and t.get_device() == device >= 0
+            and (t.is_contiguous() or (rows and t.stride(-1) == 1))):
+        for w, n in zip(shape, t.shape):
+            if w is not None and w != n:
+                break
+        else:
+            return
     if t.dtype not in dtypes:
         raise TypeError(f'{name}: unsupported dtype {t.dtype}')
     if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
         raise ValueError(f'{name}: shape {tuple(t.shape)}, expected {tuple("any" if w is None else w for w in shape)}')
-    if t.device != device or device.type != 'cuda':
-        raise ValueError(f'{name}: on {t.device}, expected a GPU tensor{"" if device.type != "cuda" else f" on {device}"}')
-    if not t.is_contiguous():
-        n, want = t.dim(), 1
-        for d in range(n - 1, (n - inner if inner else 0) - 1, -1):
-            if t.shape[d] != 1 and t.stride(d) != want:
-                raise ValueError(f'{name}: strides {t.stride()} of shape {tuple(t.shape)} are not supported')
-            want *= t.shape[d]
+    if device < 0 or t.get_device() != device:
+        raise ValueError(f'{name}: on {t.device}, expected a tensor on ' + (f'GPU {device}' if device >= 0 else 'a GPU'))
+    raise ValueError(f'{name}: strides {t.stride()} of shape {tuple(t.shape)} are not supported')
 
 
-def _ws_arg(ws: Optional[torch.Tensor], device: torch.device):
+def _ws_arg(ws: Optional[torch.Tensor], device: int):
     """(pointer, bytes) of a workspace, or (None, 0) without one."""
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f'ws: expected a contiguous tensor on {device}')
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f'ws: expected a contiguous tensor on GPU {device}')
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-class _on:
-    """The device of a call's tensors made current for its launches, and the
-    stream they go to: the caller's, or that device's current one."""
-    __slots__ = ('device', 'stream', 'back')
-
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream, self.back = device, stream, None
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if self.device.index is not None and self.device.index != cur:
-            self.back = cur
-            torch.cuda.set_device(self.device)
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _call(fn: str, device: int, stream, *args) -> None:
+    """The library's call on the device of its tensors: on the caller's stream,
+    or on that device's current one."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if stream is None:
+        s = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    else:
+        s = _stream(stream)
+    rc = getattr(_native.load(), fn)(*args, s)
+    if rc != 0:
+        raise EchError(fn, rc)
 
 
-def _paged_args(pool, page_table, row0, seq_len, dtypes):
+def _batch_args(pool, page_table, row0, seq_len):
     """Checks shared by the paged calls; returns (device, B)."""
-    dev = pool.device
-    _arg('pool', pool, dtypes, (None, None), dev)
-    B = seq_len.shape[0] if seq_len.dim() == 1 else -1
-    _arg('seq_len', seq_len, _I32, (None,), dev)
+    dev = pool.get_device()
+    B = seq_len.numel()
+    _arg('seq_len', seq_len, _I32, (B,), dev)
     _arg('row0', row0, _I32, (B + 1,), dev)
     _arg('page_table', page_table, _I32, (B, None), dev)
     return dev, B
@@ -328,18 +325,18 @@ def _paged_args(pool, page_table, row0, seq_len, dtypes):
 
 def ech_paged_append(pool, page_table, page_size: int, row0, seq_len, rows, status=None, stream=None) -> None:
     """A step's new rows [T, row] go into their sequences' pages: pool [slots,
-    row] (any type of `rows`' element size), page_table [B, pages] i32, row0
-    [B+1] i32, seq_len [B] i32 (with the new rows), status [1] i32 or None."""
-    dev, B = _paged_args(pool, page_table, row0, seq_len, (pool.dtype,))
-    _arg('rows', rows, (pool.dtype,), (None, pool.shape[1]), dev, inner=1)
+    row] (any type, the type of `rows`), page_table [B, pages] i32, row0 [B+1]
+    i32, seq_len [B] i32 (with the new rows), status [1] i32 or None."""
+    dev, B = _batch_args(pool, page_table, row0, seq_len)
+    _arg('pool', pool, (pool.dtype,), (None, None), dev)
+    n_slots, width = pool.shape
+    _arg('rows', rows, (pool.dtype,), (None, width), dev, rows=True)
     if status is not None:
         _arg('status', status, _I32, (1,), dev)
     T, es = rows.shape[0], pool.element_size()
-    with _on(dev, stream) as s:
-        _check('ech_paged_append', lib().ech_paged_append(
-            _ptr(pool), pool.shape[0], pool.shape[1] * es, int(page_size), _ptr(page_table), page_table.shape[1],
-            _ptr(row0), _ptr(seq_len), B, T, _ptr(rows), (rows.stride(0) if T > 1 else rows.shape[1]) * es,
-            _ptr(status), s))
+    _call('ech_paged_append', dev, stream, pool.data_ptr(), n_slots, width * es, page_size, page_table.data_ptr(),
+          page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, T, rows.data_ptr(),
+          (rows.stride(0) if T > 1 else width) * es, _ptr(status))
 
 
 def ech_paged_attn_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int, window: int = 0,
@@ -353,19 +350,17 @@ def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows:
     an optional sliding window and n_sink first tokens that stay visible: q
     [T, H, 576] bf16 (or its bits; rows and heads may be strided), pool [slots,
     576] bf16 -> out [T, H, 512] bf16, lse [T, H] fp32 (optional)."""
-    dev, B = _paged_args(pool, page_table, row0, seq_len, _BITS16)
-    _arg('pool', pool, _BITS16, (None, 576), dev)
-    _arg('q', q, _BITS16, (None, None, 576), dev, inner=1)
-    T, H = q.shape[0], q.shape[1]
+    _arg('pool', pool, _BITS16, (None, 576), pool.get_device())
+    dev, B = _batch_args(pool, page_table, row0, seq_len)
+    _arg('q', q, _BITS16, (None, None, 576), dev, rows=True)
+    T, H, _ = q.shape
     _arg('out', out, _BITS16, (T, H, 512), dev)
     if lse is not None:
         _arg('lse', lse, _F32, (T, H), dev)
     wp, wb = _ws_arg(ws, dev)
-    with _on(dev, stream) as s:
-        _check('ech_paged_attn', lib().ech_paged_attn(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(pool), pool.shape[0], int(page_size), _ptr(page_table),
-            page_table.shape[1], _ptr(row0), _ptr(seq_len), B, T, H, int(max_rows), int(max_len), int(window),
-            int(n_sink), float(sm_scale), _ptr(out), _ptr(lse), wp, wb, s))
+    _call('ech_paged_attn', dev, stream, q.data_ptr(), q.stride(0), q.stride(1), pool.data_ptr(), pool.shape[0],
+          page_size, page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, T, H, max_rows,
+          max_len, window, n_sink, sm_scale, out.data_ptr(), _ptr(lse), wp, wb)
 
 
 def ech_paged_weight_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int) -> int:
@@ -378,21 +373,19 @@ def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, ma
     """The attention weight each cached token received from the step's rows
     and heads (lse: that of ech_paged_attn), added to decay * acc_in: acc_in
     [B, >= max_len] fp32 or None, acc_out like it (may be acc_in)."""
-    dev, B = _paged_args(pool, page_table, row0, seq_len, _BITS16)
-    _arg('pool', pool, _BITS16, (None, 576), dev)
-    _arg('q', q, _BITS16, (None, None, 576), dev, inner=1)
-    T, H = q.shape[0], q.shape[1]
+    _arg('pool', pool, _BITS16, (None, 576), pool.get_device())
+    dev, B = _batch_args(pool, page_table, row0, seq_len)
+    _arg('q', q, _BITS16, (None, None, 576), dev, rows=True)
+    T, H, _ = q.shape
     _arg('lse', lse, _F32, (T, H), dev)
     _arg('acc_out', acc_out, _F32, (B, None), dev)
+    ld = acc_out.shape[1]
     if acc_in is not None:
-        _arg('acc_in', acc_in, _F32, (B, acc_out.shape[1]), dev)
+        _arg('acc_in', acc_in, _F32, (B, ld), dev)
     wp, wb = _ws_arg(ws, dev)
-    with _on(dev, stream) as s:
-        _check('ech_paged_weight', lib().ech_paged_weight(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(lse), _ptr(pool), pool.shape[0], int(page_size),
-            _ptr(page_table), page_table.shape[1], _ptr(row0), _ptr(seq_len), B, T, H, int(max_rows), int(max_len),
-            int(window), int(n_sink), float(sm_scale), _ptr(acc_in), _ptr(acc_out), acc_out.shape[1], float(decay),
-            wp, wb, s))
+    _call('ech_paged_weight', dev, stream, q.data_ptr(), q.stride(0), q.stride(1), lse.data_ptr(), pool.data_ptr(),
+          pool.shape[0], page_size, page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B,
+          T, H, max_rows, max_len, window, n_sink, sm_scale, _ptr(acc_in), acc_out.data_ptr(), ld, decay, wp, wb)
 
 
 def ech_paged_evict_ws_bytes(B: int, max_len: int, keep: int) -> int:
@@ -406,25 +399,24 @@ def ech_paged_evict(acc, seq_len, max_len: int, keep: int, n_sink: int, n_recent
     keep] i32 (ascending, -1 padded), len_out [B] i32, acc_out like acc or
     None. With a pool the kept rows move from src_table's pages to dst_table's
     (src_table itself: compacted in place)."""
-    dev, B = acc.device, (seq_len.shape[0] if seq_len.dim() == 1 else -1)
-    _arg('seq_len', seq_len, _I32, (None,), dev)
+    dev, B = acc.get_device(), seq_len.numel()
+    _arg('seq_len', seq_len, _I32, (B,), dev)
     _arg('acc', acc, _F32, (B, None), dev)
-    _arg('kept', kept, _I32, (B, int(keep)), dev)
+    _arg('kept', kept, _I32, (B, keep), dev)
     _arg('len_out', len_out, _I32, (B,), dev)
+    ld = acc.shape[1]
     if acc_out is not None:
-        _arg('acc_out', acc_out, _F32, (B, acc.shape[1]), dev)
-    n_slots = row_bytes = ld = 0
+        _arg('acc_out', acc_out, _F32, (B, ld), dev)
+    n_slots = row_bytes = pt_ld = 0
     if pool is not None:
         _arg('pool', pool, (pool.dtype,), (None, None), dev)
         if src_table is None or dst_table is None:
             raise ValueError('src_table and dst_table are needed to move the rows of a pool')
         _arg('src_table', src_table, _I32, (B, None), dev)
-        _arg('dst_table', dst_table, _I32, (B, src_table.shape[1]), dev)
-        n_slots, row_bytes, ld = pool.shape[0], pool.shape[1] * pool.element_size(), src_table.shape[1]
+        pt_ld = src_table.shape[1]
+        _arg('dst_table', dst_table, _I32, (B, pt_ld), dev)
+        n_slots, row_bytes = pool.shape[0], pool.shape[1] * pool.element_size()
     wp, wb = _ws_arg(ws, dev)
-    with _on(dev, stream) as s:
-        _check('ech_paged_evict', lib().ech_paged_evict(
-            _ptr(acc), acc.shape[1], _ptr(seq_len), B, int(max_len), int(keep), int(n_sink), int(n_recent),
-            _ptr(kept), _ptr(acc_out), _ptr(len_out), _ptr(pool), n_slots, row_bytes, int(page_size),
-            _ptr(src_table) if pool is not None else None, _ptr(dst_table) if pool is not None else None, ld, wp, wb,
-            s))
+    _call('ech_paged_evict', dev, stream, acc.data_ptr(), ld, seq_len.data_ptr(), B, max_len, keep, n_sink, n_recent,
+          kept.data_ptr(), _ptr(acc_out), len_out.data_ptr(), _ptr(pool), n_slots, row_bytes, page_size,
+          _ptr(src_table) if pool is not None else None, _ptr(dst_table) if pool is not None else None, pt_ld, wp, wb)
