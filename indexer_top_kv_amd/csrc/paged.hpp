@@ -68,34 +68,55 @@ __device__ __forceinline__ SeqRows seq_rows(const int32_t* row0, const int32_t* 
   return SeqRows{r0, min(r1 - r0, max_rows), len - (r1 - r0), len};
 }
 
-// Which sequence and which of its tiles `tile` is, when sequence b's n rows of
-// H heads make ceil(n H / per) tiles and the tiles are numbered through the
-// batch; b = -1 past the last one. Every lane of the wave takes part: 64
-// sequences a round.
-__device__ __forceinline__ void find_tile(const int32_t* row0, int B, int T, int max_rows, int H, int per, int tile,
-                                          int* b_out, int* t_out) {
+// Inclusive prefix sum over the wave's lanes in the vector unit (rows of 16 by
+// shifts, then the rows' last lanes to the rows behind them), and the last
+// lane's value, the same in every lane.
+__device__ __forceinline__ int lanes_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast 15 to rows 1, 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast 31 to rows 2, 3
+  return x;
+}
+__device__ __forceinline__ int last_lane(int x) { return __builtin_amdgcn_readlane(x, 63); }
+
+// What a workgroup does: span sp of the n_span spans of tile mt of sequence b
+// (-1: nothing), whose new rows are sr; in a plan, the batch's tile `tile` of
+// `tiles`.
+struct Work {
+  int b, mt, sp, n_span;
+  SeqRows sr;
+  int tile, tiles;
+};
+__device__ __forceinline__ SeqRows rows_of_lane(const SeqRows& sr, int l) {
+  return SeqRows{__builtin_amdgcn_readlane(sr.first, l), __builtin_amdgcn_readlane(sr.n, l),
+                 __builtin_amdgcn_readlane(sr.pos0, l), __builtin_amdgcn_readlane(sr.len, l)};
+}
+
+// Tile `tile` of the batch as one piece of work, when sequence b's n rows of H
+// heads make ceil(n H / per) tiles and the tiles are numbered through the
+// batch. Every lane of the wave takes part: 64 sequences a round.
+__device__ __forceinline__ Work tile_work(const int32_t* row0, const int32_t* seq_len, const Pages& pg, int B, int T,
+                                          int H, int max_rows, int max_len, int per, int tile) {
   const int lane = ech::lane_id();
   int base = 0;
   for (int b0 = 0; b0 < B; b0 += 64) {
     const int b = b0 + lane;
-    int n = 0;
-    if (b < B) {
-      const int r0 = min(max(row0[b], 0), T), r1 = min(max(row0[b + 1], r0), T);
-      n = min(r1 - r0, max_rows);
-    }
-    const int tiles = (int)(((int64_t)n * H + per - 1) / per);
-    const int incl = ech::wave_incl_scan(tiles);
+    SeqRows sr{0, 0, 0, 0};
+    if (b < B) sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+    const int tiles = (sr.n * H + per - 1) / per;          // T H < 2^30
+    const int incl = lanes_scan(tiles);
     const unsigned long long past = __ballot(base + incl > tile);
     if (past != 0ull) {
       const int l = __builtin_ctzll(past);
-      *b_out = b0 + l;
-      *t_out = tile - base - (__shfl(incl, l, 64) - __shfl(tiles, l, 64));
-      return;
+      const int before = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l);
+      return Work{b0 + l, tile - base - before, 0, 1, rows_of_lane(sr, l), 0, 0};
     }
-    base += __shfl(incl, 63, 64);
+    base += last_lane(incl);
   }
-  *b_out = -1;
-  *t_out = 0;
+  return Work{-1, 0, 0, 1, SeqRows{0, 0, 0, 0}, 0, 0};
 }
 
 // Whether a row at position p sees token t (t < len is the caller's).

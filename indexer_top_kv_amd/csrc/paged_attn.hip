@@ -51,6 +51,40 @@ __device__ __forceinline__ bf16x8_t ld_tr8(const uint8_t* p0, const uint8_t* p1)
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+constexpr int kOutPitch = 272;               // bytes of a query's 128 output columns in LDS (256 + 16: bank spread)
+
+// `n` queries' 128 columns (those below `most`) from LDS to their rows of the
+// output, 16 lanes a query.
+__device__ __forceinline__ void store_columns(uint16_t* out, const uint8_t* t, int most, int n, int lane) {
+  for (int q0 = 0; q0 < n; q0 += 4) {
+    const int mm = q0 + (lane >> 4);
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(t + mm * kOutPitch + (lane & 15) * 16);
+    if (mm < most) *reinterpret_cast<u32x4_t*>(out + (int64_t)mm * kPagedVal + (lane & 15) * 8) = v;
+  }
+}
+
+// A span's unnormalised output, in the order of the registers: 16 bytes per
+// [workgroup][row tile][wave][column tile ct][j][lane] = columns 128 wave + 32
+// ct + 8 j + 4 (lane / 32) .. +3 of query lane % 32 of the row tile, so that
+// writing and joining move whole kilobytes.
+__device__ __forceinline__ f32x4_t* part_at(float* part, int wg, int row_tiles, int r, int wave) {
+  return reinterpret_cast<f32x4_t*>(part) + (((int64_t)wg * row_tiles + r) * 4 + wave) * 1024;
+}
+__device__ __forceinline__ void store_part(float* part, int wg, int row_tiles, const f32x16_t (&acc)[4][4], int wave,
+                                           int lane) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (r < row_tiles) {
+      f32x4_t* o = part_at(part, wg, row_tiles, r, wave) + lane;
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[(ct * 4 + j) * 64] = f32x4_t{acc[ct][r][4 * j], acc[ct][r][4 * j + 1], acc[ct][r][4 * j + 2], acc[ct][r][4 * j + 3]};
+    }
+  }
+}
+
 // Workgroup = (tile of 128 queries of one sequence, span of its steps). With
 // one span it writes out and lse; with several the span's maximum, sum and
 // unnormalised output go to the workspace, and where its spans are to `info`.
@@ -69,12 +103,12 @@ __device__ __forceinline__ bf16x8_t ld_tr8(const uint8_t* p0, const uint8_t* p1)
 __global__ void __launch_bounds__(256, 1)
     paged_attn_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool, Pages pg,
                       const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B, int T, int H,
-                      int max_rows, int max_len, int window, int n_sink, float scale2, int planned, int rows_per,
+                      int max_rows, int max_len, int window, int n_sink, float scale2, int planned, int row_tiles,
                       uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
-                      float2* __restrict__ part_ml, int2* __restrict__ info) {
+                      float2* __restrict__ part_ml, PartInfo* __restrict__ info) {
   __shared__ __align__(128) uint8_t tiles[kBufs * kTileB];
   __shared__ __align__(16) uint8_t ps[kMT * kPPitch];
-  __shared__ float s_alpha[kMT], s_m[kMT], s_l[kMT];
+  __shared__ float s_alpha[kMT], s_l[kMT];
   __shared__ int s_flag[4];   // per row tile: 1 = its maximum grew, 2 = a score that does not count is not finite
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -84,30 +118,27 @@ __global__ void __launch_bounds__(256, 1)
     wk = plan_work<kMT, kStepTok>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
   } else {
     // more tiles than CUs: a tile each, the last (and in a chunk longest) first
-    wk = Work{-1, 0, 0, 1, 0};
-    find_tile(row0, B, T, max_rows, H, kMT, (int)(gridDim.x - 1 - blockIdx.x), &wk.b, &wk.mt);
+    wk = tile_work(row0, seq_len, pg, B, T, H, max_rows, max_len, kMT, (int)(gridDim.x - 1 - blockIdx.x));
   }
-  const int b = __builtin_amdgcn_readfirstlane(wk.b), mt = __builtin_amdgcn_readfirstlane(wk.mt);
-  const int sp = __builtin_amdgcn_readfirstlane(wk.sp), nsp = __builtin_amdgcn_readfirstlane(wk.n_span);
-  if (b < 0) return;
-  const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+  const int b = wk.b, mt = wk.mt, sp = wk.sp, nsp = wk.n_span;
+  const SeqRows sr = wk.sr;
   const int M = sr.n * H;                                  // fits: T H < 2^30 (checked on the host)
   const int m0 = mt * kMT;
+  const int64_t mg0 = (int64_t)sr.first * H + m0;          // first query among the batch's (row, head) pairs
+  if (planned) note_tile(info, wk, mg0, min(kMT, M - m0), planned);
+  if (b < 0) return;
   const int r_lo = m0 / H, r_hi = (min(m0 + kMT, M) - 1) / H;
   const int p_lo = sr.pos0 + r_lo, p_hi = sr.pos0 + r_hi;
   const Ranges rg = ranges_of<kStepTok>(p_lo, p_hi, window, n_sink);
   const int per = (rg.steps + nsp - 1) / nsp;
   const int step0 = min(sp * per, rg.steps), nsteps = min(step0 + per, rg.steps) - step0;
 
-  const int64_t mg0 = (int64_t)sr.first * H + m0;          // first query among the batch's (row, head) pairs
-  float2* const my_ml = part_ml + (int64_t)blockIdx.x * rows_per;
-  if (planned && sp == 0)
-    for (int x = threadIdx.x; x < min(kMT, M - m0); x += 256) info[mg0 + x] = make_int2(wk.base * kMT + x, nsp);
+  float2* const my_ml = part_ml + (int64_t)blockIdx.x * kMT;
   if (nsteps <= 0) {
     // nothing to see (a table without pages for it, a span past the end)
-    for (int x = threadIdx.x; x < min(kMT, M - m0); x += 256) {
+    for (int x = threadIdx.x; x < kMT; x += 256) {
       if (nsp > 1) my_ml[x] = make_float2(-__builtin_inff(), 0.f);
-      else if (lse) lse[mg0 + x] = -__builtin_inff();
+      else if (lse && x < M - m0) lse[mg0 + x] = -__builtin_inff();
     }
     if (nsp == 1)
       for (int x = threadIdx.x; x < min(kMT, M - m0) * (kPagedVal / 8); x += 256)
@@ -408,50 +439,37 @@ __global__ void __launch_bounds__(256, 1)
   l = pair_sum(l);
   int tid = threadIdx.x;             // recomputed: held across the loop these would take registers it needs
   asm volatile("" : "+v"(tid));
-  const int ecol = tid & 31, eg = (tid >> 5) & 1;
-  const bool elive = m0 + wave * 32 + ecol < M;
-  if (eg == 0) {
-    s_m[wave * 32 + ecol] = mx;
-    s_l[wave * 32 + ecol] = l;
-  }
-  if (nsp == 1) {
-    __syncthreads();
-    if (lse && elive && eg == 0)
-      lse[mg0 + wave * 32 + ecol] = l == 0.f ? -__builtin_inff() : (mx + log2f(l)) * 0.69314718055994531f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int mm = r * 32 + ecol;
-      const float sl = s_l[mm];
-      const float inv = sl == 0.f ? 0.f : 1.f / sl;
-      if (m0 + mm < M) {
-        uint16_t* o = out + (mg0 + mm) * kPagedVal + wave * 128 + 4 * eg;
-#pragma unroll
-        for (int ct = 0; ct < 4; ++ct)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
-            bf16x4_t x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (__bf16)(acc[ct][r][4 * j + e] * inv);
-            *reinterpret_cast<uint2*>(o + ct * 32 + 8 * j) = __builtin_bit_cast(uint2, x);
-          }
-      }
-    }
+  const int ecol = tid & 31, eg = (tid >> 5) & 1, elane = tid & 63;
+  if (eg == 0) s_l[wave * 32 + ecol] = l;
+  if (nsp > 1) {
+    if (eg == 0) my_ml[wave * 32 + ecol] = make_float2(mx, l);
+    store_part(part_o, blockIdx.x, row_tiles, acc, wave, elane);
     return;
   }
-  if (elive && eg == 0) my_ml[wave * 32 + ecol] = make_float2(mx, l);
+  __syncthreads();                   // every wave's sums; and every wave is done with the step buffers
+  if (lse && eg == 0 && m0 + wave * 32 + ecol < M)
+    lse[mg0 + wave * 32 + ecol] = l == 0.f ? -__builtin_inff() : (mx + log2f(l)) * 0.69314718055994531f;
+  // two row tiles at a time through this wave's part of the buffers, so that a
+  // query's 128 columns leave as 256 bytes
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int mm = r * 32 + ecol;
-    if (m0 + mm < M) {
-      float* o = part_o + ((int64_t)blockIdx.x * rows_per + mm) * kPagedVal + wave * 128 + 4 * eg;
+  for (int half = 0; half < 2; ++half) {
+    uint8_t* const t = tiles + wave * (64 * kOutPitch);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = half * 2 + u;
+      const float sl = s_l[r * 32 + ecol];
+      const float inv = sl == 0.f ? 0.f : 1.f / sl;
 #pragma unroll
       for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<f32x4_t*>(o + ct * 32 + 8 * j) =
-              f32x4_t{acc[ct][r][4 * j], acc[ct][r][4 * j + 1], acc[ct][r][4 * j + 2], acc[ct][r][4 * j + 3]};
+        for (int j = 0; j < 4; ++j) {
+          bf16x4_t x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = (__bf16)(acc[ct][r][4 * j + e] * inv);
+          *reinterpret_cast<uint2*>(t + (u * 32 + ecol) * kOutPitch + ct * 64 + j * 16 + eg * 8) = __builtin_bit_cast(uint2, x);
+        }
     }
+    store_columns(out + (mg0 + half * 64) * kPagedVal + wave * 128, t, M - m0 - half * 64, 64, elane);
   }
 }
 
@@ -495,27 +513,26 @@ __global__ void __launch_bounds__(256, 1)
     paged_attn_narrow_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool,
                              Pages pg, const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B,
                              int T, int H, int max_rows, int max_len, int window, int n_sink, float scale2, int planned,
-                             int rows_per, uint16_t* __restrict__ out, float* __restrict__ lse,
-                             float* __restrict__ part_o, float2* __restrict__ part_ml, int2* __restrict__ info) {
+                             int row_tiles, uint16_t* __restrict__ out, float* __restrict__ lse,
+                             float* __restrict__ part_o, float2* __restrict__ part_ml, PartInfo* __restrict__ info) {
   __shared__ __align__(128) uint8_t tiles[4 * 2 * kNTile];
   __shared__ int s_page[4][2][64];   // per wave: page-table entries of two steps' tokens
   __shared__ float2 s_ml[4][kNM];    // per wave: maximum and sum of each query
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, col = lane & 31, g = lane >> 5;
-  Work wk{-1, 0, 0, 1, 0};
+  Work wk;
   if (planned) wk = plan_work<kNM, kNRound>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
-  else find_tile(row0, B, T, max_rows, H, kNM, (int)blockIdx.x, &wk.b, &wk.mt);
-  const int b = __builtin_amdgcn_readfirstlane(wk.b);
-  const int sp = __builtin_amdgcn_readfirstlane(wk.sp), nsp = __builtin_amdgcn_readfirstlane(wk.n_span);
-  if (b < 0) return;
-  const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+  else wk = tile_work(row0, seq_len, pg, B, T, H, max_rows, max_len, kNM, (int)blockIdx.x);
+  const int b = wk.b, sp = wk.sp, nsp = wk.n_span;
+  const SeqRows sr = wk.sr;
   const int M = sr.n * H;                                  // 1 .. 32
   const int64_t mg0 = (int64_t)sr.first * H;
+  if (planned) note_tile(info, wk, mg0, M, planned);
+  if (b < 0) return;
   const Ranges rg = ranges_of<kNRound>(sr.pos0, sr.pos0 + sr.n - 1, window, n_sink);
   const int per = (rg.steps + nsp - 1) / nsp;
   const int round0 = min(sp * per, rg.steps), rounds = min(round0 + per, rg.steps) - round0;
-  if (planned && sp == 0 && threadIdx.x < M) info[mg0 + threadIdx.x] = make_int2(wk.base * kMT + threadIdx.x, nsp);
 
   // tokens of this wave's step i (one per round): [t0, t0 + count), count <= 0: none
   auto step_tok = [&](int i, int* count) -> int {
@@ -674,7 +691,6 @@ __global__ void __launch_bounds__(256, 1)
           x[v] = __builtin_amdgcn_exp2f(x[v] - ref);
           psum += x[v];
         }
-        typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
         const bf16x4_t pb = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
         const uint2 u = __builtin_bit_cast(uint2, pb);
         pk[h][0] = u.x;
@@ -782,90 +798,90 @@ __global__ void __launch_bounds__(256, 1)
     }
     __syncthreads();
   }
-  if (col >= M) return;
-  if (nsp == 1) {
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    if (lse && wave == 0 && g == 0)
-      lse[mg0 + col] = den == 0.f ? -__builtin_inff() : (top + log2f(den)) * 0.69314718055994531f;
-    uint16_t* o = out + (mg0 + col) * kPagedVal + wave * 128 + 4 * g;
+  if (nsp > 1) {
+    if (wave == 0 && g == 0) part_ml[(int64_t)blockIdx.x * kMT + col] = make_float2(top, den);
+    f32x4_t* o = part_at(part_o, blockIdx.x, row_tiles, 0, wave) + lane;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
-        bf16x4_t x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = (__bf16)(res[c][4 * j + e] * inv);
-        *reinterpret_cast<uint2*>(o + c * 32 + 8 * j) = __builtin_bit_cast(uint2, x);
-      }
+      for (int j = 0; j < 4; ++j)
+        o[(c * 4 + j) * 64] = f32x4_t{res[c][4 * j], res[c][4 * j + 1], res[c][4 * j + 2], res[c][4 * j + 3]};
     return;
   }
-  if (wave == 0 && g == 0) part_ml[(int64_t)blockIdx.x * rows_per + col] = make_float2(top, den);
-  float* o = part_o + ((int64_t)blockIdx.x * rows_per + col) * kPagedVal + wave * 128 + 4 * g;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  if (lse && wave == 0 && g == 0 && col < M)
+    lse[mg0 + col] = den == 0.f ? -__builtin_inff() : (top + log2f(den)) * 0.69314718055994531f;
+  uint8_t* const t = tiles + wave * (32 * kOutPitch);
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<f32x4_t*>(o + c * 32 + 8 * j) =
-          f32x4_t{res[c][4 * j], res[c][4 * j + 1], res[c][4 * j + 2], res[c][4 * j + 3]};
+    for (int j = 0; j < 4; ++j) {
+      bf16x4_t x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = (__bf16)(res[c][4 * j + e] * inv);
+      *reinterpret_cast<uint2*>(t + col * kOutPitch + c * 64 + j * 16 + g * 8) = __builtin_bit_cast(uint2, x);
+    }
+  store_columns(out + mg0 * kPagedVal + wave * 128, t, M, 32, lane);
 }
 
-// out and lse of every query that took several spans, from their partials in
-// span order. grid (T H), 128 threads: four value columns each; the spans'
-// loads go out kG at a time before the first is waited for.
+// out and lse of the tiles that took several spans, in span order. grid (tiles,
+// 16 x row tiles), 256 threads: a workgroup joins 32 columns of 32 queries, a
+// thread one 16-byte piece, kG spans' loads under way at a time.
 constexpr int kG = 8;
-__global__ void __launch_bounds__(128)
+constexpr int kJoinPitch = 80;               // bytes of a query's 32 columns in LDS (64 + 16: bank spread)
+__global__ void __launch_bounds__(256)
     paged_attn_merge_kernel(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
-                            const int2* __restrict__ info, const int32_t* __restrict__ row0, int B, int T, int H,
-                            int rows_per, int n_wg, uint16_t* __restrict__ out, float* __restrict__ lse) {
-  const int64_t mg = blockIdx.x;
-  const int row = (int)(mg / H);
-  if (row < row0[0] || row >= row0[B]) return;              // a row of no sequence stays as it was
-  const int2 in = info[mg];
-  const int n = in.y;
-  const int base = in.x / kMT, mm = in.x % kMT;
-  // one span wrote its output itself; a query past max_rows has no info
-  if (n <= 1 || in.x < 0 || n > n_wg || base > n_wg - n || mm >= rows_per) return;
-  const float2* ml = part_ml + (int64_t)base * rows_per + mm;
-  const float* po = part_o + ((int64_t)base * rows_per + mm) * kPagedVal + 4 * threadIdx.x;
+                            const PartInfo* __restrict__ info, int row_tiles, uint16_t* __restrict__ out,
+                            float* __restrict__ lse) {
+  __shared__ __align__(16) uint8_t t[32 * kJoinPitch];
+  const int r = blockIdx.y >> 4, cw = (blockIdx.y >> 2) & 3, ct = blockIdx.y & 3;
+  const PartInfo in = info[blockIdx.x];
+  const int n = in.n_span, most = in.queries - r * 32;
+  if (n <= 1 || most <= 0 || in.base < 0 || in.base > kCus - n) return;   // one span wrote its output itself
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, g = lane >> 5;
+  const float2* ml = part_ml + (int64_t)in.base * kMT + r * 32 + col;
+  const f32x4_t* po = part_at(const_cast<float*>(part_o), in.base, row_tiles, r, cw) + ct * 256 + threadIdx.x;
+  const int64_t stride = (int64_t)row_tiles * 4 * 1024;
   float mx = -__builtin_inff(), den = 0.f;
   f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
   for (int s0 = 0; s0 < n; s0 += kG) {
     float2 a[kG];
     f32x4_t x[kG];
 #pragma unroll
-    for (int j = 0; j < kG; ++j) {
-      const int64_t s = min(s0 + j, n - 1);
-      a[j] = ml[s * rows_per];
-      x[j] = *reinterpret_cast<const f32x4_t*>(po + s * rows_per * kPagedVal);
+    for (int u = 0; u < kG; ++u) {
+      const int s = min(s0 + u, n - 1);
+      a[u] = ml[(int64_t)s * kMT];
+      x[u] = po[s * stride];
     }
     float top = mx;
 #pragma unroll
-    for (int j = 0; j < kG; ++j) top = fmaxf(top, a[j].x);
+    for (int u = 0; u < kG; ++u) top = fmaxf(top, a[u].x);
     const float ref = top == -__builtin_inff() ? 0.f : top;
-    const float r = exp2f((mx == -__builtin_inff() ? ref : mx) - ref);   // o and den are 0 before anything is seen
-    den *= r;
+    const float f = exp2f((mx == -__builtin_inff() ? ref : mx) - ref);   // o and den are 0 before anything is seen
+    den *= f;
+    o *= f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= r;
-#pragma unroll
-    for (int j = 0; j < kG; ++j) {
-      if (s0 + j < n && a[j].y != 0.f) {                    // a span that saw nothing wrote no output
-        const float w = exp2f((a[j].x == -__builtin_inff() ? ref : a[j].x) - ref);
-        den += w * a[j].y;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += w * x[j][e];
+    for (int u = 0; u < kG; ++u) {
+      if (s0 + u < n && a[u].y != 0.f) {                    // a span that saw nothing wrote no output
+        const float w = exp2f((a[u].x == -__builtin_inff() ? ref : a[u].x) - ref);
+        den += w * a[u].y;
+        o += w * x[u];
       }
     }
     mx = top;
   }
+  if (lse && cw == 0 && ct == 0 && wave == 0 && g == 0 && col < most)
+    lse[in.first + r * 32 + col] = den == 0.f ? -__builtin_inff() : (mx + log2f(den)) * 0.69314718055994531f;
   const float inv = den == 0.f ? 0.f : 1.f / den;
-  typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
-  bf16x4_t y;
+  bf16x4_t y;                         // this thread's piece: columns 8 wave + 4 g .. +3 of query col
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = (__bf16)(o[e] * inv);
-  *reinterpret_cast<uint2*>(out + mg * kPagedVal + 4 * threadIdx.x) = __builtin_bit_cast(uint2, y);
-  if (lse && threadIdx.x == 0)
-    lse[mg] = den == 0.f ? -__builtin_inff() : (mx + log2f(den)) * 0.69314718055994531f;
+  *reinterpret_cast<uint2*>(t + col * kJoinPitch + wave * 16 + g * 8) = __builtin_bit_cast(uint2, y);
+  __syncthreads();
+  const int mm = threadIdx.x >> 2;    // 32 queries x 64 bytes, four threads a query
+  if (mm < min(most, 32))
+    *reinterpret_cast<u32x4_t*>(out + (in.first + r * 32 + mm) * kPagedVal + cw * 128 + ct * 32 + (threadIdx.x & 3) * 8) =
+        *reinterpret_cast<const u32x4_t*>(t + mm * kJoinPitch + (threadIdx.x & 3) * 16);
 }
 
 // Upper bound of the batch's tiles: every sequence rounds up once.
@@ -879,7 +895,7 @@ struct Split {
   bool narrow;        // at most 32 queries a sequence
   bool planned;
   int64_t tiles;
-  int rows_per;       // queries a partial holds
+  int row_tiles;      // of 32 queries a partial holds
   size_t part_o, part_ml, info, bytes;
 };
 Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
@@ -891,11 +907,10 @@ Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n
   if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1 + kStepTok);
   sp.planned = sp.tiles <= kCus && B <= kPlanSeqs && seen > kMinSpan * kStepTok;
   if (!sp.planned) return sp;
-  sp.rows_per = (int)std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H);
-  auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-  sp.part_ml = (size_t)kCus * sp.rows_per * kPagedVal * sizeof(float);
-  sp.info = sp.part_ml + up((size_t)kCus * sp.rows_per * sizeof(float2));
-  sp.bytes = sp.info + up((size_t)T * H * sizeof(int2));
+  sp.row_tiles = (int)((std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H) + 31) / 32);
+  sp.part_ml = (size_t)kCus * sp.row_tiles * 32 * kPagedVal * sizeof(float);
+  sp.info = sp.part_ml + (size_t)kCus * kMT * sizeof(float2);
+  sp.bytes = sp.info + (size_t)kCus * sizeof(PartInfo);
   return sp;
 }
 
@@ -932,16 +947,16 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   char* w = static_cast<char*>(ws);
   float* part_o = reinterpret_cast<float*>(w);
   float2* part_ml = sp.planned ? reinterpret_cast<float2*>(w + sp.part_ml) : nullptr;
-  int2* info = sp.planned ? reinterpret_cast<int2*>(w + sp.info) : nullptr;
+  PartInfo* info = sp.planned ? reinterpret_cast<PartInfo*>(w + sp.info) : nullptr;
   const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
   hipLaunchKernelGGL((sp.narrow ? paged_attn_narrow_kernel : paged_attn_kernel), dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
                      static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg,
                      row0, seq_len, B, T, H, max_rows, max_len, window, n_sink, sm_scale * 1.4426950408889634f,
-                     (int)sp.planned, sp.rows_per, static_cast<uint16_t*>(out), lse, part_o, part_ml, info);
+                     sp.planned ? (int)sp.tiles : 0, sp.row_tiles, static_cast<uint16_t*>(out), lse, part_o, part_ml, info);
   ECH_LAUNCH_CHECK();
   if (sp.planned) {
-    hipLaunchKernelGGL(paged_attn_merge_kernel, dim3((unsigned)((int64_t)T * H)), dim3(kPagedVal / 4), 0, s, part_o,
-                       part_ml, info, row0, B, T, H, sp.rows_per, kCus, static_cast<uint16_t*>(out), lse);
+    hipLaunchKernelGGL(paged_attn_merge_kernel, dim3((unsigned)sp.tiles, 16 * sp.row_tiles), dim3(256), 0, s, part_o, part_ml, info,
+                       sp.row_tiles, static_cast<uint16_t*>(out), lse);
     ECH_LAUNCH_CHECK();
   }
   return ECH_OK;

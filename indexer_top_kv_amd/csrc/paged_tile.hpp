@@ -9,6 +9,7 @@ namespace {
 
 typedef __attribute__((__vector_size__(8 * sizeof(__bf16)))) __bf16 bf16x8_t;
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
+typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_t;
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef short v4s_t __attribute__((ext_vector_type(4)));
@@ -90,20 +91,18 @@ __device__ __forceinline__ uint32_t sees_bits(int p, int t0, int window, int n_s
   return bits;
 }
 
-// What a workgroup does: span sp of the n_span spans of tile mt of sequence b;
-// the tile's spans are workgroups base .. base + n_span - 1.
-struct Work {
-  int b, mt, sp, n_span, base;
-};
-
 constexpr int kCus = 256;
 constexpr int kMinSpan = 4;          // steps a span is worth its start and its partial
 constexpr int kPlanSeqs = 256;       // sequences a plan covers (four per lane)
 
-__device__ __forceinline__ int wave_max(int v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = max(v, __shfl_xor(v, d, 64));
-  return v;
+__device__ __forceinline__ int lanes_max(int x) {           // x >= 0
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return last_lane(x);
 }
 
 // The batch's tiles split over the card's CUs: every tile takes ceil(steps /
@@ -119,36 +118,38 @@ __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* se
                                           int H, int max_rows, int max_len, int window, int n_sink, int wg) {
   const int lane = ech::lane_id();
   int nt[kPlanSeqs / 64], st[kPlanSeqs / 64];
+  SeqRows sr[kPlanSeqs / 64];
   int tiles = 0, total = 0, longest = 1;
 #pragma unroll
   for (int c = 0; c < kPlanSeqs / 64; ++c) {
     nt[c] = 0;
     st[c] = 1;
+    sr[c] = SeqRows{0, 0, 0, 0};
     if (c * 64 < B) {
       const int b = c * 64 + lane;
-      if (b < B) {
-        const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
-        nt[c] = (sr.n * H + PER - 1) / PER;
-        if (ALL) {
-          nt[c] = sr.len > 0;
-          st[c] = max(1, (sr.len + STEP - 1) / STEP);
-        } else if (nt[c] > 0)
-          st[c] = max(1, ranges_of<STEP>(sr.pos0 + (nt[c] - 1) * PER / H, sr.pos0 + sr.n - 1, window, n_sink).steps);
+      if (b < B) sr[c] = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+      if (ALL) {
+        nt[c] = sr[c].len > 0;
+        st[c] = max(1, (sr[c].len + STEP - 1) / STEP);
+      } else {
+        nt[c] = (sr[c].n * H + PER - 1) / PER;
+        if (nt[c] > 0)
+          st[c] = max(1, ranges_of<STEP>(sr[c].pos0 + (nt[c] - 1) * PER / H, sr[c].pos0 + sr[c].n - 1, window, n_sink).steps);
       }
       tiles += nt[c];
       total += nt[c] * st[c];
       if (nt[c] > 0) longest = max(longest, st[c]);
     }
   }
-  tiles = ech::wave_sum(tiles);
-  total = ech::wave_sum(total);
-  longest = wave_max(longest);
+  tiles = last_lane(lanes_scan(tiles));
+  total = last_lane(lanes_scan(total));
+  longest = lanes_max(longest);
   auto spans = [&](int S) -> int {
     int n = 0;
 #pragma unroll
     for (int c = 0; c < kPlanSeqs / 64; ++c)
       if (c * 64 < B) n += nt[c] * ((st[c] + S - 1) / S);
-    return ech::wave_sum(n);
+    return last_lane(lanes_scan(n));
   };
   int lo = max(kMinSpan * kStepTok / STEP, (total + kCus - 1) / kCus), hi = max(lo, longest);   // spans(hi) = tiles <= kCus
   if (tiles < kCus) hi = min(hi, max(lo, total / (kCus - tiles) + 1));         // sum ceil(x) < sum x + tiles
@@ -157,23 +158,40 @@ __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* se
     if (spans(mid) <= kCus) hi = mid;
     else lo = mid + 1;
   }
-  int base = 0;
+  int base = 0, tile0 = 0;
 #pragma unroll
   for (int c = 0; c < kPlanSeqs / 64; ++c) {
     if (c * 64 < B) {
       const int n = (st[c] + hi - 1) / hi, mine = nt[c] * n;
-      const int incl = ech::wave_incl_scan(mine);
+      const int incl = lanes_scan(mine);
       const unsigned long long past = __ballot(base + incl > wg);
       if (past != 0ull) {
         const int l = __builtin_ctzll(past);
-        const int first = base + __shfl(incl, l, 64) - __shfl(mine, l, 64), ns = __shfl(n, l, 64);
-        const int mt = (wg - first) / ns, at = first + mt * ns;
-        return Work{c * 64 + l, mt, wg - at, ns, at};
+        const int in = wg - base - __builtin_amdgcn_readlane(incl, l) + __builtin_amdgcn_readlane(mine, l);
+        const int ns = __builtin_amdgcn_readlane(n, l), mt = in / ns;
+        tile0 += __builtin_amdgcn_readlane(lanes_scan(nt[c]) - nt[c], l);
+        return Work{c * 64 + l, mt, in - mt * ns, ns, rows_of_lane(sr[c], l), tile0 + mt, tiles};
       }
-      base += __shfl(incl, 63, 64);
+      base += last_lane(incl);
+      tile0 += last_lane(lanes_scan(nt[c]));
     }
   }
-  return Work{-1, 0, 0, 1, 0};
+  return Work{-1, 0, 0, 1, SeqRows{0, 0, 0, 0}, 0, tiles};
+}
+
+// How a tile's partials are joined: its first query and how many it has, and
+// which workgroups hold its spans (n_span <= 1: nothing to join).
+struct PartInfo {
+  int64_t first;
+  int queries, base, n_span, spare;
+};
+// Written by the workgroup of a tile's first span; the first workgroup marks
+// the entries past the last tile, up to `bound`. Call from all threads.
+__device__ __forceinline__ void note_tile(PartInfo* info, const Work& wk, int64_t first, int queries, int bound) {
+  if (blockIdx.x == 0)
+    for (int x = wk.tiles + threadIdx.x; x < bound; x += blockDim.x) info[x] = PartInfo{0, 0, 0, 0, 0};
+  if (wk.b >= 0 && wk.sp == 0 && threadIdx.x == 0 && wk.tile < bound)
+    info[wk.tile] = PartInfo{first, queries, (int)blockIdx.x, wk.n_span, 0};
 }
 
 }  // namespace

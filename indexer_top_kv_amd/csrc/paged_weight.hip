@@ -53,17 +53,19 @@ __global__ void __launch_bounds__(256, 1)
   __shared__ int s_page[4][2][64];   // per wave: page-table entries of two steps' tokens
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, col = lane & 31, g = lane >> 5;
-  Work wk{(int)blockIdx.x, 0, 0, 1, 0};
+  Work wk;
   if (planned) {
     if (window == 0)
       wk = plan_work<kMS, kStepTok, true>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
     else
       wk = plan_work<kMS, kStepTok>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
+  } else {
+    wk = Work{(int)blockIdx.x, 0, 0, 1, seq_rows(row0, seq_len, pg, blockIdx.x, T, max_rows, max_len), 0, 0};
   }
   const int b = __builtin_amdgcn_readfirstlane(wk.b);
   const int sp = __builtin_amdgcn_readfirstlane(wk.sp), nsp = __builtin_amdgcn_readfirstlane(wk.n_span);
   if (b < 0) return;
-  const SeqRows sr = seq_rows(row0, seq_len, pg, b, T, max_rows, max_len);
+  const SeqRows sr = wk.sr;
   const int M = sr.n * H;
   // without a window all tokens are written here (the last ones by rows that see
   // them, those of a sequence without rows by nobody's weight); with one, those
