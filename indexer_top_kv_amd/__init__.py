@@ -267,26 +267,28 @@ def ech_kv_append(host_pool, kcache, kscale, state: LayerState, seq_tok0, seq_le
 _BITS16 = (torch.int16, torch.uint16, torch.bfloat16)
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, '_cuda_getCurrentRawStream') else None
+# torch's own lookups without its wrappers' cost, where this build has them
+_raw_stream = getattr(torch._C, '_cuda_getCurrentRawStream', lambda d: torch.cuda.current_stream(d).cuda_stream)
+_current_device = getattr(torch._C, '_cuda_getDevice', torch.cuda.current_device)
 
 
 def _arg(name: str, t: torch.Tensor, dtypes, shape, device: int, rows: bool = False) -> None:
     """Refuse a tensor that the kernels would misread: its type, shape (None:
     any), device, or strides (`rows`: only the last dimension is dense)."""
-    if (t.dtype in dtypes and t.dim() == len(shape) and t.get_device() == device >= 0
+    if (t.dtype in dtypes and t.get_device() == device >= 0 and (t.shape == shape or _fits(t.shape, shape))
             and (t.is_contiguous() or (rows and t.stride(-1) == 1))):
-        for w, n in zip(shape, t.shape):
-            if w is not None and w != n:
-                break
-        else:
-            return
+        return
     if t.dtype not in dtypes:
         raise TypeError(f'{name}: unsupported dtype {t.dtype}')
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    if not _fits(t.shape, shape):
         raise ValueError(f'{name}: shape {tuple(t.shape)}, expected {tuple("any" if w is None else w for w in shape)}')
     if device < 0 or t.get_device() != device:
         raise ValueError(f'{name}: on {t.device}, expected a tensor on ' + (f'GPU {device}' if device >= 0 else 'a GPU'))
     raise ValueError(f'{name}: strides {t.stride()} of shape {tuple(t.shape)} are not supported')
+
+
+def _fits(have, want) -> bool:
+    return len(have) == len(want) and all(w is None or w == n for w, n in zip(want, have))
 
 
 def _ws_arg(ws: Optional[torch.Tensor], device: int):
@@ -301,14 +303,10 @@ def _ws_arg(ws: Optional[torch.Tensor], device: int):
 def _call(fn: str, device: int, stream, *args) -> None:
     """The library's call on the device of its tensors: on the caller's stream,
     or on that device's current one."""
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
-    if stream is None:
-        s = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
-    else:
-        s = _stream(stream)
-    rc = getattr(_native.load(), fn)(*args, s)
+    rc = getattr(_native.load(), fn)(*args, _raw_stream(device) if stream is None else _stream(stream))
     if rc != 0:
         raise EchError(fn, rc)
 
@@ -319,7 +317,7 @@ def _batch_args(pool, page_table, row0, seq_len):
     B = seq_len.numel()
     _arg('seq_len', seq_len, _I32, (B,), dev)
     _arg('row0', row0, _I32, (B + 1,), dev)
-    _arg('page_table', page_table, _I32, (B, None), dev)
+    _arg('page_table', page_table, _I32, (B, page_table.shape[-1]), dev)
     return dev, B
 
 
@@ -330,10 +328,10 @@ def ech_paged_append(pool, page_table, page_size: int, row0, seq_len, rows, stat
     dev, B = _batch_args(pool, page_table, row0, seq_len)
     _arg('pool', pool, (pool.dtype,), (None, None), dev)
     n_slots, width = pool.shape
-    _arg('rows', rows, (pool.dtype,), (None, width), dev, rows=True)
+    T, es = rows.shape[0], pool.element_size()
+    _arg('rows', rows, (pool.dtype,), (T, width), dev, rows=True)
     if status is not None:
         _arg('status', status, _I32, (1,), dev)
-    T, es = rows.shape[0], pool.element_size()
     _call('ech_paged_append', dev, stream, pool.data_ptr(), n_slots, width * es, page_size, page_table.data_ptr(),
           page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, T, rows.data_ptr(),
           (rows.stride(0) if T > 1 else width) * es, _ptr(status))
@@ -350,10 +348,10 @@ def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows:
     an optional sliding window and n_sink first tokens that stay visible: q
     [T, H, 576] bf16 (or its bits; rows and heads may be strided), pool [slots,
     576] bf16 -> out [T, H, 512] bf16, lse [T, H] fp32 (optional)."""
-    _arg('pool', pool, _BITS16, (None, 576), pool.get_device())
+    _arg('pool', pool, _BITS16, (pool.shape[0], 576), pool.get_device())
     dev, B = _batch_args(pool, page_table, row0, seq_len)
-    _arg('q', q, _BITS16, (None, None, 576), dev, rows=True)
-    T, H, _ = q.shape
+    T, H = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+    _arg('q', q, _BITS16, (T, H, 576), dev, rows=True)
     _arg('out', out, _BITS16, (T, H, 512), dev)
     if lse is not None:
         _arg('lse', lse, _F32, (T, H), dev)
@@ -373,10 +371,10 @@ def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, ma
     """The attention weight each cached token received from the step's rows
     and heads (lse: that of ech_paged_attn), added to decay * acc_in: acc_in
     [B, >= max_len] fp32 or None, acc_out like it (may be acc_in)."""
-    _arg('pool', pool, _BITS16, (None, 576), pool.get_device())
+    _arg('pool', pool, _BITS16, (pool.shape[0], 576), pool.get_device())
     dev, B = _batch_args(pool, page_table, row0, seq_len)
-    _arg('q', q, _BITS16, (None, None, 576), dev, rows=True)
-    T, H, _ = q.shape
+    T, H = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+    _arg('q', q, _BITS16, (T, H, 576), dev, rows=True)
     _arg('lse', lse, _F32, (T, H), dev)
     _arg('acc_out', acc_out, _F32, (B, None), dev)
     ld = acc_out.shape[1]

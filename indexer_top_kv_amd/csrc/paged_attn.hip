@@ -475,26 +475,26 @@ __global__ void __launch_bounds__(256, 1)
 
 // ------------------------------------------------------------------ few queries
 // The same for sequences of at most 32 queries (a decoded token of up to 32
-// heads, two of 16): bound by the rows it reads, not by the products. The four
-// waves of a workgroup are token lanes of their own: each takes every fourth
-// 16-token step of the span with all 32 queries and all 512 value columns (256
-// accumulators), its own maximum and sum, and two step buffers of its own, so
-// nothing waits for another wave until the span's end, where the waves' states
-// are joined through LDS. In a step, on v_mfma_f32_16x16x32_bf16,
-//   S^T[token][m] = K . Q^T       16 tokens x 2 x 16 queries
-// leaves a lane four tokens of two queries; two lane swaps of the packed
-// weights turn them into the operand of O^T[col][m] += V^T . P^T
-// (v_mfma_f32_32x32x16_bf16), so P needs no LDS.
-// With the 128-query kernel: 64 sequences, one token, 32 heads, window 1024 of
-// 100K 41 us, one token of 16 heads over 1000 21 us; with this 38 and 20 us.
+// heads, two of 16): bound by the rows it reads, or, over short ranges, by the
+// chain of waits of a round. A round takes 64 tokens. Wave w loads tokens 16 w
+// .. +15 and forms their scores with all QT x 16 queries,
+//   S^T[token][m] = K . Q^T       v_mfma_f32_16x16x32_bf16
+// (four tokens of QT queries in a lane); the waves' maxima cross through LDS,
+// the weights (4 KiB, after two lane swaps already the operand of the next
+// product) cross too, and wave w adds value columns 128 w .. +127 of all 64:
+//   O^T[col][m] += V^T . P^T      v_mfma_f32_32x32x16_bf16, 64 accumulators
+// Two barriers a round; the next round's rows are asked for behind the first,
+// when every wave has left the buffer they go to. Waves that are token lanes
+// of their own, joined through LDS at the end, need no barrier but took 8.5K
+// cycles to join: 64 sequences, one token, 32 heads, window 1024 of 100K 35 us,
+// one token of 16 heads over 1000 19 us; with this 32 and 14 us.
 constexpr int kNM = 32;                      // queries per workgroup
-constexpr int kNTok = 16;                    // tokens per step of a wave
-constexpr int kNRound = 4 * kNTok;           // tokens per step of the four waves
-constexpr int kNTail = kNTok * kVPitch;
-constexpr int kNTile = kNTail + kNTok * 128;
+constexpr int kNTok = 16;                    // tokens per wave and round
+constexpr int kNRound = 4 * kNTok;
+constexpr int kNTail = kNRound * kVPitch;
+constexpr int kNTile = kNTail + kNRound * 128;
 constexpr int kNKs = kPagedRow / 32;         // contraction steps of the scores (18)
 constexpr int kNKD = 6;                      // key fragments in flight
-constexpr int kNLoads = kNTok + 2;           // row loads per step
 
 __device__ __forceinline__ f32x4_t mfma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   typedef __attribute__((__vector_size__(4 * sizeof(float)))) float v4_t;
@@ -509,24 +509,28 @@ __device__ __forceinline__ float quad_sum(float x) {
   return pair_sum(__uint_as_float(p[0]) + __uint_as_float(p[1]));
 }
 
+template <int QT>
 __global__ void __launch_bounds__(256, 1)
     paged_attn_narrow_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool,
                              Pages pg, const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B,
                              int T, int H, int max_rows, int max_len, int window, int n_sink, float scale2, int planned,
                              int row_tiles, uint16_t* __restrict__ out, float* __restrict__ lse,
                              float* __restrict__ part_o, float2* __restrict__ part_ml, PartInfo* __restrict__ info) {
-  __shared__ __align__(128) uint8_t tiles[4 * 2 * kNTile];
-  __shared__ int s_page[4][2][64];   // per wave: page-table entries of two steps' tokens
-  __shared__ float2 s_ml[4][kNM];    // per wave: maximum and sum of each query
+  __shared__ __align__(128) uint8_t tiles[2 * kNTile];
+  __shared__ __align__(16) uint8_t s_p[4 * 1024];   // P: per wave's tokens, a lane's 16 bytes
+  __shared__ int s_page[4][2][64];   // per wave: page-table entries of two rounds' tokens
+  __shared__ float s_x[4][kNM];      // per wave: a round's maximum of each query; at the end its sum
+  __shared__ int s_poison[4];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, col = lane & 31, g = lane >> 5;
+  const bool hi = (lane & 16) != 0;                        // query `col` is one of the second sixteen
   Work wk;
   if (planned) wk = plan_work<kNM, kNRound>(row0, seq_len, pg, B, T, H, max_rows, max_len, window, n_sink, blockIdx.x);
   else wk = tile_work(row0, seq_len, pg, B, T, H, max_rows, max_len, kNM, (int)blockIdx.x);
   const int b = wk.b, sp = wk.sp, nsp = wk.n_span;
   const SeqRows sr = wk.sr;
-  const int M = sr.n * H;                                  // 1 .. 32
+  const int M = sr.n * H;                                  // 1 .. 16 QT
   const int64_t mg0 = (int64_t)sr.first * H;
   if (planned) note_tile(info, wk, mg0, M, planned);
   if (b < 0) return;
@@ -534,18 +538,18 @@ __global__ void __launch_bounds__(256, 1)
   const int per = (rg.steps + nsp - 1) / nsp;
   const int round0 = min(sp * per, rg.steps), rounds = min(round0 + per, rg.steps) - round0;
 
-  // tokens of this wave's step i (one per round): [t0, t0 + count), count <= 0: none
-  auto step_tok = [&](int i, int* count) -> int {
+  // tokens of this wave in round i: [t0, t0 + count), count <= 0: none
+  auto round_tok = [&](int i, int* count) -> int {
     const int st = round0 + i;
     const int t0 = (st < rg.s0 ? st * kNRound : rg.w0 + (st - rg.s0) * kNRound) + wave * kNTok;
     *count = min(kNTok, (st < rg.s0 ? rg.n0 : rg.w1) - t0);
     return t0;
   };
   const int32_t* trow = pg.table + (int64_t)b * pg.ld;
-  // entry and slot of the step's token c16 (past the count: its last, or token 0's)
+  // entry and slot of the round's token c16 (past the count: its last, or token 0's)
   auto entry_of = [&](int i, int& off) -> const int32_t* {
     int cnt;
-    const int t0 = step_tok(i, &cnt);
+    const int t0 = round_tok(i, &cnt);
     const int t = cnt > 0 ? t0 + min(c16, cnt - 1) : 0;
     const uint32_t idx = page_index(pg, t);
     off = t - (int)idx * pg.size;
@@ -553,63 +557,58 @@ __global__ void __launch_bounds__(256, 1)
   };
   auto slot_at = [&](int i, int page, int off) -> int {
     int cnt;
-    step_tok(i, &cnt);
+    round_tok(i, &cnt);
     const int sl = slot_in(pg, page, off);
     return c16 < cnt ? sl : -1;
   };
-  uint8_t* const mine = tiles + wave * 2 * kNTile;
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(mine)));
-  const uint32_t page0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(&s_page[wave][0][0])));
+  const uint32_t lds0 = lds_addr(tiles), page0 = lds_addr(&s_page[wave][0][0]);
   auto issue_pages = [&](int i) {
     int off;
-    const int32_t* e = entry_of(min(i, rounds - 1), off);
-    const uint32_t lds = page0 + (i & 1) * 256u;
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(e) : "memory", "m0");
+    lds_load_dwords(page0 + (i & 1) * 256u, entry_of(min(i, rounds - 1), off));
   };
+  // a token without a slot brings slot 0's row, which no query weighs
   auto issue = [&](int slot, int buf) {
-    const uint32_t base = lds0 + static_cast<uint32_t>(buf * kNTile), voff = lane * 16;
+    const uint32_t base = lds0 + static_cast<uint32_t>(buf * kNTile + wave * kNTok * kVPitch);
+    const uint32_t tail = lds0 + static_cast<uint32_t>(buf * kNTile + kNTail + wave * kNTok * 128);
 #pragma unroll
     for (int j = 0; j < kNTok; ++j) {
       const int sl = max(__builtin_amdgcn_readlane(slot, j), 0);
-      const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2);
-      const uint32_t lds = base + static_cast<uint32_t>(j * kVPitch);
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src)
-                   : "memory", "m0");
+      lds_load_row(base + j * kVPitch, lane * 16, pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2));
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int k = lane >> 3;
-      const int sl = max(__shfl(slot, j * 8 + k, 64), 0);
-      const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16);
-      const uint32_t lds = base + static_cast<uint32_t>(kNTail + j * 1024);
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+      const int k = lane >> 3, sl = max(__shfl(slot, j * 8 + k, 64), 0);
+      lds_load_lanes(tail + j * 1024, pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16));
     }
   };
-  // key fragment s (32 values) of token c16: its piece 4 s + grp
+  // key fragment s (32 values) of this wave's token c16: its piece 4 s + grp
+  const uint32_t k_off = (wave * kNTok + c16) * kVPitch + grp * 16, k_tail = kNTail + (wave * kNTok + c16) * 128;
   auto kload = [&](const uint8_t* buf, int s) -> bf16x8_t {
-    return s < 16 ? ld_bf16x8(buf + c16 * kVPitch + s * 64 + grp * 16)
-                  : ld_bf16x8(buf + kNTail + c16 * 128 + (((4 * (s - 16) + grp) ^ (c16 & 7)) * 16));
+    return ld_bf16x8(buf + (s < 16 ? k_off + s * 64 : k_tail + (((4 * (s - 16) + grp) ^ (c16 & 7)) * 16)));
   };
-  // value fragment (V^T) of column tile ct: tokens 8 g .. +7
-  const uint32_t v_off = (8 * g + (c16 >> 2)) * kVPitch + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
-  auto vload = [&](const uint8_t* buf, int ct) -> bf16x8_t {
-    const uint8_t* v = buf + v_off + ct * 64;
+  // value fragment (V^T) of this wave's column tile ct, tokens 16 kk + 8 g .. +7
+  const uint32_t v_off = (8 * g + (c16 >> 2)) * kVPitch + wave * 256 + ((lane >> 4) & 1) * 32 + 8 * (lane & 3);
+  auto vload = [&](const uint8_t* buf, int kk, int ct) -> bf16x8_t {
+    const uint8_t* v = buf + v_off + kk * 16 * kVPitch + ct * 64;
     return ld_tr8(v, v + 4 * kVPitch);
   };
 
-  f32x16_t acc[16];   // [column tile]: O^T[col][query col]
-  float mx[2] = {-__builtin_inff(), -__builtin_inff()}, l[2] = {0.f, 0.f};   // of queries c16, 16 + c16
+  f32x16_t acc[4];    // [column tile]: O^T[col][query col]
+  float mx[QT], l[QT];   // of queries c16, 16 + c16: the same in every wave; this lane's part of this wave's
 #pragma unroll
-  for (int c = 0; c < 16; ++c)
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[c][v] = 0.f;
+#pragma unroll
+  for (int h = 0; h < QT; ++h) {
+    mx[h] = -__builtin_inff();
+    l[h] = 0.f;
+  }
 
   if (rounds > 0) {
-    int p_row[2];
-    bf16x8_t qf[2][kNKs];
+    int p_row[QT];
+    bf16x8_t qf[QT][kNKs];
     int slot;
-    uint32_t ok;
-    bool any_before = false;           // the accumulators hold something
     {
       int off0;
       const int page = *entry_of(0, off0);
@@ -618,80 +617,85 @@ __global__ void __launch_bounds__(256, 1)
       issue(slot, 0);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < QT; ++h) {
       const int m = min(16 * h + c16, M - 1), mr = m / H, mh = m - mr * H;   // past the end: the last one again
       p_row[h] = sr.pos0 + mr;
       const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + grp * 16;
 #pragma unroll
       for (int s = 0; s < kNKs; ++s) qf[h][s] = ld_bf16x8(qp + s * 64);
     }
-    __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): step 0, the entries of step 1, the queries
     for (int i = 0; i < rounds; ++i) {
-      const uint8_t* buf = mine + (i & 1) * kNTile;
+      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's rows of round i, the entries of round i + 1
+      asm volatile("" ::: "memory");
+      const uint8_t* buf = tiles + (i & 1) * kNTile;
       int cnt;
-      const int t0 = step_tok(i, &cnt);
-      ok = (uint32_t)__ballot(slot >= 0) & 0xffffu;
-      // step i + 1 starts loading (its buffer's step is done), its entries are in
-      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00 | (kNLoads & 15) | ((kNLoads >> 4) << 14));
-      asm volatile("" ::: "memory");
-      {
-        int off;
-        const int j = min(i + 1, rounds - 1);
-        entry_of(j, off);
-        const int sl = slot_at(j, s_page[wave][(i + 1) & 1][lane], off);
-        slot = i + 1 < rounds ? sl : -1;
-      }
-      issue_pages(i + 2);
-      issue(slot, (i + 1) & 1);
-      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00 | ((kNLoads + 1) & 15) | (((kNLoads + 1) >> 4) << 14));   // step i is in
-      asm volatile("" ::: "memory");
-      if (cnt <= 0) continue;
-
-      f32x4_t st[2] = {f32x4_t{0.f, 0.f, 0.f, 0.f}, f32x4_t{0.f, 0.f, 0.f, 0.f}};
+      const int t0 = round_tok(i, &cnt);
+      const uint32_t ok = (uint32_t)__ballot(slot >= 0) & 0xffffu;
+      f32x4_t st[QT];
+#pragma unroll
+      for (int h = 0; h < QT; ++h) st[h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       bf16x8_t kb[kNKD];
 #pragma unroll
       for (int s = 0; s < kNKD; ++s) kb[s] = kload(buf, s);
 #pragma unroll
       for (int s = 0; s < kNKs; ++s) {
-        st[0] = mfma16(kb[s % kNKD], qf[0][s], st[0]);
-        st[1] = mfma16(kb[s % kNKD], qf[1][s], st[1]);
+#pragma unroll
+        for (int h = 0; h < QT; ++h) st[h] = mfma16(kb[s % kNKD], qf[h][s], st[h]);
         if (s + kNKD < kNKs) kb[s % kNKD] = kload(buf, s + kNKD);
         __builtin_amdgcn_sched_barrier(0);
       }
-      bf16x8_t vf[4];
+      float tmax[QT];
+      bool poison = false;   // a score that does not count is not finite: its row holds infinities or NaN
+      {
+        const bool whole = ok == 0xffffu && t0 + kNTok - 1 <= sr.pos0 &&
+                           (window == 0 || t0 > sr.pos0 + sr.n - 1 - window || t0 + kNTok <= n_sink);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) vf[c] = vload(buf, c);
-      const bool full = ok == 0xffffu && t0 + kNTok - 1 <= sr.pos0 &&
-                        (window == 0 || t0 > sr.pos0 + sr.n - 1 - window || t0 + kNTok <= n_sink);
-      bool poison = false;
-      float alpha[2];
-      uint32_t pk[2][2];
+        for (int h = 0; h < QT; ++h) {
+          const uint32_t bits = whole ? 0xffffu : (sees_bits(p_row[h], t0, window, n_sink) & ok);
+          tmax[h] = -__builtin_inff();
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float x = st[h][v] * scale2;
+            const bool seen = (bits >> (4 * grp + v)) & 1;
+            poison |= !seen && !(fabsf(x) < __builtin_inff());
+            st[h][v] = seen ? x : -__builtin_inff();
+            tmax[h] = fmaxf(tmax[h], st[h][v]);
+          }
+          tmax[h] = quad_max(tmax[h]);
+        }
+      }
+      s_x[wave][col] = QT == 2 && hi ? tmax[QT - 1] : tmax[0];   // lanes l and l ^ 32 write the same
+      s_poison[wave] = __any(poison);
+      __syncthreads();
+      // every wave has left round i - 1: its buffer takes round i + 1
+      int next = -1;
+      if (i + 1 < rounds) {
+        int off;
+        entry_of(i + 1, off);
+        next = slot_at(i + 1, s_page[wave][(i + 1) & 1][lane], off);
+        issue_pages(i + 2);
+        issue(next, (i + 1) & 1);
+      }
+      float alpha[QT];
+      uint32_t pk[2][2] = {{0u, 0u}, {0u, 0u}};
       bool grown = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t bits = full ? 0xffffu : (sees_bits(p_row[h], t0, window, n_sink) & ok);
-        float x[4], tmax = -__builtin_inff();
+      for (int h = 0; h < QT; ++h) {
+        float top = s_x[0][16 * h + c16];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float sc = st[h][v] * scale2;
-          const bool seen = (bits >> (4 * grp + v)) & 1;
-          poison |= !seen && !(fabsf(sc) < __builtin_inff());
-          x[v] = seen ? sc : -__builtin_inff();
-          tmax = fmaxf(tmax, x[v]);
-        }
-        tmax = quad_max(tmax);
-        const bool grow = __any(tmax > mx[h] + 8.f);   // as in the 128-query kernel
-        const float mn = grow ? fmaxf(mx[h], tmax) : mx[h];
+        for (int w = 1; w < 4; ++w) top = fmaxf(top, s_x[w][16 * h + c16]);
+        const bool grow = __any(top > mx[h] + 8.f);            // as in the 128-query kernel; alike in every wave
+        const float mn = grow ? fmaxf(mx[h], top) : mx[h];
         const float ref = mn == -__builtin_inff() ? 0.f : mn;
         alpha[h] = grow ? __builtin_amdgcn_exp2f(mx[h] - ref) : 1.f;
         grown |= grow;
-        float psum = 0.f;
+        float p[4], psum = 0.f;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          x[v] = __builtin_amdgcn_exp2f(x[v] - ref);
-          psum += x[v];
+          p[v] = __builtin_amdgcn_exp2f(st[h][v] - ref);
+          psum += p[v];
         }
-        const bf16x4_t pb = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        const bf16x4_t pb = {(__bf16)p[0], (__bf16)p[1], (__bf16)p[2], (__bf16)p[3]};
         const uint2 u = __builtin_bit_cast(uint2, pb);
         pk[h][0] = u.x;
         pk[h][1] = u.y;
@@ -700,104 +704,60 @@ __global__ void __launch_bounds__(256, 1)
       }
       // Lane group r holds tokens 4 r .. +3 of queries c16 and 16 + c16; after
       // the swaps lane l holds tokens 8 g .. +7 of query l % 32.
-      const auto s01 = __builtin_amdgcn_permlane16_swap(pk[0][0], pk[1][0], false, false);
-      const auto s23 = __builtin_amdgcn_permlane16_swap(pk[0][1], pk[1][1], false, false);
-      const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, u32x4_t{s01[0], s23[0], s01[1], s23[1]});
-      if (grown && any_before) {
-        mfma32_acc_done();
-        const float a = (lane & 16) ? alpha[1] : alpha[0];
+      {
+        const auto s01 = __builtin_amdgcn_permlane16_swap(pk[0][0], pk[1][0], false, false);
+        const auto s23 = __builtin_amdgcn_permlane16_swap(pk[0][1], pk[1][1], false, false);
+        *reinterpret_cast<u32x4_t*>(s_p + wave * 1024 + lane * 16) = u32x4_t{s01[0], s23[0], s01[1], s23[1]};
+      }
+      if (grown && i > 0) {
+        const float a = QT == 2 && hi ? alpha[QT - 1] : alpha[0];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          asm volatile("" : "+a"(acc[c]));   // one accumulator at a time leaves its registers
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[c][v] *= a;
-          asm volatile("" : "+a"(acc[c]));
-        }
-        asm volatile("s_nop 7");
       }
-      if (__any(poison)) {
-        // as in the 128-query kernel: values that are not finite become 0
-        uint8_t* wbuf = mine + (i & 1) * kNTile;
-        for (int y = lane; y < kNTok * 64; y += 64) {
-          uint16_t* e = reinterpret_cast<uint16_t*>(wbuf + (y >> 6) * kVPitch + (y & 63) * 16);
+      __syncthreads();                            // P, and every wave's rows, are there
+      if (s_poison[0] | s_poison[1] | s_poison[2] | s_poison[3]) {
+        // as in the 128-query kernel: values that are not finite become 0, each
+        // wave in its columns
+        uint8_t* wbuf = tiles + (i & 1) * kNTile + wave * 256;
+        for (int y = lane; y < kNRound * 16; y += 64) {
+          uint16_t* e = reinterpret_cast<uint16_t*>(wbuf + (y >> 4) * kVPitch + (y & 15) * 16);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-        for (int c = 0; c < 4; ++c) vf[c] = vload(buf, c);
       }
-      any_before = true;
+      bf16x8_t pf[4], vf[4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) pf[kk] = ld_bf16x8(s_p + kk * 1024 + lane * 16);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) vf[x] = vload(buf, 0, x);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        mfma32_acc(acc[c], vf[c & 3], pf);
-        if (c + 4 < 16) vf[c & 3] = vload(buf, c + 4);
+      for (int x = 0; x < 16; ++x) {
+        acc[x & 3] = mfma32(vf[x & 3], pf[x >> 2], acc[x & 3]);
+        if (x + 4 < 16) vf[x & 3] = vload(buf, (x + 4) >> 2, x & 3);
         __builtin_amdgcn_sched_barrier(0);
       }
+      slot = next;
     }
   }
-  __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // no load is under way when the buffers change hands
-  mfma32_acc_done();
 
-  // the four waves' states: query l % 32 of every lane
+  // the waves' sums: query l % 32 of every lane
+  __syncthreads();                                // s_x of the last round is read
   {
-    const float l0 = quad_sum(l[0]), l1 = quad_sum(l[1]);
-    const bool hi = (lane & 16) != 0;
-    if (lane < kNM) s_ml[wave][lane] = make_float2(hi ? mx[1] : mx[0], hi ? l1 : l0);
+    float x = quad_sum(l[0]);
+    if (QT == 2) {
+      const float y = quad_sum(l[QT - 1]);
+      x = hi ? y : x;
+    }
+    s_x[wave][col] = x;
   }
   __syncthreads();
-  float top = -__builtin_inff(), den = 0.f, f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w][col].x);
-  const float ref = top == -__builtin_inff() ? 0.f : top;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float2 ml = s_ml[w][col];
-    den += ml.y == 0.f ? 0.f : exp2f(ml.x - ref) * ml.y;   // a wave that saw nothing: (-inf, 0)
-  }
-  f = s_ml[wave][col].y == 0.f ? 0.f : exp2f(s_ml[wave][col].x - ref);
-  // wave w ends up with value columns 128 w .. +127 of all waves: two quarters
-  // cross at a time (128 KiB of the buffers)
-  f32x16_t res[4];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int quarter = half * 2 + u;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f32x16_t x = acc[quarter * 4 + c];
-#pragma unroll
-        for (int v = 0; v < 16; ++v) x[v] *= f;
-        if (wave == quarter) {
-          res[c] = x;
-        } else {
-          f32x4_t* to = reinterpret_cast<f32x4_t*>(tiles + ((wave * 2 + u) * 4 + c) * 4096 + lane * 16);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) to[j * 64] = f32x4_t{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
-        }
-      }
-    }
-    __syncthreads();
-    if ((wave >> 1) == half) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int w = 1; w < 4; ++w) {   // the others in ring order
-          const f32x4_t* from =
-              reinterpret_cast<const f32x4_t*>(tiles + ((((wave + w) & 3) * 2 + (wave & 1)) * 4 + c) * 4096 + lane * 16);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4_t x = from[j * 64];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) res[c][4 * j + e] += x[e];
-          }
-        }
-    }
-    __syncthreads();
-  }
+  const float den = (s_x[0][col] + s_x[1][col]) + (s_x[2][col] + s_x[3][col]);
+  const float top = QT == 2 && hi ? mx[QT - 1] : mx[0];
   if (nsp > 1) {
     if (wave == 0 && g == 0) part_ml[(int64_t)blockIdx.x * kMT + col] = make_float2(top, den);
     f32x4_t* o = part_at(part_o, blockIdx.x, row_tiles, 0, wave) + lane;
@@ -805,20 +765,20 @@ __global__ void __launch_bounds__(256, 1)
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o[(c * 4 + j) * 64] = f32x4_t{res[c][4 * j], res[c][4 * j + 1], res[c][4 * j + 2], res[c][4 * j + 3]};
+        o[(c * 4 + j) * 64] = f32x4_t{acc[c][4 * j], acc[c][4 * j + 1], acc[c][4 * j + 2], acc[c][4 * j + 3]};
     return;
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
   if (lse && wave == 0 && g == 0 && col < M)
     lse[mg0 + col] = den == 0.f ? -__builtin_inff() : (top + log2f(den)) * 0.69314718055994531f;
-  uint8_t* const t = tiles + wave * (32 * kOutPitch);
+  uint8_t* const t = tiles + wave * (32 * kOutPitch);   // every wave has left the buffers
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       bf16x4_t x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = (__bf16)(res[c][4 * j + e] * inv);
+      for (int e = 0; e < 4; ++e) x[e] = (__bf16)(acc[c][4 * j + e] * inv);
       *reinterpret_cast<uint2*>(t + col * kOutPitch + c * 64 + j * 16 + g * 8) = __builtin_bit_cast(uint2, x);
     }
   store_columns(out + mg0 * kPagedVal + wave * 128, t, M, 32, lane);
@@ -922,7 +882,7 @@ bool shape_ok(int B, int T, int H, int max_rows, int max_len, int window, int n_
 }  // namespace
 
 extern "C" size_t ech_paged_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
-  if (!shape_ok(B, T, H, max_rows, max_len, window, n_sink)) return 0;
+  if (!shape_ok(B, T, H, max_rows, max_len, window, n_sink) || T == 0 || max_rows == 0) return 0;
   return split_of(B, T, H, max_rows, max_len, window, n_sink).bytes;
 }
 
@@ -949,7 +909,9 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   float2* part_ml = sp.planned ? reinterpret_cast<float2*>(w + sp.part_ml) : nullptr;
   PartInfo* info = sp.planned ? reinterpret_cast<PartInfo*>(w + sp.info) : nullptr;
   const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
-  hipLaunchKernelGGL((sp.narrow ? paged_attn_narrow_kernel : paged_attn_kernel), dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
+  const int64_t queries = (int64_t)std::min(max_rows, T) * H;
+  const auto kernel = !sp.narrow ? paged_attn_kernel : queries <= 16 ? paged_attn_narrow_kernel<1> : paged_attn_narrow_kernel<2>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
                      static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg,
                      row0, seq_len, B, T, H, max_rows, max_len, window, n_sink, sm_scale * 1.4426950408889634f,
                      sp.planned ? (int)sp.tiles : 0, sp.row_tiles, static_cast<uint16_t*>(out), lse, part_o, part_ml, info);
