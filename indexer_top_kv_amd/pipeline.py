@@ -30,6 +30,12 @@ Prefill (ECHO explainer, "Prefill: one-round histogram"): query blocks are
 scored one after another; the recall of block i runs on S1 while S0 scores
 block i+1.
 
+Resident layers (PagedLayer): a layer whose rows all stay on the device, in
+pages of a pool (contexts below k tokens, where a selection would take every
+token anyway; windowed layers; caches held to a budget of tokens). One step
+takes any mix of prompt chunks and single tokens: append, attention over the
+pages, and with a budget the received weights and the eviction by them.
+
 Nothing here computes: this module sizes buffers with torch, chooses the
 order of the C-ABI calls and the stream events between them.
 """
@@ -43,7 +49,9 @@ import torch
 from . import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, LayerState, ech_cache_reset, ech_cache_step,
                ech_cache_step_ws_bytes, ech_index_logits, ech_index_logits_causal, ech_index_logits_early,
                ech_index_logits_early_ws_bytes, ech_kv_append, ech_recall, ech_recall_early_live, ech_recall_rest,
-               ech_topk, ech_topk_early, ech_topk_ws_bytes)
+               ech_topk, ech_topk_early, ech_topk_ws_bytes, ech_paged_append, ech_paged_attn,
+               ech_paged_attn_ws_bytes, ech_paged_evict, ech_paged_evict_ws_bytes, ech_paged_weight,
+               ech_paged_weight_ws_bytes)
 
 
 def round_up(x: int, m: int) -> int:
@@ -609,3 +617,167 @@ class DecodeStack:
     def replay(self, qs) -> None:
         """One L-layer step through the captured graphs (current stream)."""
         self._run(qs, graphs=True)
+
+
+class PageTables:
+    """Host side of a paged pool: which pages each sequence holds, in token
+    order, and which are free. `table` [B, per_seq] int32 is what the kernels
+    read (a copy of it goes to the device); entries past a sequence's pages are
+    -1."""
+
+    def __init__(self, B: int, n_pages: int, page_size: int, per_seq: int):
+        self.page_size, self.n_pages, self.per_seq = page_size, n_pages, per_seq
+        self.table = np.full((B, per_seq), -1, np.int32)
+        self.held = np.zeros(B, np.int64)
+        self.free = list(range(n_pages - 1, -1, -1))
+
+    def need(self, lens) -> np.ndarray:
+        """Pages that sequences of these lengths hold."""
+        return -(-np.asarray(lens, np.int64) // self.page_size)
+
+    def resize(self, lens) -> bool:
+        """Give every sequence the pages of its length, taking free ones and
+        returning those it no longer needs; True if the table changed. Raises,
+        with nothing changed, if a sequence or the pool cannot hold them."""
+        need = self.need(lens)
+        if np.any(need > self.per_seq):
+            raise ValueError(f'a sequence needs {int(need.max())} pages, its table has {self.per_seq}')
+        if int((need - self.held).sum()) > len(self.free):
+            raise ValueError(f'{int((need - self.held).sum())} more pages needed, {len(self.free)} are free')
+        changed = np.flatnonzero(need != self.held)
+        for b in changed[np.argsort((need - self.held)[changed])]:     # those that shrink first
+            have, n = int(self.held[b]), int(need[b])
+            if n < have:
+                self.free.extend(int(p) for p in self.table[b, n:have][::-1])
+                self.table[b, n:have] = -1
+            else:
+                for i in range(have, n):
+                    self.table[b, i] = self.free.pop()
+            self.held[b] = n
+        return len(changed) > 0
+
+
+class PagedLayer:
+    """One resident layer: its pool of pages, page tables and buffers.
+
+    step(q, rows, counts) takes the step's new rows of all sequences, counts[b]
+    of them for sequence b (zero, one or a chunk) one after another: they join
+    the pages, attend (causal; window and n_sink as in ech_paged_attn), and
+    the step returns out [T, H, 512] bf16 and lse [T, H]. With a budget the
+    rows' received weights join a running sum (times decay each step), and
+    sequences longer than budget + slack are cut down to budget tokens: the
+    first n_sink, the last n_recent, and the heaviest between.
+
+    The host knows every length (an eviction leaves budget tokens), so nothing
+    waits for the device. place(counts) does the host's part, launch(q, rows)
+    the step's kernels, trim() the eviction; a launch of the same T may be
+    captured and replayed, the tables and lengths being read in place. The
+    buffers a step returns are the layer's: the next step of the same T
+    writes them again. Steps of one layer must be ordered."""
+
+    def __init__(self, B: int, H: int, n_pages: int, max_len: int, max_rows: int, page_size: int = 64,
+                 sm_scale: float = 1.0 / 192.0 ** 0.5, window: int = 0, n_sink: int = 0,
+                 budget: Optional[int] = None, n_recent: int = 0, slack: int = 0, decay: float = 1.0, device='cuda'):
+        if budget is not None and (budget < 1 or n_sink + n_recent > budget or slack < 0):
+            raise ValueError('budget must hold n_sink + n_recent tokens, slack must not be negative')
+        self.B, self.H, self.max_len, self.max_rows = B, H, max_len, max_rows
+        self.sm_scale, self.window, self.n_sink = sm_scale, window, n_sink
+        self.budget, self.n_recent, self.slack, self.decay = budget, n_recent, slack, decay
+        self.pages = PageTables(B, n_pages, page_size, -(-max_len // page_size))
+        dev = dict(device=device)
+        self.device = torch.device(device)
+        self.pool = torch.zeros((n_pages * page_size, 576), dtype=torch.bfloat16, **dev)
+        self.table = torch.from_numpy(self.pages.table).to(**dev)
+        self.lens = np.zeros(B, np.int64)
+        self.row0 = torch.zeros(B + 1, dtype=torch.int32, **dev)
+        self.seq_len = torch.zeros(B, dtype=torch.int32, **dev)
+        self.status = torch.zeros(1, dtype=torch.int32, **dev)
+        self.acc = torch.zeros((B, max_len), dtype=torch.float32, **dev) if budget is not None else None
+        self.kept = torch.empty((B, budget), dtype=torch.int32, **dev) if budget is not None else None
+        self.evict_ws = (torch.empty(ech_paged_evict_ws_bytes(B, max_len, budget), dtype=torch.uint8, **dev)
+                         if budget is not None else None)
+        self._bufs = {}
+
+    def _buffers(self, T: int):
+        if T not in self._bufs:
+            dev = dict(device=self.device)
+            R = min(self.max_rows, T)
+            ws = ech_paged_attn_ws_bytes(self.B, T, self.H, R, self.max_len, self.window, self.n_sink)
+            if self.budget is not None:     # the two calls run one after the other: one workspace
+                ws = max(ws, ech_paged_weight_ws_bytes(self.B, T, self.H, R, self.max_len))
+            self._bufs[T] = (torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
+                             torch.empty((T, self.H), dtype=torch.float32, **dev),
+                             torch.empty(ws, dtype=torch.uint8, **dev))
+        return self._bufs[T]
+
+    def place(self, counts) -> int:
+        """Pages and lengths of a step that brings counts[b] rows to sequence
+        b; returns T. Raises, with nothing changed, if they do not fit."""
+        counts = np.asarray(counts, np.int64)
+        if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > self.max_rows):
+            raise ValueError(f'counts must be {self.B} numbers from 0 to max_rows = {self.max_rows}')
+        lens = self.lens + counts
+        if np.any(lens > self.max_len):
+            raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
+        if self.pages.resize(lens):
+            self.table.copy_(torch.from_numpy(self.pages.table))
+        self.lens = lens
+        off = np.zeros(self.B + 1, np.int32)
+        np.cumsum(counts, out=off[1:])
+        self.row0.copy_(torch.from_numpy(off))
+        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        return int(off[-1])
+
+    def launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
+        """The kernels of the step that place() prepared: q [T, H, 576], rows
+        [T, 576] bf16 -> (out, lse)."""
+        T, ps = q.shape[0], self.pages.page_size
+        out, lse, ws = self._buffers(T)
+        ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
+        ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
+                       self.sm_scale, out, lse, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+        if self.budget is not None:
+            ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
+                             self.sm_scale, self.acc, self.acc, decay=self.decay, window=self.window,
+                             n_sink=self.n_sink, ws=ws, stream=stream)
+        return out, lse
+
+    def trim(self, stream=None) -> bool:
+        """Cut sequences longer than budget + slack down to budget tokens (all
+        that are longer than budget go with them); True if any was."""
+        if self.budget is None or not np.any(self.lens > self.budget + self.slack):
+            return False
+        ech_paged_evict(self.acc, self.seq_len, self.max_len, self.budget, self.n_sink, self.n_recent, self.kept,
+                        self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
+                        page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
+        self.lens = np.minimum(self.lens, self.budget)
+        if self.pages.resize(self.lens):
+            with torch.cuda.stream(_as_stream(stream, self.device)):
+                self.table.copy_(torch.from_numpy(self.pages.table))
+        return True
+
+    def step(self, q: torch.Tensor, rows: torch.Tensor, counts):
+        """place, launch and trim on the current stream; returns (out, lse)."""
+        T = self.place(counts)
+        if q.shape[0] != T or rows.shape[0] != T:
+            raise ValueError(f'counts name {T} rows, q has {q.shape[0]} and rows {rows.shape[0]}')
+        got = self.launch(q, rows)
+        self.trim()
+        return got
+
+    def release(self, b: int) -> None:
+        """Sequence b ends: its pages are free and its place starts empty."""
+        lens = self.lens.copy()
+        lens[b] = 0
+        self.pages.resize(lens)
+        self.lens = lens
+        self.table.copy_(torch.from_numpy(self.pages.table))
+        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        if self.acc is not None:
+            self.acc[b].zero_()
+
+
+def _as_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)

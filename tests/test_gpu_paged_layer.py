@@ -1,0 +1,156 @@
+"""PagedLayer: append, attention, received weight and eviction as a model's
+layer calls them, step after step, against the oracle run the same way: the
+oracle keeps each sequence's rows as a plain list. Tolerances as in
+test_gpu_paged.py; the kept tokens have to be exactly those that the layer's own
+weights rank first."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads as wk
+from gpu_util import dev, host, need_gpu
+from indexer_top_kv_amd.pipeline import PagedLayer
+from test_gpu_paged import U, check_attn
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / np.sqrt(192.0)
+
+
+class Model:
+    """The oracle's side: rows of every sequence in order, and their weights."""
+
+    def __init__(self, B):
+        self.rows = [np.zeros((0, 576), np.uint16) for _ in range(B)]
+
+    def dense(self):
+        """(pool, table, lengths) with one page per sequence."""
+        n = max(max(len(r) for r in self.rows), 1)
+        pool = np.zeros((len(self.rows) * n, 576), np.uint16)
+        for b, r in enumerate(self.rows):
+            pool[b * n:b * n + len(r)] = r
+        return pool, np.arange(len(self.rows))[:, None], n, np.array([len(r) for r in self.rows])
+
+
+def run(layer, steps, seed, window, sink):
+    r = np.random.default_rng(seed)
+    B, H = layer.B, layer.H
+    m = Model(B)
+    acc = np.zeros((B, layer.max_len))
+    slack_err = np.zeros((B, layer.max_len))
+    trimmed = 0
+    for i, counts in enumerate(steps):
+        T = sum(counts)
+        q = wk.to_bf16_bits(r.standard_normal((T, H, 576)).astype(np.float32))
+        x = wk.to_bf16_bits(r.standard_normal((T, 576)).astype(np.float32))
+        row0 = np.concatenate([[0], np.cumsum(counts)])
+        Tn = layer.place(counts)
+        assert Tn == T
+        out, lse = layer.launch(dev(q).view(torch.bfloat16), dev(x).view(torch.bfloat16))
+        got = out.float().cpu().numpy(), host(lse)
+        for b in range(B):
+            m.rows[b] = np.concatenate([m.rows[b], x[row0[b]:row0[b + 1]]])
+        pool, table, page, lens = m.dense()
+        assert np.array_equal(lens, layer.lens)
+        ref = oracle.paged.attention(q, pool, table, page, row0, lens, SCALE, window, sink)
+        check_attn(got, ref, int(lens.max()), f'step {i}')
+        if layer.budget is None:
+            continue
+        L = layer.max_len
+        acc = oracle.paged.received(q, got[1], pool, table, page, row0, lens, SCALE, acc, layer.decay, window, sink)
+        mag = ref[3].max() if T else 0.0
+        de = 576 * U * mag + 8 * U * (1 + mag)
+        slack_err = slack_err * layer.decay + acc * (de * 1.01 + (layer.max_rows * H + 4) * U) + 1e-30
+        a_gpu = host(layer.acc)
+        for b in range(B):
+            assert np.all(np.abs(a_gpu[b, :lens[b]] - acc[b, :lens[b]]) <= slack_err[b, :lens[b]]), f'step {i}'
+        if layer.trim():
+            trimmed += 1
+            torch.cuda.synchronize()
+            kept = oracle.paged.evict(a_gpu, lens, layer.budget, layer.n_sink, layer.n_recent)
+            new_acc, new_err = np.zeros((B, L)), np.zeros((B, L))
+            for b in range(B):
+                n = len(kept[b])
+                np.testing.assert_array_equal(host(layer.kept)[b, :n], kept[b])
+                m.rows[b] = m.rows[b][kept[b]]
+                new_acc[b, :n], new_err[b, :n] = acc[b, kept[b]], slack_err[b, kept[b]]
+            acc, slack_err = new_acc, new_err
+            np.testing.assert_array_equal(host(layer.seq_len), [len(k) for k in kept])
+        held = layer.pages.need(layer.lens)
+        assert np.array_equal(held, layer.pages.held)
+        assert len(layer.pages.free) == layer.pages.n_pages - held.sum()
+    assert int(layer.status.item()) == 0
+    return trimmed
+
+
+STEPS = [[40, 0, 7], [1, 90, 1], [0, 0, 33], [1, 1, 1], [64, 1, 0], [1, 1, 1], [1, 1, 100], [1, 1, 1], [1, 1, 1]]
+
+
+@pytest.mark.parametrize('page,window,sink', [(16, 0, 0), (24, 50, 4), (1, 0, 0)])
+def test_steps_without_a_budget(page, window, sink):
+    need_gpu()
+    layer = PagedLayer(3, 16, n_pages=3 * (-(-260 // page)), max_len=260, max_rows=100, page_size=page, window=window,
+                       n_sink=sink)
+    run(layer, STEPS, 1, window, sink)
+
+
+@pytest.mark.parametrize('page,window,H,slack', [(16, 0, 16, 0), (7, 0, 4, 10), (16, 40, 2, 0), (64, 0, 64, 0)])
+def test_steps_with_a_budget(page, window, H, slack):
+    need_gpu()
+    layer = PagedLayer(3, H, n_pages=3 * (-(-200 // page)), max_len=200, max_rows=100, page_size=page, window=window,
+                       n_sink=3, budget=60, n_recent=20, slack=slack, decay=0.9)
+    assert run(layer, STEPS, 2 + page, window, 3) >= 2
+
+
+def test_captured_decode_steps_follow_the_tables():
+    """The launch of a decode step captured once; place() between the replays
+    moves lengths and pages, and every replay equals an eager layer's step,
+    with eager work between the replays."""
+    need_gpu()
+    r = np.random.default_rng(5)
+    mk = lambda: PagedLayer(2, 16, n_pages=80, max_len=600, max_rows=300, page_size=16, budget=500, n_recent=8)  # noqa: E731
+    a, b = mk(), mk()
+    bits = lambda *s: dev(wk.to_bf16_bits(r.standard_normal(s).astype(np.float32))).view(torch.bfloat16)  # noqa: E731
+    q0, x0 = bits(400, 16, 576), bits(400, 576)
+    for layer in (a, b):
+        layer.step(q0, x0, [270, 130])
+    q, x = bits(2, 16, 576), bits(2, 576)
+    for layer in (a, b):                        # warm-up outside the capture, buffers of T = 2
+        layer.step(q, x, [1, 1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = a.launch(q, x)
+    for i in range(6):
+        q.copy_(bits(2, 16, 576))
+        x.copy_(bits(2, 576))
+        a.place([1, 1])
+        g.replay()
+        o2, l2 = b.step(q, x, [1, 1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.equal(a.acc, b.acc), i
+        y = torch.arange(4096, device='cuda', dtype=torch.float32)
+        assert float((y * 2).sum().item()) == 4096 * 4095
+    assert torch.equal(a.pool, b.pool)
+
+
+def test_release_and_refusals():
+    need_gpu()
+    layer = PagedLayer(2, 4, n_pages=8, max_len=100, max_rows=64, page_size=16, budget=50)
+    z = lambda n: (torch.zeros((n, 4, 576), dtype=torch.bfloat16, device='cuda'),  # noqa: E731
+                   torch.zeros((n, 576), dtype=torch.bfloat16, device='cuda'))
+    layer.step(*z(64), [64, 0])                 # cut to 50: 4 pages
+    assert layer.lens.tolist() == [50, 0] and len(layer.pages.free) == 4
+    before = layer.pages.table.copy()
+    for counts in ([65, 0], [1], [-1, 0], [0, 64 + 1], [51, 0]):
+        with pytest.raises(ValueError):
+            layer.place(counts)
+    with pytest.raises(ValueError):
+        layer.place([40, 64])                   # 6 + 4 pages of 8
+    assert np.array_equal(layer.pages.table, before) and layer.lens.tolist() == [50, 0]
+    with pytest.raises(ValueError):
+        layer.step(*z(3), [2, 2])
+    layer.release(0)
+    assert layer.lens[0] == 0
+    layer.step(*z(64), [0, 64])
+    with pytest.raises(ValueError):
+        PagedLayer(1, 4, 4, 64, 8, n_sink=40, n_recent=30, budget=60)

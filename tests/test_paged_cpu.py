@@ -104,3 +104,27 @@ def test_oracle_evict_by_brute_force():
             inn = [t for t in mid if t in got]
             for t in set(mid) - set(got):
                 assert all((acc[0, u], -u) > (acc[0, t], -t) for u in inn)
+
+
+def test_page_tables():
+    """Pages are given, returned and never held twice; a request that does not
+    fit changes nothing."""
+    from indexer_top_kv_amd.pipeline import PageTables
+    r = np.random.default_rng(4)
+    t = PageTables(4, 20, 8, 9)
+    lens = np.zeros(4, int)
+    for _ in range(300):
+        want = np.clip(lens + r.integers(-30, 40, 4), 0, 80)
+        before = (t.table.copy(), list(t.free))
+        need = -(-want // 8)
+        try:
+            t.resize(want)
+            lens = want
+        except ValueError:
+            assert need.max() > 9 or need.sum() > 20
+            assert np.array_equal(before[0], t.table) and before[1] == t.free
+        used = t.table[t.table >= 0]
+        assert len(set(used.tolist())) == len(used) and sorted(used.tolist() + t.free) == list(range(20))
+        for b in range(4):
+            n = -(-int(lens[b]) // 8)
+            assert np.all(t.table[b, :n] >= 0) and np.all(t.table[b, n:] == -1)
