@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(256, 1)
   __shared__ __align__(16) uint8_t s_p[4 * 1024];   // P: per wave's tokens, a lane's 16 bytes
   __shared__ int s_page[4][2][64];   // per wave: page-table entries of two rounds' tokens
   __shared__ float s_x[4][kNM];      // per wave: a round's maximum of each query; at the end its sum
-  __shared__ int s_poison[4];
+  __shared__ int s_poison[2][4];     // by the round's parity: a wave may write the next round's while another reads
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, col = lane & 31, g = lane >> 5;
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(256, 1)
         }
       }
       s_x[wave][col] = QT == 2 && hi ? tmax[QT - 1] : tmax[0];   // lanes l and l ^ 32 write the same
-      s_poison[wave] = __any(poison);
+      s_poison[i & 1][wave] = __any(poison);
       __syncthreads();
       // every wave has left round i - 1: its buffer takes round i + 1
       int next = -1;
@@ -717,7 +717,8 @@ __global__ void __launch_bounds__(256, 1)
           for (int v = 0; v < 16; ++v) acc[c][v] *= a;
       }
       __syncthreads();                            // P, and every wave's rows, are there
-      if (s_poison[0] | s_poison[1] | s_poison[2] | s_poison[3]) {
+      const int* const bad = s_poison[i & 1];
+      if (bad[0] | bad[1] | bad[2] | bad[3]) {
         // as in the 128-query kernel: values that are not finite become 0, each
         // wave in its columns
         uint8_t* wbuf = tiles + (i & 1) * kNTile + wave * 256;
@@ -865,7 +866,7 @@ Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n
   sp.tiles = tiles_of(B, T, H, max_rows, per);
   int64_t seen = max_len;                                  // tokens a tile can read
   if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1 + kStepTok);
-  sp.planned = sp.tiles <= kCus && B <= kPlanSeqs && seen > kMinSpan * kStepTok;
+  sp.planned = sp.tiles <= kCus && seen > kMinSpan * kStepTok && plan_fits(B, sp.tiles, seen);
   if (!sp.planned) return sp;
   sp.row_tiles = (int)((std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H) + 31) / 32);
   sp.part_ml = (size_t)kCus * sp.row_tiles * 32 * kPagedVal * sizeof(float);
