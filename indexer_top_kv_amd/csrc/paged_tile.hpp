@@ -95,6 +95,12 @@ constexpr int kCus = 256;
 constexpr int kMinSpan = 4;          // steps a span is worth its start and its partial
 constexpr int kPlanSeqs = 256;       // sequences a plan covers (four per lane)
 
+// Whether a plan covers B sequences, and its sums, steps of so many tiles that
+// read up to `tokens` each, stay in 31 bits.
+inline bool plan_fits(int B, int64_t tiles, int64_t tokens) {
+  return B <= kPlanSeqs && tiles * (tokens / kStepTok + 1) < (1ll << 30);
+}
+
 __device__ __forceinline__ int lanes_max(int x) {           // x >= 0
   x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
   x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));

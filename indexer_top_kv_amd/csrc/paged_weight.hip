@@ -508,7 +508,7 @@ extern "C" int ech_paged_weight(const void* q, int64_t q_row_stride, int64_t q_h
       acc_in = acc_out;
       decay = 1.f;
     }
-    const bool planned = B <= kCus && B <= kPlanSeqs;
+    const bool planned = B <= kCus && plan_fits(B, B, max_len);
     hipLaunchKernelGGL(paged_weight_stream_kernel, dim3(planned ? kCus : B), dim3(256), 0, s,
                        static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, lse,
                        static_cast<const uint8_t*>(pool), pg, row0, seq_len, B, T, H, max_rows, max_len, window, n_sink,

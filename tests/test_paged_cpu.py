@@ -128,3 +128,11 @@ def test_page_tables():
         for b in range(4):
             n = -(-int(lens[b]) // 8)
             assert np.all(t.table[b, :n] >= 0) and np.all(t.table[b, n:] == -1)
+
+
+def test_workspace_of_long_batches():
+    """A batch whose steps would not fit the plan's 31-bit sums is not split,
+    and needs no workspace; a shorter one is and does."""
+    assert ech.ech_paged_attn_ws_bytes(256, 256, 128, 1, 1 << 20) > 0
+    assert ech.ech_paged_attn_ws_bytes(256, 256, 128, 1, 1 << 30) == 0
+    assert ech.ech_paged_attn_ws_bytes(1, 1, 128, 1, 1 << 30) > 0
