@@ -24,8 +24,8 @@ __global__ void __launch_bounds__(256)
     if (c < 64) break;
   }
   if (b >= B) return;                                       // behind the last sequence
-  const int pos = seq_len[b] - (row0[b + 1] - t);
-  const int slot = pos >= 0 ? slot_of(pg, pg.table + (int64_t)b * pg.ld, pos) : -1;
+  const int64_t pos = (int64_t)seq_len[b] - row0[b + 1] + t;   // < seq_len: row0[b + 1] > t
+  const int slot = pos >= 0 ? slot_of(pg, pg.table + (int64_t)b * pg.ld, (int)pos) : -1;
   if (slot < 0) {
     if (status && lane == 0) atomicOr(status, ECH_ST_FULL);
     return;
