@@ -273,22 +273,25 @@ _current_device = getattr(torch._C, '_cuda_getDevice', torch.cuda.current_device
 
 
 def _arg(name: str, t: torch.Tensor, dtypes, shape, device: int, rows: bool = False) -> None:
-    """Refuse a tensor that the kernels would misread: its type, shape (None:
-    any), device, or strides (`rows`: only the last dimension is dense)."""
-    if (t.dtype in dtypes and t.get_device() == device >= 0 and (t.shape == shape or _fits(t.shape, shape))
+    """Refuse a tensor that the kernels would misread: its type, shape, device,
+    or strides (`rows`: only the last dimension is dense)."""
+    if (t.dtype in dtypes and t.get_device() == device >= 0 and t.shape == shape
             and (t.is_contiguous() or (rows and t.stride(-1) == 1))):
         return
     if t.dtype not in dtypes:
         raise TypeError(f'{name}: unsupported dtype {t.dtype}')
-    if not _fits(t.shape, shape):
-        raise ValueError(f'{name}: shape {tuple(t.shape)}, expected {tuple("any" if w is None else w for w in shape)}')
+    if t.shape != shape:
+        raise ValueError(f'{name}: shape {tuple(t.shape)}, expected {tuple(shape)}')
     if device < 0 or t.get_device() != device:
         raise ValueError(f'{name}: on {t.device}, expected a tensor on ' + (f'GPU {device}' if device >= 0 else 'a GPU'))
     raise ValueError(f'{name}: strides {t.stride()} of shape {tuple(t.shape)} are not supported')
 
 
-def _fits(have, want) -> bool:
-    return len(have) == len(want) and all(w is None or w == n for w, n in zip(want, have))
+def _pair(name: str, t: torch.Tensor):
+    """The shape of a tensor that has to have two dimensions."""
+    if t.dim() != 2:
+        raise ValueError(f'{name}: shape {tuple(t.shape)}, expected two dimensions')
+    return t.shape
 
 
 def _ws_arg(ws: Optional[torch.Tensor], device: int):
@@ -317,7 +320,7 @@ def _batch_args(pool, page_table, row0, seq_len):
     B = seq_len.numel()
     _arg('seq_len', seq_len, _I32, (B,), dev)
     _arg('row0', row0, _I32, (B + 1,), dev)
-    _arg('page_table', page_table, _I32, (B, page_table.shape[-1]), dev)
+    _arg('page_table', page_table, _I32, (B, _pair('page_table', page_table)[1]), dev)
     return dev, B
 
 
@@ -326,10 +329,11 @@ def ech_paged_append(pool, page_table, page_size: int, row0, seq_len, rows, stat
     row] (any type, the type of `rows`), page_table [B, pages] i32, row0 [B+1]
     i32, seq_len [B] i32 (with the new rows), status [1] i32 or None."""
     dev, B = _batch_args(pool, page_table, row0, seq_len)
-    _arg('pool', pool, (pool.dtype,), (None, None), dev)
-    n_slots, width = pool.shape
+    n_slots, width = have = _pair('pool', pool)
+    dtype = (pool.dtype,)
+    _arg('pool', pool, dtype, have, dev)
     T, es = rows.shape[0], pool.element_size()
-    _arg('rows', rows, (pool.dtype,), (T, width), dev, rows=True)
+    _arg('rows', rows, dtype, (T, width), dev, rows=True)
     if status is not None:
         _arg('status', status, _I32, (1,), dev)
     _call('ech_paged_append', dev, stream, pool.data_ptr(), n_slots, width * es, page_size, page_table.data_ptr(),
@@ -376,8 +380,8 @@ def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, ma
     T, H = q.shape[0], q.shape[1] if q.dim() == 3 else -1
     _arg('q', q, _BITS16, (T, H, 576), dev, rows=True)
     _arg('lse', lse, _F32, (T, H), dev)
-    _arg('acc_out', acc_out, _F32, (B, None), dev)
-    ld = acc_out.shape[1]
+    ld = _pair('acc_out', acc_out)[1]
+    _arg('acc_out', acc_out, _F32, (B, ld), dev)
     if acc_in is not None:
         _arg('acc_in', acc_in, _F32, (B, ld), dev)
     wp, wb = _ws_arg(ws, dev)
@@ -399,19 +403,19 @@ def ech_paged_evict(acc, seq_len, max_len: int, keep: int, n_sink: int, n_recent
     (src_table itself: compacted in place)."""
     dev, B = acc.get_device(), seq_len.numel()
     _arg('seq_len', seq_len, _I32, (B,), dev)
-    _arg('acc', acc, _F32, (B, None), dev)
+    ld = _pair('acc', acc)[1]
+    _arg('acc', acc, _F32, (B, ld), dev)
     _arg('kept', kept, _I32, (B, keep), dev)
     _arg('len_out', len_out, _I32, (B,), dev)
-    ld = acc.shape[1]
     if acc_out is not None:
         _arg('acc_out', acc_out, _F32, (B, ld), dev)
     n_slots = row_bytes = pt_ld = 0
     if pool is not None:
-        _arg('pool', pool, (pool.dtype,), (None, None), dev)
+        _arg('pool', pool, (pool.dtype,), _pair('pool', pool), dev)
         if src_table is None or dst_table is None:
             raise ValueError('src_table and dst_table are needed to move the rows of a pool')
-        _arg('src_table', src_table, _I32, (B, None), dev)
-        pt_ld = src_table.shape[1]
+        pt_ld = _pair('src_table', src_table)[1]
+        _arg('src_table', src_table, _I32, (B, pt_ld), dev)
         _arg('dst_table', dst_table, _I32, (B, pt_ld), dev)
         n_slots, row_bytes = pool.shape[0], pool.shape[1] * pool.element_size()
     wp, wb = _ws_arg(ws, dev)
