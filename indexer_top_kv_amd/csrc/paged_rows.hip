@@ -8,7 +8,11 @@
 
 namespace {
 
-// grid (ceil(T / 4)), 256 threads: one wave per row.
+// grid (ceil(T / 4)), 256 threads: one wave per row, which finds its sequence by
+// counting the row ends at or before it, 64 sequences a round. Bound by the
+// rows' bytes, or with few rows by the two dependent reads (offsets, page) and
+// the launch: 16384 rows of 1152 bytes 5.8 us (6.5 TB/s of reads and writes, a
+// part of them from cache), 64 rows 3.1 us.
 __global__ void __launch_bounds__(256)
     paged_append_kernel(uint4* __restrict__ pool, int row16, Pages pg, const int32_t* __restrict__ row0,
                         const int32_t* __restrict__ seq_len, int B, int T, const uint4* __restrict__ rows,
@@ -44,6 +48,21 @@ __global__ void __launch_bounds__(256)
 // so ranks come from ballots.
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 2048;
+// A bin's count in LDS is kept four times over, lane l adding to the l % 4-th:
+// equal keys (zeros, above all) go to one bin, one after the other. 16384 equal
+// weights 24 us, with one count 54 us; spread ones 17 us either way.
+constexpr int kCopies = 4;
+__device__ __forceinline__ void clear_bins(int* hist) {
+#pragma unroll
+  for (int z = 0; z < kBins * kCopies / kThreads; ++z) hist[z * kThreads + threadIdx.x] = 0;
+}
+__device__ __forceinline__ void add_to_bin(int* hist, uint32_t bin) {
+  atomicAdd(&hist[bin * kCopies + (threadIdx.x & (kCopies - 1))], 1);
+}
+__device__ __forceinline__ int bin_count(const int* hist, int bin) {
+  const int4 v = *reinterpret_cast<const int4*>(hist + bin * kCopies);
+  return (v.x + v.y) + (v.z + v.w);
+}
 
 // Order of a weight: larger first; NaN above everything, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float x) { return x != x ? 0xffffffffu : ech::ord_key(x); }
@@ -131,12 +150,15 @@ __device__ __forceinline__ void write_kept(const float (&x)[KPT], const Row& r, 
 
 // Rows of at most KPT * 1024 tokens: one workgroup per sequence, its weights in
 // registers from the first read on, so acc_out may be acc and len_out seq_len.
-// 32 sequences of 8K-16K tokens (KPT 16) 12 us; the form for long rows 22 us.
+// Bound by the chain of its three digits (counting in LDS, a scan, a barrier
+// each). KPT 4 to 4096 tokens, 16 to 16384, the form below for longer rows:
+//   4096 tokens    1, 32, 256 sequences  KPT 4 7.6, 8.0, 8.6 us   KPT 16 13.2, 13.5, 14.3 us
+//   16384 tokens   1, 32, 256 sequences  KPT 16 16.7, 17.3, 20.2  long rows 24.2, 25.8, 44.1
 template <int KPT>
 __global__ void __launch_bounds__(kThreads)
     paged_evict_row_kernel(const float* acc, int64_t acc_ld, const int32_t* seq_len, int max_len, int keep, int n_sink,
                            int n_recent, int32_t* __restrict__ kept, float* acc_out, int32_t* len_out) {
-  __shared__ int hist[kBins];
+  __shared__ __align__(16) int hist[kBins * kCopies];
   __shared__ int scratch[kWaves], s_found[2];
   __shared__ int s_cnt[kWaves][2];
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -155,18 +177,17 @@ __global__ void __launch_bounds__(kThreads)
     uint32_t prefix = 0;
     for (int level = 0; level < 3; ++level) {
       const int shift = digit_shift(level), width = level == 2 ? 10 : 11;
-      hist[tid] = 0;
-      hist[tid + kThreads] = 0;
+      clear_bins(hist);
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < KPT; ++j) {
         const int t = token_of<KPT>(0, j);
         const uint32_t k = weight_key(x[j]);
         if (t >= r.lo && t < r.hi && (level == 0 || (k >> (shift + width)) == prefix))
-          atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
+          add_to_bin(hist, (k >> shift) & ((1u << width) - 1u));
       }
       __syncthreads();
-      find_digit(hist[kBins - 1 - 2 * tid], hist[kBins - 2 - 2 * tid], want, scratch, s_found);
+      find_digit(bin_count(hist, kBins - 1 - 2 * tid), bin_count(hist, kBins - 2 - 2 * tid), want, scratch, s_found);
       prefix = (prefix << width) | (uint32_t)s_found[0];
       want = s_found[1];
       __syncthreads();
@@ -187,7 +208,9 @@ __global__ void __launch_bounds__(kThreads)
 // Longer rows: blocks of 8192 tokens, a launch per digit and one that writes.
 // ws per sequence: what is found so far {digit 0, rest, digit 1, rest}, and per
 // block its counts above the digits found so far, then every block's histogram
-// of each level. Nothing needs to start at zero.
+// of each level. Nothing needs to start at zero. Bound by the launches: 131072
+// tokens 4.9 + 7.4 + 7.6 us for the digits and 11 us for the last digit, ranks
+// and writes, of which the weights' 512 KiB are a tenth of a microsecond.
 constexpr int kBlockKpt = 8, kBlock = kBlockKpt * kThreads;
 struct LongWs {
   int32_t* found;   // [B][4]
@@ -227,7 +250,7 @@ template <int LEVEL>
 __global__ void __launch_bounds__(kThreads)
     paged_evict_digit_kernel(const float* __restrict__ acc, int64_t acc_ld, const int32_t* __restrict__ seq_len,
                              int max_len, int keep, int n_sink, int n_recent, LongWs w) {
-  __shared__ int hist[kBins];
+  __shared__ __align__(16) int hist[kBins * kCopies];
   __shared__ int scratch[kWaves], s_found[2];
   const int b = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x, t0 = blk * kBlock;
   const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
@@ -240,8 +263,7 @@ __global__ void __launch_bounds__(kThreads)
     const int t = token_of<kBlockKpt>(t0, j);
     x[j] = t < r.n ? a[t] : 0.f;
   }
-  hist[tid] = 0;
-  hist[tid + kThreads] = 0;
+  clear_bins(hist);
   uint32_t prefix = 0;
   if (LEVEL > 0) {
     int want = r.want, before[2];
@@ -271,12 +293,12 @@ __global__ void __launch_bounds__(kThreads)
     const int t = token_of<kBlockKpt>(t0, j);
     const uint32_t k = weight_key(x[j]);
     if (t >= r.lo && t < r.hi && (LEVEL == 0 || (k >> ((shift + width) & 31)) == prefix))
-      atomicAdd(&hist[(k >> shift) & ((1u << width) - 1u)], 1);
+      add_to_bin(hist, (k >> shift) & ((1u << width) - 1u));
   }
   __syncthreads();
   int32_t* h = hist_of(w, LEVEL, b, blk);
-  h[tid] = hist[tid];
-  h[tid + kThreads] = hist[tid + kThreads];
+  h[tid] = bin_count(hist, tid);
+  h[tid + kThreads] = bin_count(hist, tid + kThreads);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -349,7 +371,9 @@ __global__ void __launch_bounds__(256)
 
 // Rows of kept tokens to the pages of another table. grid (ceil(keep / 64),
 // B), 256 threads: 64 rows' slots, then their 16-byte pieces, kMovePieces of a
-// thread's loads under way at a time. ROW16: pieces per row (0: row16).
+// thread's loads under way at a time. ROW16: pieces per row (0: row16). Bound
+// by the rows read and written: 32 x 8192 rows of 1152 bytes 107-123 us, 4.9 to
+// 5.6 TB/s (with row16 in place of the constant 7 us more).
 constexpr int kMoveRows = 64, kMovePieces = 6;
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 template <int ROW16>
@@ -387,27 +411,53 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The same within one table. A kept token's place is never behind it, so
-// ascending rounds are safe as long as a round's rows are read before any is
-// written: one workgroup carries a 64-byte column of every row, alone, 256
-// rows a round. grid (ceil(row16 / 4), B), 1024 threads.
-__global__ void __launch_bounds__(1024)
-    paged_move_within_kernel(uint4* __restrict__ pool, int row16, Pages pg, const int32_t* __restrict__ kept, int keep) {
-  const int b = blockIdx.y, c = blockIdx.x * 4 + (threadIdx.x & 3);
+// The same within one table. A kept token's place is never behind it, so a
+// batch of rows may be written once all of it is read; the rows that later
+// batches read lie behind every place of this one. One workgroup carries a
+// 128-byte column of its sequence's rows, kWithin rows a thread under way at a
+// time (their entries, then the rows, without a branch between), and all columns
+// of a sequence run on one XCD: lines that its columns share, and writes to
+// them, meet in one cache. 32 x 8192 rows of 1152 bytes 143 us, bound by the
+// rows (to other pages 128 us); one sequence of 8192 rows 38 us, bound by the
+// waits of its batches. (64-byte columns spread over the XCDs, a row a thread
+// and batch: 198 and 40 us; 512 threads 144 and 44 us.)
+constexpr int kWithin = 4, kWithinThreads = 1024, kWithinCol = 8;   // pieces a thread and batch; threads; pieces a column
+__global__ void __launch_bounds__(kWithinThreads)
+    paged_move_within_kernel(u32x4_t* __restrict__ pool, int row16, Pages pg, const int32_t* __restrict__ kept, int keep,
+                             int most, int B) {
+  const int cols = (row16 + kWithinCol - 1) / kWithinCol, i = blockIdx.x >> 3, b = i / cols * 8 + (blockIdx.x & 7);
+  const int c = i % cols * kWithinCol + (int)threadIdx.x % kWithinCol;
+  if (b >= B) return;
   const int32_t* row = pg.table + (int64_t)b * pg.ld;
-  for (int j0 = 0; j0 < keep; j0 += 256) {
-    const int j = j0 + (threadIdx.x >> 2);
-    const int t = j < keep ? kept[(int64_t)b * keep + j] : -1;
-    int s = -1, d = -1;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (t > j && c < row16) {
-      s = slot_of(pg, row, t);
-      d = slot_of(pg, row, j);
-      if (s >= 0 && d >= 0) v = pool[(int64_t)s * row16 + c];
+  const int32_t* kb = kept + (int64_t)b * keep;
+  const int last = (int)min(pg.ld - 1, (int64_t)INT32_MAX);
+  constexpr int kRound = kWithinThreads / kWithinCol;
+  for (int j0 = 0; j0 < most; j0 += kRound * kWithin) {   // most = min(keep, max_len) places can be taken
+    u32x4_t v[kWithin];
+    int t[kWithin], ps[kWithin], pd[kWithin], to[kWithin];
+#pragma unroll
+    for (int u = 0; u < kWithin; ++u) t[u] = kb[min(j0 + u * kRound + (int)threadIdx.x / kWithinCol, keep - 1)];
+#pragma unroll
+    for (int u = 0; u < kWithin; ++u) {
+      const int j = j0 + u * kRound + (int)threadIdx.x / kWithinCol;
+      ps[u] = row[min((int)page_index(pg, max(t[u], 0)), last)];
+      pd[u] = row[min((int)page_index(pg, j), last)];
     }
+#pragma unroll
+    for (int u = 0; u < kWithin; ++u) {
+      const int j = j0 + u * kRound + (int)threadIdx.x / kWithinCol, tt = max(t[u], 0);
+      const int is = (int)page_index(pg, tt), id = (int)page_index(pg, j);
+      const int s = is <= last ? slot_in(pg, ps[u], tt - is * pg.size) : -1;
+      const int d = id <= last ? slot_in(pg, pd[u], j - id * pg.size) : -1;
+      const bool moves = j < keep && t[u] > j && c < row16 && s >= 0;
+      to[u] = moves ? d : -1;
+      v[u] = pool[(int64_t)(moves ? s : 0) * row16 + (moves ? c : 0)];   // what does not move reads the pool's first piece
+    }
+    __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0)
     __syncthreads();
-    if (s >= 0 && d >= 0) pool[(int64_t)d * row16 + c] = v;
-    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kWithin; ++u)
+      if (to[u] >= 0) pool[(int64_t)to[u] * row16 + c] = v[u];
   }
 }
 
@@ -524,8 +574,8 @@ extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* 
   const dim3 mgrid((std::min(keep, max_len) + kMoveRows - 1) / kMoveRows, B);
   if (mgrid.x == 0) return ECH_OK;
   if (src_table == dst_table)
-    hipLaunchKernelGGL(paged_move_within_kernel, dim3((row16 + 3) / 4, B), dim3(1024), 0, s, static_cast<uint4*>(pool),
-                       row16, a, kept, keep);
+    hipLaunchKernelGGL(paged_move_within_kernel, dim3((row16 + kWithinCol - 1) / kWithinCol * ((B + 7) / 8 * 8)),
+                       dim3(kWithinThreads), 0, s, static_cast<u32x4_t*>(pool), row16, a, kept, keep, std::min(keep, max_len), B);
   else if (row16 == kPagedChunks)
     hipLaunchKernelGGL(paged_move_kernel<kPagedChunks>, mgrid, dim3(256), 0, s, static_cast<u32x4_t*>(pool), row16, a, d, kept,
                        keep);

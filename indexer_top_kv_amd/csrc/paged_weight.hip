@@ -10,10 +10,15 @@
 // step. No other lane or workgroup adds to a token out of order: the same call
 // gives the same bits.
 //  - Sequences of at most 128 queries (decoding): the queries stay in registers
-//    and the rows stream past them; bound by the rows' bytes.
-//  - More queries (chunks): 256 tokens' rows stay in registers (64 a wave, 288
-//    registers) and the queries stream past, 16 KiB of products per LDS
-//    kilobyte; bound by the matrix cores.
+//    and the rows stream past them; bound by the rows' bytes: 32 tokens of 128
+//    heads over 8K to 16K tokens 104-109 us, 4.2 TB/s (the other form 164 us;
+//    a whole sequence per workgroup 962 us).
+//  - More queries (chunks), which this form would have to pass the rows by more
+//    than once: 256 tokens' rows stay in registers (64 a wave, 288 registers)
+//    and the queries stream past; bound by the matrix cores: 4 chunks of 64 rows
+//    at 64 heads over 10K tokens 211-216 us, 890 TF/s (a step's products are
+//    2304 of its ~4000 cycles: the weights' exponentials and LDS reads take
+//    issue slots between them; a workgroup starts in 24K cycles, its rows' load).
 #include <algorithm>
 
 #include "common.hpp"
@@ -455,7 +460,8 @@ bool shape_ok(int B, int T, int H, int max_rows, int max_len) {
 bool few(int T, int H, int max_rows) { return (int64_t)std::min(max_rows, T) * H <= kMS; }
 
 // Parts of the queries: as many as fill the CUs evenly with the batch's token
-// tiles (a part is at least 16 steps, which its rows' loads are worth).
+// tiles (a part is at least 16 steps, which its rows' loads are worth). 4 x 40
+// token tiles of 128 steps: 3 parts (chosen) 216 us, 4 230 us, 5 249 us, 6 223 us.
 int parts_of(int B, int T, int H, int max_rows, int max_len) {
   if (few(T, H, max_rows)) return 1;
   const int64_t wgs = (int64_t)B * ((max_len + kTokWg - 1) / kTokWg);
