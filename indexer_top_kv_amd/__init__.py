@@ -294,6 +294,12 @@ def _pair(name: str, t: torch.Tensor):
     return t.shape
 
 
+def _steps(q: torch.Tensor, T: int, H: int):
+    """Values from row to row and from head to head; 0 along a dimension of one,
+    whose stride says nothing."""
+    return q.stride(0) if T > 1 else 0, q.stride(1) if H > 1 else 0
+
+
 def _ws_arg(ws: Optional[torch.Tensor], device: int):
     """(pointer, bytes) of a workspace, or (None, 0) without one."""
     if ws is None:
@@ -360,7 +366,7 @@ def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows:
     if lse is not None:
         _arg('lse', lse, _F32, (T, H), dev)
     wp, wb = _ws_arg(ws, dev)
-    _call('ech_paged_attn', dev, stream, q.data_ptr(), q.stride(0), q.stride(1), pool.data_ptr(), pool.shape[0],
+    _call('ech_paged_attn', dev, stream, q.data_ptr(), *_steps(q, T, H), pool.data_ptr(), pool.shape[0],
           page_size, page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, T, H, max_rows,
           max_len, window, n_sink, sm_scale, out.data_ptr(), _ptr(lse), wp, wb)
 
@@ -385,7 +391,7 @@ def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, ma
     if acc_in is not None:
         _arg('acc_in', acc_in, _F32, (B, ld), dev)
     wp, wb = _ws_arg(ws, dev)
-    _call('ech_paged_weight', dev, stream, q.data_ptr(), q.stride(0), q.stride(1), lse.data_ptr(), pool.data_ptr(),
+    _call('ech_paged_weight', dev, stream, q.data_ptr(), *_steps(q, T, H), lse.data_ptr(), pool.data_ptr(),
           pool.shape[0], page_size, page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B,
           T, H, max_rows, max_len, window, n_sink, sm_scale, _ptr(acc_in), acc_out.data_ptr(), ld, decay, wp, wb)
 

@@ -235,3 +235,32 @@ def test_evict_at_the_forms_ends_with_room_to_spare(L):
         lens = np.array(lens, np.int32)
         check_evict(run_evict(acc, lens, keep, 0, 0), acc, lens, keep, 0, 0)
         check_evict(run_evict(acc, lens, keep, 0, 0, in_place=True), acc, lens, keep, 0, 0)
+
+
+@pytest.mark.parametrize('T,H', [(1, 16), (1, 1), (7, 1)])
+def test_strides_of_single_rows_and_heads_do_not_matter(T, H):
+    """A dimension of one has no stride worth checking: a row or a head cut
+    from a tensor whose rows or heads are oddly spaced."""
+    need_gpu()
+    c = Case([T], [300], H, 16, seed=T + H)
+    want = c.attn()
+    if T == 1:
+        q = torch.as_strided(dev(c.q).view(torch.bfloat16), (1, H, 576), (1, 576, 1))
+    else:
+        q = torch.as_strided(dev(c.q).view(torch.bfloat16), (T, 1, 576), (576, 3, 1))
+    got = c.attn(q=q)
+    np.testing.assert_array_equal(got[0], want[0])
+    acc = np.zeros((1, c.max_len), np.float32)
+    np.testing.assert_array_equal(c.weight(want[1], acc, 1.0, q=q), c.weight(want[1], acc, 1.0))
+
+
+@pytest.mark.parametrize('rows,ctx,H', [([1], [900], 16), ([1, 40], [10, 400], 64), ([300], [0], 128)])
+def test_attention_without_lse(rows, ctx, H):
+    need_gpu()
+    c = Case(rows, ctx, H, 16, seed=H)
+    want, _ = c.attn()
+    out = torch.full((c.T, H, 512), 7.0, dtype=torch.bfloat16, device='cuda')
+    ech.ech_paged_attn(dev(c.q), dev(c.pool), dev(c.table), 16, dev(c.row0), dev(c.seq_len), c.max_rows, c.max_len,
+                       SCALE, out, ws=c.ws(ech.ech_paged_attn_ws_bytes, c.B, c.T, H, c.max_rows, c.max_len))
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(out.float().cpu().numpy(), want)
