@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(64 * NH * TL, 1)
         const int sl = slots[si][t];
         const uint4* src = cache + (size_t)max(sl, 0) * kChunks + c;
         const uint32_t lds = lds0 + static_cast<uint32_t>(ins * 1024);
-        asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(src) : "memory", "m0");
+        // a wait state between M0's write and the load that uses it: the hardware does not wait by itself
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(src) : "memory", "m0");
       }
     }
   };
