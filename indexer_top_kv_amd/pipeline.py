@@ -669,9 +669,10 @@ class PagedLayer:
     first n_sink, the last n_recent, and the heaviest between.
 
     The host knows every length (an eviction leaves budget tokens), so nothing
-    waits for the device. place(counts) does the host's part, launch(q, rows)
-    the step's kernels, trim() the eviction; a launch of the same T may be
-    captured and replayed, the tables and lengths being read in place. The
+    waits for the device. place(counts) does the host's part (its copies are on
+    the current stream, before the kernels of launch), launch(q, rows) the
+    step's kernels, trim() the eviction; a launch of the same T may be captured
+    and replayed, the tables and lengths being read in place. The
     buffers a step returns are the layer's: the next step of the same T
     writes them again. Steps of one layer must be ordered."""
 
@@ -758,9 +759,10 @@ class PagedLayer:
 
     def step(self, q: torch.Tensor, rows: torch.Tensor, counts):
         """place, launch and trim on the current stream; returns (out, lse)."""
-        T = self.place(counts)
+        T = int(np.sum(counts))
         if q.shape[0] != T or rows.shape[0] != T:
             raise ValueError(f'counts name {T} rows, q has {q.shape[0]} and rows {rows.shape[0]}')
+        self.place(counts)
         got = self.launch(q, rows)
         self.trim()
         return got

@@ -149,6 +149,9 @@ def test_release_and_refusals():
     assert np.array_equal(layer.pages.table, before) and layer.lens.tolist() == [50, 0]
     with pytest.raises(ValueError):
         layer.step(*z(3), [2, 2])
+    assert layer.lens.tolist() == [50, 0]       # nothing was placed
+    layer.step(*z(0), [0, 0])                   # a step without rows changes nothing but the decay
+    assert layer.lens.tolist() == [50, 0]
     layer.release(0)
     assert layer.lens[0] == 0
     layer.step(*z(64), [0, 64])
