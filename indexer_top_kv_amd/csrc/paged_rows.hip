@@ -50,7 +50,7 @@ constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = 2048;
 // A bin's count in LDS is kept four times over, lane l adding to the l % 4-th:
 // equal keys (zeros, above all) go to one bin, one after the other. 16384 equal
-// weights 24 us, with one count 54 us; spread ones 17 us either way.
+// weights 20 us, with one count 50 us; spread ones 12 us either way.
 constexpr int kCopies = 4;
 __device__ __forceinline__ void clear_bins(int* hist) {
 #pragma unroll
@@ -70,21 +70,34 @@ __device__ __forceinline__ uint32_t weight_key(float x) { return x != x ? 0xffff
 __device__ __forceinline__ int digit_shift(int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; }
 
 struct Row {
-  int n, lo, hi, want;   // tokens; those between are [lo, hi); how many of them stay (0 also where all stay)
-  bool cut;              // n > keep
-};
+  int n, lo, hi, want;   // tokens; those between the protected ones are [lo, hi); how many of them stay
+};                       // (none are between where n <= keep)
 __device__ __forceinline__ Row row_of(const int32_t* seq_len, int b, int max_len, int keep, int n_sink, int n_recent) {
   const int n = min(max(seq_len[b], 0), max_len);
   const bool cut = n > keep;
-  return Row{n, cut ? n_sink : 0, cut ? n - n_recent : 0, cut ? keep - n_sink - n_recent : 0, cut};
+  return Row{n, cut ? n_sink : 0, cut ? n - n_recent : 0, cut ? keep - n_sink - n_recent : 0};
+}
+
+// The sum of one value per wave (the same in all of its lanes), and what the
+// waves before this one hold of it. scratch: kWaves; a barrier has to stand
+// between two uses. Call from all threads.
+__device__ __forceinline__ int waves_sum(int x, int* scratch, int* before) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+  if (lane == 0) scratch[wave] = x;
+  __syncthreads();
+  const int w = lane < kWaves ? scratch[lane] : 0, incl = lanes_scan(w);
+  *before = __builtin_amdgcn_readlane(incl, wave) - x;
+  return last_lane(incl);
 }
 
 // The digit d of descending bins that holds the want-th entry, and how many of
 // that bin are wanted. Thread t brings the counts of bins 2047 - 2t and 2046 -
 // 2t; out[0] = d, out[1] = rest. Call from all threads.
 __device__ __forceinline__ void find_digit(int c0, int c1, int want, int* scratch, int* out) {
-  int tot;
-  const int before = ech::block_excl_scan<kThreads>(c0 + c1, scratch, &tot);
+  const int incl = lanes_scan(c0 + c1);
+  int waves;
+  (void)waves_sum(last_lane(incl), scratch, &waves);
+  const int before = waves + incl - (c0 + c1);
   const int d0 = kBins - 1 - 2 * (int)threadIdx.x;
   if (before < want && want <= before + c0) {
     out[0] = d0;
@@ -96,80 +109,139 @@ __device__ __forceinline__ void find_digit(int c0, int c1, int want, int* scratc
   __syncthreads();
 }
 
-// This thread's tokens of a block of KPT * 1024 starting at t0: wave w owns
-// KPT * 64 consecutive ones, register j 64 of them.
+// A block of KPT * 1024 tokens from t0: wave w owns KPT * 64 consecutive ones,
+// register j 64 of them from this token on.
 template <int KPT>
-__device__ __forceinline__ int token_of(int t0, int j) {
-  return t0 + (int)(threadIdx.x >> 6) * (KPT * 64) + j * 64 + (int)(threadIdx.x & 63);
+__device__ __forceinline__ int base_of(int t0, int j) {
+  return t0 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * (KPT * 64) + j * 64;
+}
+// This thread's weights of a block (up to max_len, before the length is known),
+// and their keys: 0, which no weight has, for a token that is protected or does
+// not exist.
+template <int KPT>
+__device__ __forceinline__ void load_weights(const float* a, int t0, int max_len, float (&x)[KPT]) {
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t = base_of<KPT>(t0, j) + (int)(threadIdx.x & 63);
+    x[j] = t < max_len ? a[t] : 0.f;
+  }
+}
+template <int KPT>
+__device__ __forceinline__ void keys_of(const float (&x)[KPT], int t0, const Row& r, uint32_t (&k)[KPT]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int t = base_of<KPT>(t0, j) + lane;
+    k[j] = (uint32_t)(t - r.lo) < (uint32_t)(r.hi - r.lo) ? weight_key(x[j]) : 0u;
+  }
 }
 
-// Ranks and writes of one block: its tokens above thr, its protected ones, and
-// its equals of thr while `ties` (less those before the block, ties0) last go
-// to places at0, at0 + 1, ... in token order.
+// Counts digit `(k >> shift) mod 2^width` of the block's keys whose higher
+// digits are `prefix` (first: of all).
 template <int KPT>
-__device__ __forceinline__ void write_kept(const float (&x)[KPT], const Row& r, int t0, uint32_t thr, int ties, int ties0,
-                                           int at0, int keep, int32_t* kb, float* ao, int (*s_cnt)[2]) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+__device__ __forceinline__ void count_digits(const uint32_t (&k)[KPT], bool first, uint32_t prefix, int shift, int width,
+                                             int* hist) {
+  const uint32_t mask = (1u << width) - 1u;
+  if (first) {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j)
+      if (k[j] != 0) add_to_bin(hist, k[j] >> shift);
+  } else {
+#pragma unroll
+    for (int j = 0; j < KPT; ++j)
+      if (k[j] >> (shift + width) == prefix) add_to_bin(hist, (k[j] >> shift) & mask);
+  }
+}
+
+__device__ __forceinline__ int set_rank(uint64_t set) {   // of this lane: members in lower lanes
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(set >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)set, 0));
+}
+
+// The places of one block's kept tokens, put(place, token, weight) each: the
+// protected ones' are known; those with keys above thr, and the equals of thr
+// while `ties` (less those before the block, ties0) last, go to places at0, at0
+// + 1, ... in token order. A workgroup's 16 waves share one CU's issue and its
+// instruction cache, and this code runs once: it is kept short (with a branch
+// per case 10K cycles at KPT 16).
+template <int KPT, class Put>
+__device__ __forceinline__ void place_kept(const float* a, const float (&x)[KPT], uint32_t (&k)[KPT], const Row& r,
+                                           int t0, uint32_t thr, int ties, int ties0, int at0, int nk, int (*s_cnt)[2],
+                                           Put put) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
   int gt = 0, eq = 0;
 #pragma unroll
   for (int j = 0; j < KPT; ++j) {
-    const int t = token_of<KPT>(t0, j);
-    const bool mid = r.cut && t >= r.lo && t < r.hi;
-    const uint32_t k = weight_key(x[j]);
-    gt += (int)__popcll(__ballot(t < r.n && (!mid || k > thr)));
-    eq += (int)__popcll(__ballot(t < r.n && mid && k == thr));
+    gt += (int)__popcll(__ballot(k[j] > thr));
+    eq += (int)__popcll(__ballot(k[j] == thr));
   }
   if (lane == 0) {
     s_cnt[wave][0] = gt;
     s_cnt[wave][1] = eq;
   }
   __syncthreads();
-  int at = at0, seen = ties0;
-  for (int w = 0; w < wave; ++w) {
-    at += s_cnt[w][0] + min(max(ties - seen, 0), s_cnt[w][1]);
-    seen += s_cnt[w][1];
-  }
+  // the waves before this one, a wave per lane; of equals the first ties - ties0 stay
+  const int2 c = lane < wave ? *reinterpret_cast<const int2*>(s_cnt[lane]) : make_int2(0, 0);
+  const int gt0 = last_lane(lanes_scan(c.x)), eq0 = last_lane(lanes_scan(c.y));
+  int at = at0 + gt0 + min(max(ties - ties0, 0), eq0), left = ties - ties0 - eq0;
 #pragma unroll
   for (int j = 0; j < KPT; ++j) {
-    const int t = token_of<KPT>(t0, j);
-    const bool mid = r.cut && t >= r.lo && t < r.hi;
-    const uint32_t k = weight_key(x[j]);
-    const bool tie = t < r.n && mid && k == thr;
-    const unsigned long long below = (1ull << lane) - 1ull, tm = __ballot(tie);
-    const bool take = (t < r.n && (!mid || k > thr)) || (tie && seen + (int)__popcll(tm & below) < ties);
-    const unsigned long long m = __ballot(take);
-    const int place = at + (int)__popcll(m & below);
-    if (take && place < keep) {
-      kb[place] = t;
-      if (ao) ao[place] = x[j];
+    asm volatile("" : "+v"(k[j]));   // compared again: the sets, held, would not fit the scalar registers
+    const uint64_t tie = __ballot(k[j] == thr), set = __ballot(k[j] > thr) | (tie & __ballot(set_rank(tie) < left));
+    const int place = at + set_rank(set);
+    if (__builtin_amdgcn_inverse_ballot_w64(set)) put(place, base_of<KPT>(t0, j) + lane, x[j]);
+    at += (int)__popcll(set);
+    left -= (int)__popcll(tie);
+  }
+  auto fixed = [&](int from, int to) {
+    for (int t = from + (int)threadIdx.x; t < to; t += kThreads) put(t < r.lo ? t : t - r.n + nk, t, a[t]);
+  };
+  const int end = t0 + KPT * kThreads;
+  fixed(t0, min(r.lo, end));
+  fixed(max(r.hi, t0), min(r.n, end));
+}
+
+// Values from LDS to memory, 16 bytes a thread: src[0 .. n), then `rest` up to
+// `all`. src stands as far past a 16-byte boundary as dst: at lead_of(dst).
+__device__ __forceinline__ int lead_of(const void* dst) { return (int)((reinterpret_cast<uintptr_t>(dst) >> 2) & 3); }
+template <class V>
+__device__ __forceinline__ void copy_out(V* dst, const V* src, int n, V rest, int all) {
+  typedef V vec_t __attribute__((ext_vector_type(4)));
+  const int lead = lead_of(dst);
+  for (int i = 4 * (int)threadIdx.x - lead; i < all; i += 4 * kThreads) {
+    if (i >= 0 && i + 4 <= n) {
+      *reinterpret_cast<vec_t*>(dst + i) = *reinterpret_cast<const vec_t*>(src + i);
+    } else if (i >= n && i + 4 <= all) {
+      *reinterpret_cast<vec_t*>(dst + i) = vec_t{rest, rest, rest, rest};
+    } else {
+      for (int e = max(i, 0); e < min(i + 4, all); ++e) dst[e] = e < n ? src[e] : rest;
     }
-    at += (int)__popcll(m);
-    seen += (int)__popcll(tm);
   }
 }
 
 // Rows of at most KPT * 1024 tokens: one workgroup per sequence, its weights in
 // registers from the first read on, so acc_out may be acc and len_out seq_len.
-// Bound by the chain of its three digits (counting in LDS, a scan, a barrier
-// each). KPT 4 to 4096 tokens, 16 to 16384, the form below for longer rows:
-//   4096 tokens    1, 32, 256 sequences  KPT 4 7.6, 8.0, 8.6 us   KPT 16 13.2, 13.5, 14.3 us
-//   16384 tokens   1, 32, 256 sequences  KPT 16 16.7, 17.3, 20.2  long rows 24.2, 25.8, 44.1
+// Bound by one CU's issue: of 27K cycles at KPT 16 the weights take 4.7K to
+// arrive, each of the three digits 1.4K to 3.5K to count and 1.3K to find, the
+// places 6.8K, the writes 2.2K. KPT 4 to 4096 tokens, 16 to 16384, the form
+// below for longer rows; 1, 32 and 256 sequences:
+//   4096 tokens    KPT 4  6.7, 6.6, 7.2 us      KPT 16     9.3, 9.7, 10.5 us
+//   16384 tokens   KPT 16 12.1, 12.7, 16.0 us   long rows  20.8, 22.4, 35.4 us
 template <int KPT>
 __global__ void __launch_bounds__(kThreads)
     paged_evict_row_kernel(const float* acc, int64_t acc_ld, const int32_t* seq_len, int max_len, int keep, int n_sink,
                            int n_recent, int32_t* __restrict__ kept, float* acc_out, int32_t* len_out) {
-  __shared__ __align__(16) int hist[kBins * kCopies];
+  constexpr int kStage = KPT * kThreads + 4, kHist = kBins * kCopies;
+  __shared__ __align__(16) int mem[2 * kStage > kHist ? 2 * kStage : kHist];   // the counts, then what is kept
   __shared__ int scratch[kWaves], s_found[2];
-  __shared__ int s_cnt[kWaves][2];
+  __shared__ __align__(8) int s_cnt[kWaves][2];
+  int* const hist = mem;
   const int b = blockIdx.x, tid = threadIdx.x;
-  const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
   const float* a = acc + (int64_t)b * acc_ld;
   float x[KPT];
-#pragma unroll
-  for (int j = 0; j < KPT; ++j) {
-    const int t = token_of<KPT>(0, j);
-    x[j] = t < r.n ? a[t] : 0.f;
-  }
+  uint32_t k[KPT];
+  load_weights<KPT>(a, 0, max_len, x);
+  const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
+  keys_of<KPT>(x, 0, r, k);
   uint32_t thr = 0xffffffffu;
   int ties = 0;
   if (r.want > 0) {
@@ -179,13 +251,7 @@ __global__ void __launch_bounds__(kThreads)
       const int shift = digit_shift(level), width = level == 2 ? 10 : 11;
       clear_bins(hist);
       __syncthreads();
-#pragma unroll
-      for (int j = 0; j < KPT; ++j) {
-        const int t = token_of<KPT>(0, j);
-        const uint32_t k = weight_key(x[j]);
-        if (t >= r.lo && t < r.hi && (level == 0 || (k >> (shift + width)) == prefix))
-          add_to_bin(hist, (k >> shift) & ((1u << width) - 1u));
-      }
+      count_digits<KPT>(k, level == 0, prefix, shift, width, hist);
       __syncthreads();
       find_digit(bin_count(hist, kBins - 1 - 2 * tid), bin_count(hist, kBins - 2 - 2 * tid), want, scratch, s_found);
       prefix = (prefix << width) | (uint32_t)s_found[0];
@@ -198,10 +264,15 @@ __global__ void __launch_bounds__(kThreads)
   const int nk = min(r.n, keep);
   int32_t* kb = kept + (int64_t)b * keep;
   float* ao = acc_out ? acc_out + (int64_t)b * acc_ld : nullptr;
-  write_kept<KPT>(x, r, 0, thr, ties, 0, 0, keep, kb, ao, s_cnt);
-  for (int j = nk + tid; j < keep; j += kThreads) kb[j] = -1;
-  if (ao)
-    for (int j = nk + tid; j < max_len; j += kThreads) ao[j] = 0.f;
+  int* const s_kept = mem + lead_of(kb);
+  float* const s_out = reinterpret_cast<float*>(mem + kStage) + lead_of(ao);
+  place_kept<KPT>(a, x, k, r, 0, thr, ties, 0, r.lo, nk, s_cnt, [&](int place, int t, float v) {
+    s_kept[place] = t;
+    s_out[place] = v;
+  });
+  __syncthreads();
+  copy_out(kb, s_kept, nk, -1, keep);
+  if (ao) copy_out(ao, s_out, nk, 0.f, max_len);
   if (tid == 0) len_out[b] = nk;
 }
 
@@ -209,7 +280,7 @@ __global__ void __launch_bounds__(kThreads)
 // ws per sequence: what is found so far {digit 0, rest, digit 1, rest}, and per
 // block its counts above the digits found so far, then every block's histogram
 // of each level. Nothing needs to start at zero. Bound by the launches: 131072
-// tokens 4.9 + 7.4 + 7.6 us for the digits and 11 us for the last digit, ranks
+// tokens 4.4 + 5.9 + 5.8 us for the digits and 8.2 us for the last digit, ranks
 // and writes, of which the weights' 512 KiB are a tenth of a microsecond.
 constexpr int kBlockKpt = 8, kBlock = kBlockKpt * kThreads;
 struct LongWs {
@@ -258,11 +329,9 @@ __global__ void __launch_bounds__(kThreads)
   const int n_blk = (r.n + kBlock - 1) / kBlock;
   const float* a = acc + (int64_t)b * acc_ld;
   float x[kBlockKpt];
-#pragma unroll
-  for (int j = 0; j < kBlockKpt; ++j) {
-    const int t = token_of<kBlockKpt>(t0, j);
-    x[j] = t < r.n ? a[t] : 0.f;
-  }
+  uint32_t k[kBlockKpt];
+  load_weights<kBlockKpt>(a, t0, max_len, x);
+  keys_of<kBlockKpt>(x, t0, r, k);
   clear_bins(hist);
   uint32_t prefix = 0;
   if (LEVEL > 0) {
@@ -278,23 +347,18 @@ __global__ void __launch_bounds__(kThreads)
     constexpr int up = LEVEL == 1 ? 21 : 10;
 #pragma unroll
     for (int j = 0; j < kBlockKpt; ++j) {
-      const int t = token_of<kBlockKpt>(t0, j);
-      const uint32_t k = weight_key(x[j]) >> up;
-      above += t >= r.lo && t < r.hi && (LEVEL == 1 || (k >> 11) == prefix) && (k & (kBins - 1)) > (uint32_t)s_found[0];
+      const uint32_t d = k[j] >> up;
+      const bool in = (LEVEL == 1 || (d >> 11) == prefix) && (d & (kBins - 1)) > (uint32_t)s_found[0];
+      above += (int)__popcll(__ballot(in));
     }
-    above = ech::block_sum<kThreads>(above, scratch);
+    int unused;
+    above = waves_sum(above, scratch, &unused);
     if (tid == 0) w.above[((int64_t)b * 2 + LEVEL - 1) * w.blocks + blk] = above;
     prefix = (prefix << 11) | (uint32_t)s_found[0];
   }
   __syncthreads();
   constexpr int shift = LEVEL == 0 ? 21 : LEVEL == 1 ? 10 : 0, width = LEVEL == 2 ? 10 : 11;
-#pragma unroll
-  for (int j = 0; j < kBlockKpt; ++j) {
-    const int t = token_of<kBlockKpt>(t0, j);
-    const uint32_t k = weight_key(x[j]);
-    if (t >= r.lo && t < r.hi && (LEVEL == 0 || (k >> ((shift + width) & 31)) == prefix))
-      add_to_bin(hist, (k >> shift) & ((1u << width) - 1u));
-  }
+  count_digits<kBlockKpt>(k, LEVEL == 0, prefix, shift, width, hist);
   __syncthreads();
   int32_t* h = hist_of(w, LEVEL, b, blk);
   h[tid] = bin_count(hist, tid);
@@ -307,7 +371,8 @@ __global__ void __launch_bounds__(kThreads)
                             float* __restrict__ weight, int64_t weight_ld, int ends, int32_t* __restrict__ len_out,
                             LongWs w) {
   __shared__ int scratch[kWaves], s_found[2];
-  __shared__ int s_cnt[kWaves][2], s_tie0;
+  __shared__ __align__(8) int s_cnt[kWaves][2];
+  __shared__ int s_tie0;
   const int b = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x, t0 = blk * kBlock;
   const Row r = row_of(seq_len, b, max_len, keep, n_sink, n_recent);
   int32_t* kb = kept + (int64_t)b * keep;
@@ -321,14 +386,11 @@ __global__ void __launch_bounds__(kThreads)
   if (t0 >= r.n) return;
   const float* a = acc + (int64_t)b * acc_ld;
   float x[kBlockKpt];
-#pragma unroll
-  for (int j = 0; j < kBlockKpt; ++j) {
-    const int t = token_of<kBlockKpt>(t0, j);
-    x[j] = t < r.n ? a[t] : 0.f;
-  }
+  uint32_t k[kBlockKpt];
+  load_weights<kBlockKpt>(a, t0, max_len, x);
+  keys_of<kBlockKpt>(x, t0, r, k);
   uint32_t thr = 0xffffffffu;
-  int ties = 0, ties0 = 0, at0 = t0;
-  if (r.cut) at0 = min(t0, r.lo) + max(0, t0 - r.hi);       // protected tokens before the block
+  int ties = 0, ties0 = 0, at0 = r.lo;
   if (r.want > 0) {
     const int n_blk = (r.n + kBlock - 1) / kBlock;
     int before[2];
@@ -342,12 +404,18 @@ __global__ void __launch_bounds__(kThreads)
     int above = (bin0 > d2 ? before[0] : 0) + (bin0 - 1 > d2 ? before[1] : 0);
     for (int i = tid; i < blk; i += kThreads)
       above += w.above[(int64_t)b * 2 * w.blocks + i] + w.above[((int64_t)b * 2 + 1) * w.blocks + i];
-    above = ech::block_sum<kThreads>(above, scratch);       // its barriers publish s_tie0
+    int unused;
+    above = waves_sum(last_lane(lanes_scan(above)), scratch, &unused);   // its barrier publishes s_tie0
     ties0 = s_tie0;
     at0 += above + min(ties, ties0);
   }
-  write_kept<kBlockKpt>(x, r, t0, thr, ties, ties0, at0, keep, kb, weight ? weight + (int64_t)b * weight_ld : nullptr,
-                        s_cnt);
+  float* wb = weight ? weight + (int64_t)b * weight_ld : nullptr;
+  place_kept<kBlockKpt>(a, x, k, r, t0, thr, ties, ties0, at0, nk, s_cnt, [&](int place, int t, float v) {
+    if (place < keep) {
+      kb[place] = t;
+      if (wb) wb[place] = v;
+    }
+  });
 }
 
 // What has to wait until every block has read acc and seq_len, where an output
