@@ -264,3 +264,47 @@ def test_attention_without_lse(rows, ctx, H):
                        SCALE, out, ws=c.ws(ech.ech_paged_attn_ws_bytes, c.B, c.T, H, c.max_rows, c.max_len))
     torch.cuda.synchronize()
     np.testing.assert_array_equal(out.float().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize('scale', [0.0, -0.03])
+def test_scales_of_zero_and_below(scale):
+    need_gpu()
+    for rows, H in (([2, 1], 16), ([20, 3], 64)):
+        c = Case(rows, [300, 70], H, 16, seed=H)
+        ref = c.ref(scale=scale)
+        check_attn(c.attn(scale=scale), ref, c.max_len, f'scale {scale}')
+
+
+def test_every_call_beyond_32_bit_offsets():
+    """Pages behind the pool's first 4 GiB give what the same pages of a small
+    pool give."""
+    need_gpu()
+    page, n_pages = 64, 65600                    # 4.2M rows, 4.8 GB
+    r = np.random.default_rng(77)
+    big = torch.zeros((n_pages * page, 576), dtype=torch.int16, device='cuda')
+    base = n_pages - 60
+    for rows, H in (([1, 3], 16), ([40, 7], 64)):
+        c = Case(rows, [500, 90], H, page, seed=H, extra_pages=0)
+        n_tab = c.table.size                     # the small pool's second half takes the moved rows
+        c.pool, c.n_slots = np.concatenate([c.pool, np.zeros_like(c.pool)]), 2 * c.n_slots
+        assert n_tab * page * 2 == c.n_slots
+        x = dev(wk.to_bf16_bits(r.standard_normal((c.T, 576)).astype(np.float32)).view(np.int16))
+        lse = torch.zeros((c.T, H), device='cuda')
+        got = []
+        for pool, first in ((dev(c.pool.view(np.int16)), 0), (big, base)):
+            table = dev(c.table + first)
+            if first:
+                big[first * page:first * page + c.n_slots] = dev(c.pool.view(np.int16))
+            ech.ech_paged_append(pool, table, page, dev(c.row0), dev(c.seq_len), x)
+            acc = torch.zeros((2, c.max_len), device='cuda')
+            ech.ech_paged_weight(dev(c.q), lse, pool, table, page, dev(c.row0), dev(c.seq_len), c.max_rows, c.max_len,
+                                 SCALE, None, acc, ws=c.ws(ech.ech_paged_weight_ws_bytes, 2, c.T, H, c.max_rows, c.max_len))
+            n, kept, lo = dev(c.seq_len), torch.empty((2, 200), dtype=torch.int32, device='cuda'), torch.empty_like(dev(c.seq_len))
+            ech.ech_paged_evict(acc, n, c.max_len, 200, 4, 30, kept, lo, pool=pool, src_table=table,
+                                dst_table=table + n_tab, page_size=page)      # to the pages behind
+            ech.ech_paged_evict(acc, n, c.max_len, 200, 4, 30, kept, n, pool=pool, src_table=table, dst_table=table,
+                                page_size=page)                                                  # and in place
+            torch.cuda.synchronize()
+            got.append((host(acc), host(kept), pool[first * page:first * page + c.n_slots].clone()))
+        for small, large in zip(*got):
+            assert np.array_equal(small, large) if isinstance(small, np.ndarray) else torch.equal(small, large)
