@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(256, 1)
   auto pload = [&](int c, int r) -> bf16x8_t { return ld_bf16x8(pall + r * 32 * kPPitch + c * 32); };
 
   int page, off;                   // of the step to load next
+  int slot2;                       // of step 2
   uint32_t ok0, ok1, ok2;          // tokens with a slot of steps i, i + 1, i + 2
   {
     // a span shorter than three steps loads its last one again
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(256, 1)
     ok2 = (uint32_t)__ballot(s2 >= 0);
     issue(s0, 0);
     issue(s1, 1);
-    issue(s2, 2);
+    slot2 = s2;
   }
   {
     const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + g * 16;
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(256, 1)
   }
   __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
   __syncthreads();
+  issue(slot2, 2);                 // read a round later: the queries do not wait for it
   f32x16_t st, nx;
 #pragma unroll
   for (int v = 0; v < 16; ++v) st[v] = 0.f;
@@ -810,9 +812,12 @@ __global__ void __launch_bounds__(256)
     f32x4_t x[kG];
 #pragma unroll
     for (int u = 0; u < kG; ++u) {
-      const int s = min(s0 + u, n - 1);
-      a[u] = ml[(int64_t)s * kMT];
-      x[u] = po[s * stride];
+      a[u] = make_float2(-__builtin_inff(), 0.f);
+      x[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (s0 + u < n) {                                     // uniform: no load is repeated, none waits
+        a[u] = ml[(int64_t)(s0 + u) * kMT];
+        x[u] = po[(s0 + u) * stride];
+      }
     }
     float top = mx;
 #pragma unroll
@@ -823,7 +828,7 @@ __global__ void __launch_bounds__(256)
     o *= f;
 #pragma unroll
     for (int u = 0; u < kG; ++u) {
-      if (s0 + u < n && a[u].y != 0.f) {                    // a span that saw nothing wrote no output
+      if (a[u].y != 0.f) {                    // a span that saw nothing wrote no output
         const float w = exp2f((a[u].x == -__builtin_inff() ? ref : a[u].x) - ref);
         den += w * a[u].y;
         o += w * x[u];
