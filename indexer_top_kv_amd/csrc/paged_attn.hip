@@ -862,9 +862,9 @@ __global__ void __launch_bounds__(256)
         *reinterpret_cast<const u32x4_t*>(t + mm * kJoinPitch + (threadIdx.x & 3) * 16);
 }
 
-// Upper bound of the batch's tiles: every sequence rounds up once.
-int64_t tiles_of(int B, int T, int H, int max_rows, int per) {
-  const int64_t per_seq = ((int64_t)std::min(max_rows, T) * H + per - 1) / per;
+// Upper bound of the batch's tiles, when no row is two sequences': every
+// sequence rounds up once.
+int64_t tiles_of(int B, int T, int H, int64_t per_seq, int per) {
   return std::min<int64_t>(B * per_seq, (int64_t)T * H / per + B);
 }
 
@@ -880,10 +880,11 @@ Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n
   Split sp{};
   sp.narrow = (int64_t)std::min(max_rows, T) * H <= kNM;
   const int per = sp.narrow ? kNM : kMT;
-  sp.tiles = tiles_of(B, T, H, max_rows, per);
+  const int64_t per_seq = ((int64_t)std::min(max_rows, T) * H + per - 1) / per;
+  sp.tiles = tiles_of(B, T, H, per_seq, per);
   int64_t seen = max_len;                                  // tokens a tile can read
   if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1 + kStepTok);
-  sp.planned = sp.tiles <= kCus && seen > kMinSpan * kStepTok && plan_fits(B, sp.tiles, seen);
+  sp.planned = sp.tiles <= kCus && seen > kMinSpan * kStepTok && plan_fits(B, B * per_seq, seen);
   if (!sp.planned) return sp;
   sp.row_tiles = (int)((std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H) + 31) / 32);
   sp.part_ml = (size_t)kCus * sp.row_tiles * 32 * kPagedVal * sizeof(float);

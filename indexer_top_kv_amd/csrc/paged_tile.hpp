@@ -96,7 +96,7 @@ constexpr int kMinSpan = 4;          // steps a span is worth its start and its 
 constexpr int kPlanSeqs = 256;       // sequences a plan covers (four per lane)
 
 // Whether a plan covers B sequences, and its sums, steps of so many tiles that
-// read up to `tokens` each, stay in 31 bits.
+// read up to `tokens` each, stay in 31 bits (`tiles` whatever the row offsets say).
 inline bool plan_fits(int B, int64_t tiles, int64_t tokens) {
   return B <= kPlanSeqs && tiles * (tokens / kStepTok + 1) < (1ll << 30);
 }
@@ -152,11 +152,18 @@ __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* se
   tiles = last_lane(lanes_scan(tiles));
   total = last_lane(lanes_scan(total));
   longest = lanes_max(longest);
+  // ceil(x / S) by a reciprocal and one correction, which is exact: no S tried is
+  // below total / kCus, so no quotient is above kCus + 1
+  auto parts = [](int x, int S, float inv) -> int {
+    const int y = x + S - 1, n = (int)((float)y * inv), rest = y - n * S;
+    return n + (rest >= S) - (rest < 0);
+  };
   auto spans = [&](int S) -> int {
+    const float inv = __builtin_amdgcn_rcpf((float)S);
     int n = 0;
 #pragma unroll
     for (int c = 0; c < kPlanSeqs / 64; ++c)
-      if (c * 64 < B) n += nt[c] * ((st[c] + S - 1) / S);
+      if (c * 64 < B) n += nt[c] * parts(st[c], S, inv);
     return last_lane(lanes_scan(n));
   };
   int lo = max(kMinSpan * kStepTok / STEP, (total + kCus - 1) / kCus), hi = max(lo, longest);   // spans(hi) = tiles <= kCus
@@ -166,11 +173,12 @@ __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* se
     if (spans(mid) <= kCus) hi = mid;
     else lo = mid + 1;
   }
+  const float inv = __builtin_amdgcn_rcpf((float)hi);
   int base = 0, tile0 = 0;
 #pragma unroll
   for (int c = 0; c < kPlanSeqs / 64; ++c) {
     if (c * 64 < B) {
-      const int n = (st[c] + hi - 1) / hi, mine = nt[c] * n;
+      const int n = parts(st[c], hi, inv), mine = nt[c] * n;
       const int incl = lanes_scan(mine);
       const unsigned long long past = __ballot(base + incl > wg);
       if (past != 0ull) {
