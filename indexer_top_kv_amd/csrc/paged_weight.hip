@@ -16,9 +16,12 @@
 //  - More queries (chunks), which this form would have to pass the rows by more
 //    than once: 256 tokens' rows stay in registers (64 a wave, 288 registers)
 //    and the queries stream past; bound by the matrix cores: 4 chunks of 64 rows
-//    at 64 heads over 10K tokens 211-216 us, 890 TF/s (a step's products are
-//    2304 of its ~4000 cycles: the weights' exponentials and LDS reads take
-//    issue slots between them; a workgroup starts in 24K cycles, its rows' load).
+//    at 64 heads over 10K tokens 211-218 us, 880 TF/s. A step's products are 2304
+//    of its 4338 cycles, but fewer cycles do not help: with the row loads and the
+//    weights' instructions spread between the products it takes 3761, and the
+//    call as long, at a lower clock (1.8 GHz against the card's 2.4 while it
+//    runs over and over). What bounds it is the power the products, LDS reads
+//    and exponentials draw; without the exponentials it takes 172 us.
 #include <algorithm>
 
 #include "common.hpp"
