@@ -672,9 +672,10 @@ class PagedLayer:
     waits for the device. place(counts) does the host's part (its copies are on
     the current stream, before the kernels of launch), launch(q, rows) the
     step's kernels, trim() the eviction; a launch of the same T may be captured
-    and replayed, the tables and lengths being read in place. The
-    buffers a step returns are the layer's: the next step of the same T
-    writes them again. Steps of one layer must be ordered."""
+    and replayed, the tables and lengths being read in place. Buffers
+    and workspace of a step of at most B rows (decoding) are the layer's, and
+    the next step of the same T writes them again; those of more rows are new
+    each time. Steps of one layer must be ordered."""
 
     def __init__(self, B: int, H: int, n_pages: int, max_len: int, max_rows: int, page_size: int = 64,
                  sm_scale: float = 1.0 / 192.0 ** 0.5, window: int = 0, n_sink: int = 0,
@@ -699,17 +700,23 @@ class PagedLayer:
                          if budget is not None else None)
         self._bufs = {}
 
-    def _buffers(self, T: int):
-        if T not in self._bufs:
+    def _buffers(self, T: int, stream):
+        got = self._bufs.get(T)
+        if got is None:
             dev = dict(device=self.device)
             R = min(self.max_rows, T)
             ws = ech_paged_attn_ws_bytes(self.B, T, self.H, R, self.max_len, self.window, self.n_sink)
             if self.budget is not None:     # the two calls run one after the other: one workspace
                 ws = max(ws, ech_paged_weight_ws_bytes(self.B, T, self.H, R, self.max_len))
-            self._bufs[T] = (torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
-                             torch.empty((T, self.H), dtype=torch.float32, **dev),
-                             torch.empty(ws, dtype=torch.uint8, **dev))
-        return self._bufs[T]
+            got = (torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
+                   torch.empty((T, self.H), dtype=torch.float32, **dev),
+                   torch.empty(ws, dtype=torch.uint8, **dev))
+            if T <= self.B:
+                self._bufs[T] = got
+            elif stream is not None:        # freed when dropped: not before that stream is done with them
+                for t in got:
+                    t.record_stream(_as_stream(stream, self.device))
+        return got
 
     def place(self, counts) -> int:
         """Pages and lengths of a step that brings counts[b] rows to sequence
@@ -733,7 +740,7 @@ class PagedLayer:
         """The kernels of the step that place() prepared: q [T, H, 576], rows
         [T, 576] bf16 -> (out, lse)."""
         T, ps = q.shape[0], self.pages.page_size
-        out, lse, ws = self._buffers(T)
+        out, lse, ws = self._buffers(T, stream)
         ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
         ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
                        self.sm_scale, out, lse, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)

@@ -157,3 +157,25 @@ def test_release_and_refusals():
     layer.step(*z(64), [0, 64])
     with pytest.raises(ValueError):
         PagedLayer(1, 4, 4, 64, 8, n_sink=40, n_recent=30, budget=60)
+
+
+def test_chunks_of_many_sizes_keep_no_buffers():
+    """Only steps of at most B rows leave buffers with the layer; a chunk's
+    results are its own, on another stream too."""
+    need_gpu()
+    r = np.random.default_rng(9)
+    layer = PagedLayer(2, 16, n_pages=100, max_len=700, max_rows=64, page_size=16)
+    bits = lambda *s: dev(wk.to_bf16_bits(r.standard_normal(s).astype(np.float32))).view(torch.bfloat16)  # noqa: E731
+    outs = []
+    side = torch.cuda.Stream()
+    for T in (3, 17, 64, 40, 2, 1, 33):
+        q, x = bits(T, 16, 576), bits(T, 576)
+        layer.place([T, 0])
+        torch.cuda.synchronize()
+        got = layer.launch(q, x, stream=side)
+        junk = torch.full((T, 16, 512), 3.0, dtype=torch.bfloat16, device='cuda')
+        torch.cuda.synchronize()
+        outs.append((got[0], got[0].clone(), junk))
+    assert set(layer._bufs) == {1, 2}
+    for out, was, _ in outs[:4]:
+        assert torch.equal(out, was)
