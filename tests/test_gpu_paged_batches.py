@@ -308,3 +308,59 @@ def test_every_call_beyond_32_bit_offsets():
             got.append((host(acc), host(kept), pool[first * page:first * page + c.n_slots].clone()))
         for small, large in zip(*got):
             assert np.array_equal(small, large) if isinstance(small, np.ndarray) else torch.equal(small, large)
+
+
+def test_captured_chunks_and_evictions_share_a_workspace():
+    """Two graphs, of chunks under no limit and under a window, with one
+    workspace between them, each ending in an eviction (rows of one workgroup
+    and long rows, in place and to other pages): replayed in turn, with eager
+    work between, every replay equals the eager calls."""
+    need_gpu()
+    sides = []
+    for k, (rows, ctx, H, window, L) in enumerate((([70, 5], [900, 30], 64, 0, 1000), ([40, 9], [300, 600], 128, 100, 20000))):
+        c = Case(rows, ctx, H, 16, window, 4, seed=50 + k)
+        c.pool = np.concatenate([c.pool, c.pool])
+        t = dict(q=dev(c.q), table=dev(c.table), far=dev(c.table + len(c.pool) // 32), row0=dev(c.row0), n=dev(c.seq_len),
+                 pool=dev(c.pool.view(np.int16)), pool0=dev(c.pool.view(np.int16)),
+                 acc0=torch.rand((2, L), device='cuda'), acc=torch.empty((2, L), device='cuda'),
+                 out=torch.zeros((c.T, H, 512), dtype=torch.bfloat16, device='cuda'), lse=torch.zeros((c.T, H), device='cuda'),
+                 kept=torch.empty((2, 200), dtype=torch.int32, device='cuda'), lens=torch.empty(2, dtype=torch.int32, device='cuda'))
+        sides.append((c, t, L))
+    need = [max(ech.ech_paged_attn_ws_bytes(c.B, c.T, c.H, c.max_rows, L, c.window, c.sink),
+                ech.ech_paged_weight_ws_bytes(c.B, c.T, c.H, c.max_rows, L), ech.ech_paged_evict_ws_bytes(c.B, L, 200))
+            for c, _, L in sides]
+    ws = torch.full((max(need),), 0xff, dtype=torch.uint8, device='cuda')
+
+    def step(c, t, L):
+        t['pool'].copy_(t['pool0'])
+        t['acc'].copy_(t['acc0'])
+        ech.ech_paged_attn(t['q'], t['pool'], t['table'], 16, t['row0'], t['n'], c.max_rows, L, SCALE, t['out'], t['lse'],
+                           window=c.window, n_sink=c.sink, ws=ws)
+        ech.ech_paged_weight(t['q'], t['lse'], t['pool'], t['table'], 16, t['row0'], t['n'], c.max_rows, L, SCALE, t['acc'],
+                             t['acc'], decay=0.5, window=c.window, n_sink=c.sink, ws=ws)
+        ech.ech_paged_evict(t['acc'], t['n'], L, 200, 4, 50, t['kept'], t['lens'], acc_out=t['acc'], pool=t['pool'],
+                            src_table=t['table'], dst_table=t['table'] if c.window else t['far'], page_size=16, ws=ws)
+
+    names = ('out', 'lse', 'acc', 'kept', 'lens', 'pool')
+    want, graphs = [], []
+    for c, t, L in sides:
+        step(c, t, L)
+        torch.cuda.synchronize()
+        want.append({k: t[k].clone() for k in names})
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(c, t, L)
+        graphs.append(g)
+    for i in range(5):
+        for (c, t, L), w, g in zip(sides, want, graphs):
+            for k in names:
+                t[k].zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            for k in names:
+                a, b = t[k], w[k]
+                if k == 'acc':          # what lies behind the sequences is the caller's
+                    a, b = a[:, :200], b[:, :200]
+                assert torch.equal(a, b), (i, k)
+            y = torch.arange(4096, device='cuda', dtype=torch.float32)
+            assert float((y * 2).sum().item()) == 4096 * 4095
