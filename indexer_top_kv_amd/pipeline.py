@@ -41,6 +41,7 @@ order of the C-ABI calls and the stream events between them.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import List, Optional, Tuple
 
 import numpy as np
@@ -675,7 +676,14 @@ class PagedLayer:
     and replayed, the tables and lengths being read in place. Buffers
     and workspace of a step of at most B rows (decoding) are the layer's, and
     the next step of the same T writes them again; those of more rows are new
-    each time. Steps of one layer must be ordered."""
+    each time.
+
+    Steps of one layer run in the order of their calls, whatever streams these
+    name: each call's stream waits for the layer's last one, and a stream other
+    than the current one also for what is queued there (the copies of place, the
+    last users of the memory that the buffers get). Only a replay is outside of
+    this: it has to be on the stream of the place() before it, or to wait for
+    that stream, and the next call on the replay's stream, or after it."""
 
     def __init__(self, B: int, H: int, n_pages: int, max_len: int, max_rows: int, page_size: int = 64,
                  sm_scale: float = 1.0 / 192.0 ** 0.5, window: int = 0, n_sink: int = 0,
@@ -687,8 +695,8 @@ class PagedLayer:
         self.budget, self.n_recent, self.slack, self.decay = budget, n_recent, slack, decay
         self.pages = PageTables(B, n_pages, page_size, -(-max_len // page_size))
         dev = dict(device=device)
-        self.device = torch.device(device)
         self.pool = torch.zeros((n_pages * page_size, 576), dtype=torch.bfloat16, **dev)
+        self.device = self.pool.device      # with its index: the current device may change
         self.table = torch.from_numpy(self.pages.table).to(**dev)
         self.lens = np.zeros(B, np.int64)
         self.row0 = torch.zeros(B + 1, dtype=torch.int32, **dev)
@@ -699,8 +707,38 @@ class PagedLayer:
         self.evict_ws = (torch.empty(ech_paged_evict_ws_bytes(B, max_len, budget), dtype=torch.uint8, **dev)
                          if budget is not None else None)
         self._bufs = {}
+        self._last, self._done, self._streams = None, torch.cuda.Event(), set()
+        with self._call():                  # the zeros above come before the first call
+            pass
 
-    def _buffers(self, T: int, stream):
+    @contextlib.contextmanager
+    def _call(self, stream=None):
+        """The stream of a call, ordered behind the layer's last call and the
+        current stream. A capture orders nothing: it runs nothing."""
+        if self.device.type != 'cuda':      # host logic alone
+            yield None
+            return
+        s = _as_stream(stream, self.device)
+        if _capturing(s):
+            yield s
+            return
+        now = torch.cuda.current_stream(self.device)
+        if s != now:
+            s.wait_stream(now)
+        if self._last is not None and self._last != s:
+            s.wait_event(self._done)
+        if s not in self._streams:          # the layer's memory is not another's before s is done with it
+            self._streams.add(s)
+            for t in (self.pool, self.table, self.row0, self.seq_len, self.status, self.acc, self.kept, self.evict_ws):
+                if t is not None:
+                    t.record_stream(s)
+        try:
+            yield s
+        finally:
+            self._done.record(s)
+            self._last = s
+
+    def _buffers(self, T: int, s):
         got = self._bufs.get(T)
         if got is None:
             dev = dict(device=self.device)
@@ -713,9 +751,8 @@ class PagedLayer:
                    torch.empty(ws, dtype=torch.uint8, **dev))
             if T <= self.B:
                 self._bufs[T] = got
-            elif stream is not None:        # freed when dropped: not before that stream is done with them
-                for t in got:
-                    t.record_stream(_as_stream(stream, self.device))
+        for t in got:                       # freed when dropped: not before this stream is done with them
+            t.record_stream(s)
         return got
 
     def place(self, counts) -> int:
@@ -727,27 +764,30 @@ class PagedLayer:
         lens = self.lens + counts
         if np.any(lens > self.max_len):
             raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
-        if self.pages.resize(lens):
-            self.table.copy_(torch.from_numpy(self.pages.table))
+        moved = self.pages.resize(lens)
         self.lens = lens
         off = np.zeros(self.B + 1, np.int32)
         np.cumsum(counts, out=off[1:])
-        self.row0.copy_(torch.from_numpy(off))
-        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        with self._call():
+            if moved:
+                self.table.copy_(torch.from_numpy(self.pages.table))
+            self.row0.copy_(torch.from_numpy(off))
+            self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
         return int(off[-1])
 
     def launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
         """The kernels of the step that place() prepared: q [T, H, 576], rows
         [T, 576] bf16 -> (out, lse)."""
         T, ps = q.shape[0], self.pages.page_size
-        out, lse, ws = self._buffers(T, stream)
-        ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
-        ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
-                       self.sm_scale, out, lse, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
-        if self.budget is not None:
-            ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
-                             self.sm_scale, self.acc, self.acc, decay=self.decay, window=self.window,
-                             n_sink=self.n_sink, ws=ws, stream=stream)
+        with self._call(stream) as s:
+            out, lse, ws = self._buffers(T, s)
+            ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
+            ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
+                           self.sm_scale, out, lse, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+            if self.budget is not None:
+                ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows,
+                                 self.max_len, self.sm_scale, self.acc, self.acc, decay=self.decay,
+                                 window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
         return out, lse
 
     def trim(self, stream=None) -> bool:
@@ -755,13 +795,14 @@ class PagedLayer:
         that are longer than budget go with them); True if any was."""
         if self.budget is None or not np.any(self.lens > self.budget + self.slack):
             return False
-        ech_paged_evict(self.acc, self.seq_len, self.max_len, self.budget, self.n_sink, self.n_recent, self.kept,
-                        self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
-                        page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
-        self.lens = np.minimum(self.lens, self.budget)
-        if self.pages.resize(self.lens):
-            with torch.cuda.stream(_as_stream(stream, self.device)):
-                self.table.copy_(torch.from_numpy(self.pages.table))
+        with self._call(stream) as s:
+            ech_paged_evict(self.acc, self.seq_len, self.max_len, self.budget, self.n_sink, self.n_recent, self.kept,
+                            self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
+                            page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
+            self.lens = np.minimum(self.lens, self.budget)
+            if self.pages.resize(self.lens):
+                with torch.cuda.stream(s):
+                    self.table.copy_(torch.from_numpy(self.pages.table))
         return True
 
     def step(self, q: torch.Tensor, rows: torch.Tensor, counts):
@@ -780,13 +821,22 @@ class PagedLayer:
         lens[b] = 0
         self.pages.resize(lens)
         self.lens = lens
-        self.table.copy_(torch.from_numpy(self.pages.table))
-        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
-        if self.acc is not None:
-            self.acc[b].zero_()
+        with self._call():
+            self.table.copy_(torch.from_numpy(self.pages.table))
+            self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+            if self.acc is not None:
+                self.acc[b].zero_()
 
 
 def _as_stream(stream, device):
     if stream is None:
         return torch.cuda.current_stream(device)
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _capturing(s) -> bool:
+    """Whether the current stream or s records a graph."""
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    with torch.cuda.stream(s):
+        return torch.cuda.is_current_stream_capturing()

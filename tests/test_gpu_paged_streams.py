@@ -1,0 +1,70 @@
+"""PagedLayer over several streams: its calls run in their order whatever
+streams they name, and its buffers take no memory that another stream still
+uses. A step on one stream is the reference; results have to be the same bits."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as wk
+from gpu_util import dev, need_gpu
+from indexer_top_kv_amd.pipeline import PagedLayer
+
+pytestmark = pytest.mark.gpu
+WAIT = 1_000_000    # cycles of a bounded spin: long beside a step, milliseconds at most
+
+
+def bits(r, *shape):
+    return dev(wk.to_bf16_bits(r.standard_normal(shape).astype(np.float32))).view(torch.bfloat16)
+
+
+def test_calls_on_changing_streams_run_in_order():
+    """place on the current stream, launch and trim on others, each stream kept
+    busy before the call: lengths, tables, weights, rows and outputs as with
+    one stream. The budget is a whole number of pages, so that some evictions
+    change no table."""
+    need_gpu()
+    r = np.random.default_rng(21)
+    mk = lambda: PagedLayer(2, 16, n_pages=60, max_len=400, max_rows=80, page_size=16, budget=64, n_sink=2,  # noqa: E731
+                            n_recent=8, decay=0.5)
+    a, b = mk(), mk()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    steps = [[70, 3], [1, 1], [1, 61], [2, 1], [1, 1], [0, 1], [5, 60], [1, 1], [1, 1]]
+    for i, counts in enumerate(steps):
+        T = sum(counts)
+        q, x = bits(r, T, 16, 576), bits(r, T, 576)
+        torch.cuda.synchronize()            # q and x are there for every stream
+        for st in sides:
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(WAIT)
+        a.place(counts)
+        out, lse = a.launch(q, x, stream=sides[i % 2])
+        a.trim(stream=(None, sides[0], sides[1])[i % 3])
+        want = b.step(q, x, counts)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), i
+        for name in ('acc', 'seq_len', 'table', 'pool', 'row0'):
+            assert torch.equal(getattr(a, name), getattr(b, name)), (i, name)
+        assert a.lens.tolist() == b.lens.tolist() == b.seq_len.tolist()
+    a.release(0)
+    a.place([1, 0])
+    assert a.device.index == a.pool.device.index is not None
+
+
+def test_a_launch_elsewhere_takes_no_memory_still_in_use():
+    """A chunk's outputs may get memory that was freed while the current stream
+    has yet to read it: the launch's stream waits for that."""
+    need_gpu()
+    r = np.random.default_rng(22)
+    layer = PagedLayer(2, 16, n_pages=20, max_len=300, max_rows=64, page_size=16)
+    side, T = torch.cuda.Stream(), 40
+    q, x = bits(r, T, 16, 576), bits(r, T, 576)
+    layer.place([T, 0])
+    torch.cuda.synchronize()
+    old = torch.full((T, 16, 512), 5.0, dtype=torch.bfloat16, device='cuda')
+    seen = torch.empty_like(old)
+    torch.cuda._sleep(WAIT)
+    seen.copy_(old)
+    del old
+    out, _ = layer.launch(q, x, stream=side)
+    torch.cuda.synchronize()
+    assert torch.all(seen == 5.0) and not torch.any(torch.isnan(out))
