@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(256)
 // 128-byte column of its sequence's rows, kWithin rows a thread under way at a
 // time (their entries, then the rows, without a branch between), and all columns
 // of a sequence run on one XCD: lines that its columns share, and writes to
-// them, meet in one cache. 32 x 8192 rows of 1152 bytes 143 us, bound by the
+// them, meet in one cache: grid (8 x columns, ceil(B / 8)), whose workgroups go
+// to the XCDs in turn. 32 x 8192 rows of 1152 bytes 143 us, bound by the
 // rows (to other pages 128 us); one sequence of 8192 rows 38 us, bound by the
 // waits of its batches. (64-byte columns spread over the XCDs, a row a thread
 // and batch: 198 and 40 us; 512 threads 144 and 44 us.)
@@ -493,8 +494,8 @@ constexpr int kWithin = 4, kWithinThreads = 1024, kWithinCol = 8;   // pieces a 
 __global__ void __launch_bounds__(kWithinThreads)
     paged_move_within_kernel(u32x4_t* __restrict__ pool, int row16, Pages pg, const int32_t* __restrict__ kept, int keep,
                              int most, int B) {
-  const int cols = (row16 + kWithinCol - 1) / kWithinCol, i = blockIdx.x >> 3, b = i / cols * 8 + (blockIdx.x & 7);
-  const int c = i % cols * kWithinCol + (int)threadIdx.x % kWithinCol;
+  const int b = blockIdx.y * 8 + (blockIdx.x & 7);
+  const int c = (int)(blockIdx.x >> 3) * kWithinCol + (int)threadIdx.x % kWithinCol;
   if (b >= B) return;
   const int32_t* row = pg.table + (int64_t)b * pg.ld;
   const int32_t* kb = kept + (int64_t)b * keep;
@@ -642,7 +643,7 @@ extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* 
   const dim3 mgrid((std::min(keep, max_len) + kMoveRows - 1) / kMoveRows, B);
   if (mgrid.x == 0) return ECH_OK;
   if (src_table == dst_table)
-    hipLaunchKernelGGL(paged_move_within_kernel, dim3((row16 + kWithinCol - 1) / kWithinCol * ((B + 7) / 8 * 8)),
+    hipLaunchKernelGGL(paged_move_within_kernel, dim3((row16 + kWithinCol - 1) / kWithinCol * 8, (B + 7) / 8),
                        dim3(kWithinThreads), 0, s, static_cast<u32x4_t*>(pool), row16, a, kept, keep, std::min(keep, max_len), B);
   else if (row16 == kPagedChunks)
     hipLaunchKernelGGL(paged_move_kernel<kPagedChunks>, mgrid, dim3(256), 0, s, static_cast<u32x4_t*>(pool), row16, a, d, kept,
