@@ -480,7 +480,8 @@ int ech_kv_append(void* host_pool, int64_t P, int64_t row_bytes, void* kcache, i
  * sets ECH_ST_FULL in *status (int32, device; NULL: no word). Page tables must
  * not give two of the step's positions the same slot.
  *  rows [T, row_bytes], row_stride bytes apart, 16-byte aligned; row_bytes and
- *  row_stride multiples of 16, row_bytes <= row_stride. pool 16-byte aligned.
+ *  row_stride multiples of 16, row_bytes <= row_stride, row_bytes <= 2^20. pool
+ *  16-byte aligned. T <= 2^30.
  */
 int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, int page_size, const int32_t* page_table,
                      int64_t pt_ld, const int32_t* row0, const int32_t* seq_len, int B, int T, const void* rows,
@@ -551,7 +552,7 @@ int ech_paged_weight(const void* q, int64_t q_row_stride, int64_t q_head_stride,
  * is not moved. In place, no two sequences may share a page, and no page
  * may occur twice.
  *  keep >= 1, n_sink + n_recent <= keep, max_len <= 2^24, acc_ld >= max_len,
- *  row_bytes a multiple of 16, pool 16-byte aligned.
+ *  row_bytes a multiple of 16, at most 2^20, pool 16-byte aligned.
  *  ws ech_paged_evict_ws_bytes(...) bytes, as for ech_paged_attn.
  */
 size_t ech_paged_evict_ws_bytes(int B, int max_len, int keep);

@@ -8,16 +8,18 @@
 
 namespace {
 
-// grid (ceil(T / 4)), 256 threads: one wave per row, which finds its sequence by
-// counting the row ends at or before it, 64 sequences a round. Bound by the
-// rows' bytes, or with few rows by the two dependent reads (offsets, page) and
-// the launch: 16384 rows of 1152 bytes 5.8 us (6.5 TB/s of reads and writes, a
+// grid (x, y) of ceil(T / 4) workgroups or a few more, 256 threads (x is at most
+// kAppendX: a launch has less than 2^32 threads in x). One wave per row, which
+// finds its sequence by counting the row ends at or before it, 64 sequences a
+// round. Bound by the rows' bytes, or with few rows by the two dependent reads
+// (offsets, page) and the launch: 16384 rows of 1152 bytes 5.8 us (6.5 TB/s of reads and writes, a
 // part of them from cache), 64 rows 3.1 us.
+constexpr int kAppendX = 1 << 22;
 __global__ void __launch_bounds__(256)
     paged_append_kernel(uint4* __restrict__ pool, int row16, Pages pg, const int32_t* __restrict__ row0,
                         const int32_t* __restrict__ seq_len, int B, int T, const uint4* __restrict__ rows,
                         int64_t row_stride16, int32_t* __restrict__ status) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int t = (int)(blockIdx.y * kAppendX + blockIdx.x) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;   // < 2^31
   if (t >= T || t < row0[0]) return;
   // the sequence whose rows end past t: as many as end at or before it precede it
   int b = 0;
@@ -542,7 +544,9 @@ extern "C" int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, 
     return ECH_EINVAL;
   if (T == 0) return ECH_OK;
   const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
-  hipLaunchKernelGGL(paged_append_kernel, dim3((T + 3) / 4), dim3(256), 0, reinterpret_cast<hipStream_t>(stream),
+  const int wgs = (T + 3) / 4;
+  hipLaunchKernelGGL(paged_append_kernel, dim3(std::min(wgs, kAppendX), (wgs + kAppendX - 1) / kAppendX), dim3(256), 0,
+                     reinterpret_cast<hipStream_t>(stream),
                      static_cast<uint4*>(pool), (int)(row_bytes / 16), pg, row0, seq_len, B, T,
                      static_cast<const uint4*>(rows), row_stride / 16, status);
   ECH_LAUNCH_CHECK();
