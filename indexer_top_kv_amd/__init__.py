@@ -309,6 +309,12 @@ def _ws_arg(ws: Optional[torch.Tensor], device: int):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _fits(*numbers: int) -> None:
+    """Refuse numbers that the C ABI's 32-bit arguments would cut."""
+    if max(numbers) > 0x7fffffff or min(numbers) < -0x80000000:
+        raise ValueError(f'{numbers}: one of these needs more than 32 bits')
+
+
 def _call(fn: str, device: int, stream, *args) -> None:
     """The library's call on the device of its tensors: on the caller's stream,
     or on that device's current one."""
@@ -334,6 +340,7 @@ def ech_paged_append(pool, page_table, page_size: int, row0, seq_len, rows, stat
     """A step's new rows [T, row] go into their sequences' pages: pool [slots,
     row] (any type, the type of `rows`), page_table [B, pages] i32, row0 [B+1]
     i32, seq_len [B] i32 (with the new rows), status [1] i32 or None."""
+    _fits(page_size, rows.shape[0], seq_len.numel())
     dev, B = _batch_args(pool, page_table, row0, seq_len)
     n_slots, width = have = _pair('pool', pool)
     dtype = (pool.dtype,)
@@ -349,6 +356,7 @@ def ech_paged_append(pool, page_table, page_size: int, row0, seq_len, rows, stat
 
 def ech_paged_attn_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int, window: int = 0,
                             n_sink: int = 0) -> int:
+    _fits(B, T, H, max_rows, max_len, window, n_sink)
     return int(lib().ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink))
 
 
@@ -358,6 +366,7 @@ def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows:
     an optional sliding window and n_sink first tokens that stay visible: q
     [T, H, 576] bf16 (or its bits; rows and heads may be strided), pool [slots,
     576] bf16 -> out [T, H, 512] bf16, lse [T, H] fp32 (optional)."""
+    _fits(page_size, max_rows, max_len, window, n_sink, q.shape[0], seq_len.numel())
     _arg('pool', pool, _BITS16, (pool.shape[0], 576), pool.get_device())
     dev, B = _batch_args(pool, page_table, row0, seq_len)
     T, H = q.shape[0], q.shape[1] if q.dim() == 3 else -1
@@ -372,6 +381,7 @@ def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows:
 
 
 def ech_paged_weight_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int) -> int:
+    _fits(B, T, H, max_rows, max_len)
     return int(lib().ech_paged_weight_ws_bytes(B, T, H, max_rows, max_len))
 
 
@@ -381,6 +391,7 @@ def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, ma
     """The attention weight each cached token received from the step's rows
     and heads (lse: that of ech_paged_attn), added to decay * acc_in: acc_in
     [B, >= max_len] fp32 or None, acc_out like it (may be acc_in)."""
+    _fits(page_size, max_rows, max_len, window, n_sink, q.shape[0], seq_len.numel())
     _arg('pool', pool, _BITS16, (pool.shape[0], 576), pool.get_device())
     dev, B = _batch_args(pool, page_table, row0, seq_len)
     T, H = q.shape[0], q.shape[1] if q.dim() == 3 else -1
@@ -397,6 +408,7 @@ def ech_paged_weight(q, lse, pool, page_table, page_size: int, row0, seq_len, ma
 
 
 def ech_paged_evict_ws_bytes(B: int, max_len: int, keep: int) -> int:
+    _fits(B, max_len, keep)
     return int(lib().ech_paged_evict_ws_bytes(B, max_len, keep))
 
 
@@ -408,6 +420,7 @@ def ech_paged_evict(acc, seq_len, max_len: int, keep: int, n_sink: int, n_recent
     None. With a pool the kept rows move from src_table's pages to dst_table's
     (src_table itself: compacted in place)."""
     dev, B = acc.get_device(), seq_len.numel()
+    _fits(B, max_len, keep, n_sink, n_recent, page_size)
     _arg('seq_len', seq_len, _I32, (B,), dev)
     ld = _pair('acc', acc)[1]
     _arg('acc', acc, _F32, (B, ld), dev)

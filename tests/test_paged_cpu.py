@@ -136,3 +136,34 @@ def test_workspace_of_long_batches():
     assert ech.ech_paged_attn_ws_bytes(256, 256, 128, 1, 1 << 20) > 0
     assert ech.ech_paged_attn_ws_bytes(256, 256, 128, 1, 1 << 30) == 0
     assert ech.ech_paged_attn_ws_bytes(1, 1, 128, 1, 1 << 30) > 0
+
+
+def test_binding_refuses_numbers_beyond_32_bits():
+    """ctypes would cut them: 2^32 + 100 tokens would have been 100."""
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)  # noqa: E731
+    q, out, lse = z(2, 4, 576, dt=torch.bfloat16), z(2, 4, 512, dt=torch.bfloat16), z(2, 4, dt=torch.float32)
+    pool, table, row0, n, acc = z(64, 576, dt=torch.bfloat16), z(1, 4), z(2), z(1), z(1, 64, dt=torch.float32)
+    far = (1 << 32) + 100
+    ok = dict(page_size=16, max_rows=2, max_len=64, window=0, n_sink=0)
+    beyond = 'more than 32 bits'    # found before the tensors' place, the host, is
+    for name in ok:
+        for v in (far, -far):
+            a = {**ok, name: v}
+            head = (table, a['page_size'], row0, n, a['max_rows'], a['max_len'], 0.1)
+            tail = dict(window=a['window'], n_sink=a['n_sink'])
+            with pytest.raises(ValueError, match=beyond):
+                ech.ech_paged_attn(q, pool, *head, out, **tail)
+            with pytest.raises(ValueError, match=beyond):
+                ech.ech_paged_weight(q, lse, pool, *head, None, acc, **tail)
+            if name != 'page_size':
+                with pytest.raises(ValueError, match=beyond):
+                    ech.ech_paged_attn_ws_bytes(1, 2, 4, a['max_rows'], a['max_len'], **tail)
+    with pytest.raises(ValueError, match=beyond):
+        ech.ech_paged_append(pool, table, far, row0, n, pool[:2])
+    for call in (lambda: ech.ech_paged_weight_ws_bytes(1, 2, 4, 2, far), lambda: ech.ech_paged_evict_ws_bytes(1, far, 8),
+                 lambda: ech.ech_paged_evict_ws_bytes(far, 64, 8),
+                 lambda: ech.ech_paged_evict(acc, n, far, 8, 0, 0, z(1, 8), z(1)),
+                 lambda: ech.ech_paged_evict(acc, n, 64, 8, far, 0, z(1, 8), z(1)),
+                 lambda: ech.ech_paged_evict(acc, n, 64, 8, 0, far, z(1, 8), z(1))):
+        with pytest.raises(ValueError, match=beyond):
+            call()
