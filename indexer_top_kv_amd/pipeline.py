@@ -706,7 +706,7 @@ class PagedLayer:
         self.kept = torch.empty((B, budget), dtype=torch.int32, **dev) if budget is not None else None
         self.evict_ws = (torch.empty(ech_paged_evict_ws_bytes(B, max_len, budget), dtype=torch.uint8, **dev)
                          if budget is not None else None)
-        self._bufs = {}
+        self._bufs, self._placed = {}, 0
         self._last, self._done, self._streams = None, torch.cuda.Event(), set()
         with self._call():                  # the zeros above come before the first call
             pass
@@ -755,6 +755,20 @@ class PagedLayer:
             t.record_stream(s)
         return got
 
+    def _check_rows(self, q: torch.Tensor, rows: torch.Tensor) -> None:
+        """Refuse a step's tensors before anything of it is done."""
+        T, bits = q.shape[0], (torch.bfloat16, torch.int16, torch.uint16)
+        for name, t, shape, types in (('q', q, (T, self.H, 576), bits), ('rows', rows, (T, 576), bits[:1])):
+            if t.shape != shape or t.dtype not in types or t.device != self.device:
+                raise ValueError(f'{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {types[0]} on '
+                                 f'{self.device}')
+            steps = [st for n, st in zip(t.shape, t.stride()) if n > 1]
+            if t.stride(-1) != 1 or any(st % 8 for st in steps[:-1]) or t.data_ptr() % 16:
+                raise ValueError(f'{name}: strides {t.stride()} at {t.data_ptr():#x}, expected a dense last dimension and '
+                                 f'multiples of 16 bytes')
+        if T > 1 and rows.stride(0) < 576:
+            raise ValueError(f'rows: strides {rows.stride()}, the rows overlap')
+
     def place(self, counts) -> int:
         """Pages and lengths of a step that brings counts[b] rows to sequence
         b; returns T. Raises, with nothing changed, if they do not fit."""
@@ -765,7 +779,7 @@ class PagedLayer:
         if np.any(lens > self.max_len):
             raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
         moved = self.pages.resize(lens)
-        self.lens = lens
+        self.lens, self._placed = lens, int(counts.sum())
         off = np.zeros(self.B + 1, np.int32)
         np.cumsum(counts, out=off[1:])
         with self._call():
@@ -773,12 +787,16 @@ class PagedLayer:
                 self.table.copy_(torch.from_numpy(self.pages.table))
             self.row0.copy_(torch.from_numpy(off))
             self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
-        return int(off[-1])
+        return self._placed
 
     def launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
         """The kernels of the step that place() prepared: q [T, H, 576], rows
-        [T, 576] bf16 -> (out, lse)."""
+        [T, 576] bf16 -> (out, lse). T is at least the number of rows placed;
+        those behind are no sequence's, and their outputs mean nothing."""
+        self._check_rows(q, rows)
         T, ps = q.shape[0], self.pages.page_size
+        if T < self._placed:
+            raise ValueError(f'{self._placed} rows were placed, q has {T}')
         with self._call(stream) as s:
             out, lse, ws = self._buffers(T, s)
             ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
@@ -810,6 +828,7 @@ class PagedLayer:
         T = int(np.sum(counts))
         if q.shape[0] != T or rows.shape[0] != T:
             raise ValueError(f'counts name {T} rows, q has {q.shape[0]} and rows {rows.shape[0]}')
+        self._check_rows(q, rows)
         self.place(counts)
         got = self.launch(q, rows)
         self.trim()

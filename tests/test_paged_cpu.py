@@ -167,3 +167,30 @@ def test_binding_refuses_numbers_beyond_32_bits():
                  lambda: ech.ech_paged_evict(acc, n, 64, 8, 0, far, z(1, 8), z(1))):
         with pytest.raises(ValueError, match=beyond):
             call()
+
+
+def test_layer_refuses_a_step_before_anything_moves():
+    """Wrong shapes, types, places or strides: no pages, lengths or offsets
+    change."""
+    from indexer_top_kv_amd.pipeline import PagedLayer
+    layer = PagedLayer(2, 4, n_pages=20, max_len=100, max_rows=50, page_size=16, budget=60, device='cpu')
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
+    layer.place([20, 3])
+    lens, table = layer.lens.copy(), layer.pages.table.copy()
+    row0, n = layer.row0.clone(), layer.seq_len.clone()
+    bad = [(z(33, 8, 576), z(33, 576)), (z(33, 4, 512), z(33, 576)), (z(33, 4, 576), z(33, 512)),
+           (z(33, 4, 576, dt=torch.float16), z(33, 576)), (z(33, 4, 576), z(33, 576, dt=torch.float16)),
+           (z(33, 4, 576), z(33, 576, dt=torch.int16)), (z(33, 4, 576), z(32, 576)), (z(32, 4, 576), z(33, 576)),
+           (z(33, 4, 1152)[..., ::2], z(33, 576)), (z(33, 4, 580)[..., :576], z(33, 576)),
+           (z(33 * 4 * 576 + 1)[1:].view(33, 4, 576), z(33, 576)), (z(33, 4, 576), z(33, 577)[:, :576]),
+           (z(33, 4, 576), z(1, 576).expand(33, -1)), (z(33, 4, 576, dt=torch.int64), z(33, 576)),
+           (z(33, 4, 576).to('meta'), z(33, 576))]
+    for q, x in bad:
+        with pytest.raises(ValueError):
+            layer.step(q, x, [1, 32])
+        with pytest.raises(ValueError):
+            layer.launch(q, x)
+        assert np.array_equal(layer.lens, lens) and np.array_equal(layer.pages.table, table)
+        assert torch.equal(layer.row0, row0) and torch.equal(layer.seq_len, n)
+    with pytest.raises(ValueError, match='23 rows were placed'):
+        layer.launch(z(22, 4, 576), z(22, 576))
