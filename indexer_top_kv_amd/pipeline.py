@@ -673,10 +673,12 @@ class PagedLayer:
     waits for the device. place(counts) does the host's part (its copies are on
     the current stream, before the kernels of launch), launch(q, rows) the
     step's kernels, trim() the eviction; a launch of the same T may be captured
-    and replayed, the tables and lengths being read in place. Buffers
-    and workspace of a step of at most B rows (decoding) are the layer's, and
-    the next step of the same T writes them again; those of more rows are new
-    each time.
+    and replayed, the tables and lengths being read in place (the kernels' forms
+    are chosen by the step's largest count and length; for a captured launch by
+    the max_rows that place was given, else by the layer's). Buffers and
+    workspace of a step of at most B rows (decoding) are the layer's, and the
+    next step of the same T writes them again; those of more rows are new each
+    time.
 
     Steps of one layer run in the order of their calls, whatever streams these
     name: each call's stream waits for the layer's last one, and a stream other
@@ -706,7 +708,8 @@ class PagedLayer:
         self.kept = torch.empty((B, budget), dtype=torch.int32, **dev) if budget is not None else None
         self.evict_ws = (torch.empty(ech_paged_evict_ws_bytes(B, max_len, budget), dtype=torch.uint8, **dev)
                          if budget is not None else None)
-        self._bufs, self._placed = {}, 0
+        self._bufs, self._ws = {}, {}       # of decoding steps: by T; by size
+        self._placed, self._most, self._fixed = 0, 0, None
         self._last, self._done, self._streams = None, torch.cuda.Event(), set()
         with self._call():                  # the zeros above come before the first call
             pass
@@ -738,22 +741,39 @@ class PagedLayer:
             self._done.record(s)
             self._last = s
 
-    def _buffers(self, T: int, s):
+    def _bounds(self, capturing: bool) -> Tuple[int, int]:
+        """Host bounds of the placed step's rows a sequence and lengths, by which
+        the calls choose their forms: its own ones (a few lengths share one, so
+        that they share buffers). A captured launch holds for other steps too."""
+        if capturing:
+            return self.max_rows if self._fixed is None else self._fixed, self.max_len
+        return self._most if self._fixed is None else self._fixed, self._len_bound()
+
+    def _len_bound(self) -> int:
+        return min(self.max_len, 1 << max(int(self.lens.max()) - 1, 0).bit_length())
+
+    def _ws_bytes(self, T: int, R: int, L: int) -> int:
+        n = ech_paged_attn_ws_bytes(self.B, T, self.H, min(R, T), L, self.window, self.n_sink)
+        if self.budget is not None:         # the two calls run one after the other: one workspace
+            n = max(n, ech_paged_weight_ws_bytes(self.B, T, self.H, min(R, T), L))
+        return n
+
+    def _buffers(self, T: int, ws_bytes: int, s):
+        dev, keep = dict(device=self.device), T <= self.B
         got = self._bufs.get(T)
         if got is None:
-            dev = dict(device=self.device)
-            R = min(self.max_rows, T)
-            ws = ech_paged_attn_ws_bytes(self.B, T, self.H, R, self.max_len, self.window, self.n_sink)
-            if self.budget is not None:     # the two calls run one after the other: one workspace
-                ws = max(ws, ech_paged_weight_ws_bytes(self.B, T, self.H, R, self.max_len))
             got = (torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
-                   torch.empty((T, self.H), dtype=torch.float32, **dev),
-                   torch.empty(ws, dtype=torch.uint8, **dev))
-            if T <= self.B:
+                   torch.empty((T, self.H), dtype=torch.float32, **dev))
+            if keep:
                 self._bufs[T] = got
-        for t in got:                       # freed when dropped: not before this stream is done with them
+        ws = self._ws.get(ws_bytes) if keep else None
+        if ws is None:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, **dev)
+            if keep:
+                self._ws[ws_bytes] = ws
+        for t in (*got, ws):                # freed when dropped: not before this stream is done with them
             t.record_stream(s)
-        return got
+        return (*got, ws)
 
     def _check_rows(self, q: torch.Tensor, rows: torch.Tensor) -> None:
         """Refuse a step's tensors before anything of it is done."""
@@ -769,17 +789,25 @@ class PagedLayer:
         if T > 1 and rows.stride(0) < 576:
             raise ValueError(f'rows: strides {rows.stride()}, the rows overlap')
 
-    def place(self, counts) -> int:
+    def place(self, counts, max_rows: Optional[int] = None) -> int:
         """Pages and lengths of a step that brings counts[b] rows to sequence
-        b; returns T. Raises, with nothing changed, if they do not fit."""
+        b; returns T. Raises, with nothing changed, if they do not fit.
+        max_rows: the number of rows a sequence that the step's launch is made
+        for, where that is to be more than the largest count. A launch captured
+        after it is valid for steps that are placed with the same max_rows (1:
+        decoding); one captured after a place without it for any step."""
         counts = np.asarray(counts, np.int64)
-        if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > self.max_rows):
-            raise ValueError(f'counts must be {self.B} numbers from 0 to max_rows = {self.max_rows}')
+        most = self.max_rows if max_rows is None else max_rows
+        if most > self.max_rows:
+            raise ValueError(f'max_rows {max_rows}, the layer has {self.max_rows}')
+        if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > most):
+            raise ValueError(f'counts must be {self.B} numbers from 0 to max_rows = {most}')
         lens = self.lens + counts
         if np.any(lens > self.max_len):
             raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
         moved = self.pages.resize(lens)
         self.lens, self._placed = lens, int(counts.sum())
+        self._most, self._fixed = int(counts.max()), max_rows
         off = np.zeros(self.B + 1, np.int32)
         np.cumsum(counts, out=off[1:])
         with self._call():
@@ -798,14 +826,15 @@ class PagedLayer:
         if T < self._placed:
             raise ValueError(f'{self._placed} rows were placed, q has {T}')
         with self._call(stream) as s:
-            out, lse, ws = self._buffers(T, s)
+            R, L = self._bounds(_capturing(s))
+            out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s)
             ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
-            ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows, self.max_len,
-                           self.sm_scale, out, lse, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+            ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
+                           window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
             if self.budget is not None:
-                ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, self.max_rows,
-                                 self.max_len, self.sm_scale, self.acc, self.acc, decay=self.decay,
-                                 window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+                ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale,
+                                 self.acc, self.acc, decay=self.decay, window=self.window, n_sink=self.n_sink, ws=ws,
+                                 stream=stream)
         return out, lse
 
     def trim(self, stream=None) -> bool:
@@ -814,8 +843,9 @@ class PagedLayer:
         if self.budget is None or not np.any(self.lens > self.budget + self.slack):
             return False
         with self._call(stream) as s:
-            ech_paged_evict(self.acc, self.seq_len, self.max_len, self.budget, self.n_sink, self.n_recent, self.kept,
-                            self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
+            # weights at and past every length are 0 as they are: none is behind the bound
+            ech_paged_evict(self.acc, self.seq_len, self._len_bound(), self.budget, self.n_sink, self.n_recent,
+                            self.kept, self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
                             page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
             self.lens = np.minimum(self.lens, self.budget)
             if self.pages.resize(self.lens):

@@ -179,3 +179,86 @@ def test_chunks_of_many_sizes_keep_no_buffers():
     assert set(layer._bufs) == {1, 2}
     for out, was, _ in outs[:4]:
         assert torch.equal(out, was)
+
+
+def test_rows_behind_the_last_sequence_are_ignored():
+    """A launch of more rows than were placed (a captured one of a smaller
+    batch): the placed ones' results are those of a launch without them."""
+    need_gpu()
+    r = np.random.default_rng(11)
+    bits = lambda *s: dev(wk.to_bf16_bits(r.standard_normal(s).astype(np.float32))).view(torch.bfloat16)  # noqa: E731
+    a, b = (PagedLayer(3, 16, n_pages=60, max_len=300, max_rows=64, page_size=16, budget=200) for _ in range(2))
+    for counts in ([40, 0, 7], [1, 0, 1], [1, 1, 0]):
+        T = sum(counts)
+        q, x = bits(T + 5, 16, 576), bits(T + 5, 576)
+        assert a.place(counts) == T
+        out, lse = a.launch(q, x)
+        want = b.step(q[:T], x[:T], counts)
+        torch.cuda.synchronize()
+        assert torch.equal(out[:T], want[0]) and torch.equal(lse[:T], want[1])
+        assert torch.equal(a.pool, b.pool) and torch.equal(a.acc, b.acc)
+    assert int(a.status.item()) == 0
+    with pytest.raises(ValueError):
+        a.place([5, 0, 0])
+        a.launch(bits(4, 16, 576), bits(4, 576))
+
+
+def test_decode_captured_for_one_row_a_sequence():
+    """A launch captured after place(..., max_rows=1) gives the bits of eager
+    steps, which take the same form; eager chunks and evictions run between the
+    replays, and weights past a sequence's length stay 0."""
+    need_gpu()
+    r = np.random.default_rng(13)
+    bits = lambda *s: dev(wk.to_bf16_bits(r.standard_normal(s).astype(np.float32))).view(torch.bfloat16)  # noqa: E731
+    B, H = 12, 32
+    a, b = (PagedLayer(B, H, n_pages=12 * 20, max_len=2000, max_rows=500, page_size=16, budget=256, n_recent=8, slack=20)
+            for _ in range(2))
+    q0, x0 = bits(600, H, 576), bits(600, 576)
+    chunk = [250, 13, 0, 41] + [37] * 8
+    n = sum(chunk)
+    for layer in (a, b):
+        layer.step(q0[:n], x0[:n], chunk)
+    q, x = bits(B, H, 576), bits(B, 576)
+    for layer in (a, b):                        # warm-up
+        layer.step(q, x, [1] * B)
+    a.place([1] * B, max_rows=1)
+    b.place([1] * B)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = a.launch(q, x)
+    g.replay()
+    b.launch(q, x)
+    trims = 0
+    for i in range(52):
+        if i in (9, 30):
+            q1, x1 = bits(30, H, 576), bits(30, 576)
+            for layer in (a, b):
+                layer.step(q1, x1, [30] + [0] * (B - 1))
+        q.copy_(bits(B, H, 576))
+        x.copy_(bits(B, 576))
+        a.place([1] * B, max_rows=1)
+        g.replay()
+        trims += int(a.trim())
+        o2, l2 = b.step(q, x, [1] * B)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.equal(a.acc, b.acc), i
+        assert torch.equal(a.seq_len, b.seq_len) and torch.equal(a.table, b.table)
+        for s, m in enumerate(b.lens):
+            assert not torch.any(b.acc[s, int(m):]), (i, s)
+        y = torch.arange(4096, device='cuda', dtype=torch.float32)
+        assert float((y * 2).sum().item()) == 4096 * 4095
+    assert trims >= 2 and torch.equal(a.pool, b.pool)
+    with pytest.raises(ValueError):
+        a.place([2] + [1] * (B - 1), max_rows=1)
+
+
+@pytest.mark.parametrize('B,H,window,sink', [(32, 16, 0, 0), (6, 128, 0, 0), (32, 32, 100, 4)])
+def test_decode_steps_of_a_layer_with_chunks_against_the_oracle(B, H, window, sink):
+    """Decoding in a layer that also takes chunks, whose bound of rows is not a
+    decoding step's: outputs, weights and evictions."""
+    need_gpu()
+    r = np.random.default_rng(B + H)
+    layer = PagedLayer(B, H, n_pages=B * 20, max_len=300, max_rows=200, page_size=16, window=window, n_sink=sink,
+                       budget=200, n_recent=window or 20, decay=0.9)
+    steps = [[int(n) for n in r.integers(0, 200, B)]] + [[1] * B] * 2 + [[0, 1] * (B // 2), [30] + [1] * (B - 1), [1] * B]
+    run(layer, steps, 17, window, sink)

@@ -194,3 +194,37 @@ def test_layer_refuses_a_step_before_anything_moves():
         assert torch.equal(layer.row0, row0) and torch.equal(layer.seq_len, n)
     with pytest.raises(ValueError, match='23 rows were placed'):
         layer.launch(z(22, 4, 576), z(22, 576))
+
+
+def test_layer_calls_take_the_steps_own_bounds():
+    """The kernels' forms follow from host bounds: a step gives its own largest
+    count and length, not the layer's; a captured launch what place was told."""
+    from indexer_top_kv_amd.pipeline import PagedLayer
+    B, H = 32, 16
+    layer = PagedLayer(B, H, n_pages=4096, max_len=131072, max_rows=1024, page_size=64, budget=131072, device='cpu')
+    sizes = (ech.ech_paged_attn_ws_bytes, ech.ech_paged_weight_ws_bytes)
+    tight = lambda R, L, T: max(f(B, T, H, R, L) for f in sizes)  # noqa: E731
+    layer.place([1000] + [7] * 31)
+    assert layer._bounds(False) == (1000, 1024) and layer._bounds(True) == (1024, 131072)
+    layer.place([1] * B)
+    assert layer._bounds(False) == (1, 1024) and layer._bounds(True) == (1024, 131072)
+    assert layer._ws_bytes(B, *layer._bounds(False)) == tight(1, 1024, B)
+    assert tight(1, 1024, B) != tight(32, 131072, B)
+    layer.place([24] + [0] * 31, max_rows=30)
+    assert layer._bounds(False) == (30, 2048) and layer._bounds(True) == (30, 131072)
+    layer.place([1] * B, max_rows=1)
+    assert layer._bounds(False) == (1, 2048) and layer._bounds(True) == (1, 131072)
+    assert layer._ws_bytes(B, *layer._bounds(True)) == tight(1, 131072, B)
+    lens = layer.lens.copy()
+    for counts, most in (([2] + [0] * 31, 1), ([1] * B, 1025), ([1] * B, 0), ([1] * B, -1)):
+        with pytest.raises(ValueError):
+            layer.place(counts, max_rows=most)
+    assert np.array_equal(layer.lens, lens) and layer._bounds(True) == (1, 131072)
+    layer.place([0] * B)
+    assert layer._bounds(False) == (0, 2048)
+    # 129 decoded tokens of 128 heads are split over the CUs by their own bound, not by the layer's
+    H = 128
+    layer = PagedLayer(129, H, n_pages=600, max_len=16384, max_rows=1024, page_size=64, device='cpu')
+    layer.place([200] * 129)
+    layer.place([1] * 129)
+    assert layer._ws_bytes(129, *layer._bounds(False)) > 0 == ech.ech_paged_attn_ws_bytes(129, 129, H, 129, 16384)
