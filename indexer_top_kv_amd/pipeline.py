@@ -41,7 +41,6 @@ order of the C-ABI calls and the stream events between them.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import List, Optional, Tuple
 
 import numpy as np
@@ -52,7 +51,7 @@ from . import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, LayerState, ech_cache_reset, e
                ech_index_logits_early_ws_bytes, ech_kv_append, ech_recall, ech_recall_early_live, ech_recall_rest,
                ech_topk, ech_topk_early, ech_topk_ws_bytes, ech_paged_append, ech_paged_attn,
                ech_paged_attn_ws_bytes, ech_paged_evict, ech_paged_evict_ws_bytes, ech_paged_weight,
-               ech_paged_weight_ws_bytes)
+               ech_paged_weight_ws_bytes, _raw_stream, _stream)
 
 
 def round_up(x: int, m: int) -> int:
@@ -709,37 +708,45 @@ class PagedLayer:
         self.evict_ws = (torch.empty(ech_paged_evict_ws_bytes(B, max_len, budget), dtype=torch.uint8, **dev)
                          if budget is not None else None)
         self._bufs, self._ws = {}, {}       # of decoding steps: by T; by size
-        self._placed, self._most, self._fixed = 0, 0, None
-        self._last, self._done, self._streams = None, torch.cuda.Event(), set()
-        with self._call():                  # the zeros above come before the first call
-            pass
+        self._placed, self._most, self._fixed, self._long, self._sizes = 0, 0, None, 0, {}
+        self._last = self._stream = self._done = None
+        self._leave(self._enter()[1])       # the zeros above come before the first call
 
-    @contextlib.contextmanager
-    def _call(self, stream=None):
-        """The stream of a call, ordered behind the layer's last call and the
-        current stream. A capture orders nothing: it runs nothing."""
+    def _enter(self, stream=None):
+        """A call's begin: its stream is made to wait for the layer's last call
+        and for the current stream. Returns that stream (None: the current one)
+        and whether it records a graph; a capture orders nothing, it runs
+        nothing. Steps on one stream cost a comparison here: an event a call
+        would take 4 us of the device."""
         if self.device.type != 'cuda':      # host logic alone
-            yield None
-            return
-        s = _as_stream(stream, self.device)
+            return None, False
+        now = _raw_stream(self.device.index)
+        raw = now if stream is None else _stream(stream)
+        if raw == now == self._last:
+            return None, torch.cuda.is_current_stream_capturing()
+        s = torch.cuda.current_stream(self.device) if raw == now else _as_stream(stream, self.device)
         if _capturing(s):
-            yield s
-            return
-        now = torch.cuda.current_stream(self.device)
-        if s != now:
-            s.wait_stream(now)
-        if self._last is not None and self._last != s:
-            s.wait_event(self._done)
-        if s not in self._streams:          # the layer's memory is not another's before s is done with it
-            self._streams.add(s)
-            for t in (self.pool, self.table, self.row0, self.seq_len, self.status, self.acc, self.kept, self.evict_ws):
-                if t is not None:
-                    t.record_stream(s)
-        try:
-            yield s
-        finally:
-            self._done.record(s)
-            self._last = s
+            return (None if raw == now else s), True
+        if raw != now:
+            s.wait_stream(torch.cuda.current_stream(self.device))
+        if self._last is not None and self._last != raw:
+            if self._done is not None:
+                s.wait_event(self._done)
+            else:
+                s.wait_stream(self._stream)
+        self._last, self._stream, self._done = raw, s, None
+        # the layer's memory is not another's before s is done with it
+        for t in (self.pool, self.table, self.row0, self.seq_len, self.status, self.acc, self.kept, self.evict_ws,
+                  *self._ws.values(), *(t for pair in self._bufs.values() for t in pair)):
+            if t is not None:
+                t.record_stream(s)
+        return (None if raw == now else s), False
+
+    def _leave(self, capturing: bool) -> None:
+        """A call's end. A stream that is not torch's own may be destroyed
+        before the next call: it is marked now."""
+        if self._last and not capturing and self._stream.stream_id == self._last:
+            self._done = self._stream.record_event()
 
     def _bounds(self, capturing: bool) -> Tuple[int, int]:
         """Host bounds of the placed step's rows a sequence and lengths, by which
@@ -747,32 +754,41 @@ class PagedLayer:
         that they share buffers). A captured launch holds for other steps too."""
         if capturing:
             return self.max_rows if self._fixed is None else self._fixed, self.max_len
-        return self._most if self._fixed is None else self._fixed, self._len_bound()
+        return self._most if self._fixed is None else self._fixed, self._long
 
     def _len_bound(self) -> int:
-        return min(self.max_len, 1 << max(int(self.lens.max()) - 1, 0).bit_length())
+        """The longest length, up by less than 256 or an eighth."""
+        n = int(self.lens.max())
+        unit = max(256, (1 << n.bit_length()) // 16)
+        return min(self.max_len, round_up(n, unit))
 
     def _ws_bytes(self, T: int, R: int, L: int) -> int:
-        n = ech_paged_attn_ws_bytes(self.B, T, self.H, min(R, T), L, self.window, self.n_sink)
-        if self.budget is not None:         # the two calls run one after the other: one workspace
-            n = max(n, ech_paged_weight_ws_bytes(self.B, T, self.H, min(R, T), L))
+        n = self._sizes.get((T, R, L))
+        if n is None:
+            n = ech_paged_attn_ws_bytes(self.B, T, self.H, min(R, T), L, self.window, self.n_sink)
+            if self.budget is not None:     # the two calls run one after the other: one workspace
+                n = max(n, ech_paged_weight_ws_bytes(self.B, T, self.H, min(R, T), L))
+            if T <= self.B:
+                self._sizes[T, R, L] = n
         return n
 
     def _buffers(self, T: int, ws_bytes: int, s):
         dev, keep = dict(device=self.device), T <= self.B
-        got = self._bufs.get(T)
+        got, ws = (self._bufs.get(T), self._ws.get(ws_bytes)) if keep else (None, None)
+        new = []
         if got is None:
-            got = (torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
-                   torch.empty((T, self.H), dtype=torch.float32, **dev))
+            got = new = [torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
+                         torch.empty((T, self.H), dtype=torch.float32, **dev)]
             if keep:
                 self._bufs[T] = got
-        ws = self._ws.get(ws_bytes) if keep else None
         if ws is None:
             ws = torch.empty(ws_bytes, dtype=torch.uint8, **dev)
+            new = [*new, ws]
             if keep:
                 self._ws[ws_bytes] = ws
-        for t in (*got, ws):                # freed when dropped: not before this stream is done with them
-            t.record_stream(s)
+        if s is not None:                   # freed when dropped: not before that stream is done with them
+            for t in new:
+                t.record_stream(s)
         return (*got, ws)
 
     def _check_rows(self, q: torch.Tensor, rows: torch.Tensor) -> None:
@@ -782,8 +798,10 @@ class PagedLayer:
             if t.shape != shape or t.dtype not in types or t.device != self.device:
                 raise ValueError(f'{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {shape} {types[0]} on '
                                  f'{self.device}')
-            steps = [st for n, st in zip(t.shape, t.stride()) if n > 1]
-            if t.stride(-1) != 1 or any(st % 8 for st in steps[:-1]) or t.data_ptr() % 16:
+            if t.is_contiguous() and t.data_ptr() % 16 == 0:
+                continue
+            steps = [st for n, st in zip(t.shape[:-1], t.stride()) if n > 1]
+            if t.stride(-1) != 1 or any(st % 8 for st in steps) or t.data_ptr() % 16:
                 raise ValueError(f'{name}: strides {t.stride()} at {t.data_ptr():#x}, expected a dense last dimension and '
                                  f'multiples of 16 bytes')
         if T > 1 and rows.stride(0) < 576:
@@ -807,14 +825,15 @@ class PagedLayer:
             raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
         moved = self.pages.resize(lens)
         self.lens, self._placed = lens, int(counts.sum())
-        self._most, self._fixed = int(counts.max()), max_rows
+        self._most, self._fixed, self._long = int(counts.max()), max_rows, self._len_bound()
         off = np.zeros(self.B + 1, np.int32)
         np.cumsum(counts, out=off[1:])
-        with self._call():
-            if moved:
-                self.table.copy_(torch.from_numpy(self.pages.table))
-            self.row0.copy_(torch.from_numpy(off))
-            self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        _, capturing = self._enter()
+        if moved:
+            self.table.copy_(torch.from_numpy(self.pages.table))
+        self.row0.copy_(torch.from_numpy(off))
+        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        self._leave(capturing)
         return self._placed
 
     def launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
@@ -822,19 +841,22 @@ class PagedLayer:
         [T, 576] bf16 -> (out, lse). T is at least the number of rows placed;
         those behind are no sequence's, and their outputs mean nothing."""
         self._check_rows(q, rows)
+        return self._launch(q, rows, stream)
+
+    def _launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
         T, ps = q.shape[0], self.pages.page_size
         if T < self._placed:
             raise ValueError(f'{self._placed} rows were placed, q has {T}')
-        with self._call(stream) as s:
-            R, L = self._bounds(_capturing(s))
-            out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s)
-            ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
-            ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
-                           window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
-            if self.budget is not None:
-                ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale,
-                                 self.acc, self.acc, decay=self.decay, window=self.window, n_sink=self.n_sink, ws=ws,
-                                 stream=stream)
+        s, capturing = self._enter(stream)
+        R, L = self._bounds(capturing)
+        out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s)
+        ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
+        ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
+                       window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+        if self.budget is not None:
+            ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, self.acc,
+                             self.acc, decay=self.decay, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+        self._leave(capturing)
         return out, lse
 
     def trim(self, stream=None) -> bool:
@@ -842,15 +864,16 @@ class PagedLayer:
         that are longer than budget go with them); True if any was."""
         if self.budget is None or not np.any(self.lens > self.budget + self.slack):
             return False
-        with self._call(stream) as s:
-            # weights at and past every length are 0 as they are: none is behind the bound
-            ech_paged_evict(self.acc, self.seq_len, self._len_bound(), self.budget, self.n_sink, self.n_recent,
-                            self.kept, self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
-                            page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
-            self.lens = np.minimum(self.lens, self.budget)
-            if self.pages.resize(self.lens):
-                with torch.cuda.stream(s):
-                    self.table.copy_(torch.from_numpy(self.pages.table))
+        s, capturing = self._enter(stream)
+        # weights at and past every length are 0 as they are: none is behind the bound
+        ech_paged_evict(self.acc, self.seq_len, self._len_bound(), self.budget, self.n_sink, self.n_recent, self.kept,
+                        self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
+                        page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
+        self.lens = np.minimum(self.lens, self.budget)
+        if self.pages.resize(self.lens):
+            with torch.cuda.stream(s):
+                self.table.copy_(torch.from_numpy(self.pages.table))
+        self._leave(capturing)
         return True
 
     def step(self, q: torch.Tensor, rows: torch.Tensor, counts):
@@ -860,7 +883,7 @@ class PagedLayer:
             raise ValueError(f'counts name {T} rows, q has {q.shape[0]} and rows {rows.shape[0]}')
         self._check_rows(q, rows)
         self.place(counts)
-        got = self.launch(q, rows)
+        got = self._launch(q, rows)
         self.trim()
         return got
 
@@ -870,16 +893,19 @@ class PagedLayer:
         lens[b] = 0
         self.pages.resize(lens)
         self.lens = lens
-        with self._call():
-            self.table.copy_(torch.from_numpy(self.pages.table))
-            self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
-            if self.acc is not None:
-                self.acc[b].zero_()
+        _, capturing = self._enter()
+        self.table.copy_(torch.from_numpy(self.pages.table))
+        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        if self.acc is not None:
+            self.acc[b].zero_()
+        self._leave(capturing)
 
 
 def _as_stream(stream, device):
     if stream is None:
         return torch.cuda.current_stream(device)
+    if isinstance(stream, int) and stream == 0:     # torch takes a 0 for no handle
+        return torch.cuda.default_stream(device)
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
 
 

@@ -68,3 +68,30 @@ def test_a_launch_elsewhere_takes_no_memory_still_in_use():
     out, _ = layer.launch(q, x, stream=side)
     torch.cuda.synchronize()
     assert torch.all(seen == 5.0) and not torch.any(torch.isnan(out))
+
+
+def test_streams_by_handle():
+    """Streams named by their handles, the default stream's 0 among them; one
+    that torch does not own is waited for by an event of its own."""
+    need_gpu()
+    r = np.random.default_rng(23)
+    a, b = (PagedLayer(2, 16, n_pages=60, max_len=400, max_rows=80, page_size=16, budget=64, n_recent=8)
+            for _ in range(2))
+    side = torch.cuda.Stream()
+    foreign = torch.cuda.ExternalStream(side.cuda_stream)
+    for i, counts in enumerate([[70, 3], [1, 62], [1, 1], [3, 3], [1, 1], [20, 1], [1, 1]]):
+        T = sum(counts)
+        q, x = bits(r, T, 16, 576), bits(r, T, 576)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(WAIT)
+        torch.cuda._sleep(WAIT)
+        a.place(counts)
+        out, lse = a.launch(q, x, stream=(0, side.cuda_stream, foreign)[i % 3])
+        a.trim(stream=(side.cuda_stream, 0)[i % 2])
+        want = b.step(q, x, counts)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]), i
+        for name in ('acc', 'seq_len', 'table', 'pool'):
+            assert torch.equal(getattr(a, name), getattr(b, name)), (i, name)
+    assert (a._done is None) == (a._last in (0, None))

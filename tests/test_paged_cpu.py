@@ -211,17 +211,21 @@ def test_layer_calls_take_the_steps_own_bounds():
     assert layer._ws_bytes(B, *layer._bounds(False)) == tight(1, 1024, B)
     assert tight(1, 1024, B) != tight(32, 131072, B)
     layer.place([24] + [0] * 31, max_rows=30)
-    assert layer._bounds(False) == (30, 2048) and layer._bounds(True) == (30, 131072)
+    assert layer._bounds(False) == (30, 1280) and layer._bounds(True) == (30, 131072)
     layer.place([1] * B, max_rows=1)
-    assert layer._bounds(False) == (1, 2048) and layer._bounds(True) == (1, 131072)
+    assert layer._bounds(False) == (1, 1280) and layer._bounds(True) == (1, 131072)
     assert layer._ws_bytes(B, *layer._bounds(True)) == tight(1, 131072, B)
     lens = layer.lens.copy()
+    for n in (0, 1, 256, 257, 5000, 10071, 65535, 65536, 131072):
+        layer.lens = np.array([n // 2] * 31 + [n])
+        assert n <= layer._len_bound() <= n + max(255, n // 8)
+    layer.lens = lens.copy()
     for counts, most in (([2] + [0] * 31, 1), ([1] * B, 1025), ([1] * B, 0), ([1] * B, -1)):
         with pytest.raises(ValueError):
             layer.place(counts, max_rows=most)
     assert np.array_equal(layer.lens, lens) and layer._bounds(True) == (1, 131072)
     layer.place([0] * B)
-    assert layer._bounds(False) == (0, 2048)
+    assert layer._bounds(False) == (0, 1280)
     # 129 decoded tokens of 128 heads are split over the CUs by their own bound, not by the layer's
     H = 128
     layer = PagedLayer(129, H, n_pages=600, max_len=16384, max_rows=1024, page_size=64, device='cpu')
