@@ -41,6 +41,7 @@ order of the C-ABI calls and the stream events between them.
 """
 from __future__ import annotations
 
+import warnings
 from typing import List, Optional, Tuple
 
 import numpy as np
@@ -668,6 +669,13 @@ class PagedLayer:
     sequences longer than budget + slack are cut down to budget tokens: the
     first n_sink, the last n_recent, and the heaviest between.
 
+    Window, n_sink and causality count the tokens that the cache holds: an
+    eviction closes the gaps between those it keeps. With n_recent >= window - 1
+    that is the model's own window, since what an eviction drops is out of every
+    later row's sight. With fewer, tokens from behind the window come into sight
+    again and some inside it are dropped: a window over kept tokens, which is
+    another model than the one without evictions, so the layer warns of it.
+
     The host knows every length (an eviction leaves budget tokens), so nothing
     waits for the device. place(counts) does the host's part (its copies are on
     the current stream, before the kernels of launch), launch(q, rows) the
@@ -691,6 +699,9 @@ class PagedLayer:
                  budget: Optional[int] = None, n_recent: int = 0, slack: int = 0, decay: float = 1.0, device='cuda'):
         if budget is not None and (budget < 1 or n_sink + n_recent > budget or slack < 0):
             raise ValueError('budget must hold n_sink + n_recent tokens, slack must not be negative')
+        if budget is not None and n_recent < window - 1:
+            warnings.warn(f'n_recent {n_recent} is less than window - 1 = {window - 1}: after an eviction the window '
+                          f'reaches over kept tokens that it had left behind', stacklevel=2)
         self.B, self.H, self.max_len, self.max_rows = B, H, max_len, max_rows
         self.sm_scale, self.window, self.n_sink = sm_scale, window, n_sink
         self.budget, self.n_recent, self.slack, self.decay = budget, n_recent, slack, decay

@@ -262,3 +262,29 @@ def test_decode_steps_of_a_layer_with_chunks_against_the_oracle(B, H, window, si
                        budget=200, n_recent=window or 20, decay=0.9)
     steps = [[int(n) for n in r.integers(0, 200, B)]] + [[1] * B] * 2 + [[0, 1] * (B // 2), [30] + [1] * (B - 1), [1] * B]
     run(layer, steps, 17, window, sink)
+
+
+@pytest.mark.parametrize('window,sink,budget,slack', [(40, 3, 60, 0), (20, 0, 20, 7), (1, 2, 30, 0)])
+def test_window_of_the_model_survives_evictions(window, sink, budget, slack):
+    """With n_recent = window - 1 every row attends as if nothing had been
+    evicted: the oracle keeps all rows at their own positions."""
+    need_gpu()
+    r = np.random.default_rng(window)
+    B, H = 3, 16
+    layer = PagedLayer(B, H, n_pages=B * 13, max_len=200, max_rows=100, page_size=16, window=window, n_sink=sink,
+                       budget=budget, n_recent=window - 1, slack=slack)
+    m, trimmed = Model(B), 0
+    for i, counts in enumerate(STEPS):
+        T = sum(counts)
+        q = wk.to_bf16_bits(r.standard_normal((T, H, 576)).astype(np.float32))
+        x = wk.to_bf16_bits(r.standard_normal((T, 576)).astype(np.float32))
+        row0 = np.concatenate([[0], np.cumsum(counts)])
+        before = layer.lens.sum() + T
+        out, lse = layer.step(dev(q).view(torch.bfloat16), dev(x).view(torch.bfloat16), counts)
+        trimmed += int(layer.lens.sum() < before)
+        for b in range(B):
+            m.rows[b] = np.concatenate([m.rows[b], x[row0[b]:row0[b + 1]]])
+        pool, table, page, lens = m.dense()
+        ref = oracle.paged.attention(q, pool, table, page, row0, lens, SCALE, window, sink)
+        check_attn((out.float().cpu().numpy(), host(lse)), ref, int(lens.max()), f'step {i}')
+    assert trimmed >= 2 and lens.max() > budget + 40

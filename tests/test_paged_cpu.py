@@ -3,6 +3,7 @@ binding, and the oracle against closed forms."""
 import os
 import subprocess
 import sys
+import warnings
 
 import numpy as np
 import pytest
@@ -232,3 +233,16 @@ def test_layer_calls_take_the_steps_own_bounds():
     layer.place([200] * 129)
     layer.place([1] * 129)
     assert layer._ws_bytes(129, *layer._bounds(False)) > 0 == ech.ech_paged_attn_ws_bytes(129, 129, H, 129, 16384)
+
+
+def test_layer_warns_of_a_window_over_kept_tokens():
+    from indexer_top_kv_amd.pipeline import PagedLayer
+    mk = lambda **kw: PagedLayer(1, 4, n_pages=8, max_len=64, max_rows=8, page_size=16, device='cpu', **kw)  # noqa: E731
+    with pytest.warns(UserWarning, match='window'):
+        mk(window=20, n_sink=2, budget=40, n_recent=18)
+    with warnings.catch_warnings():
+        warnings.simplefilter('error')
+        mk(window=20, n_sink=2, budget=40, n_recent=19)
+        mk(window=20, n_sink=2)
+        mk(budget=40)
+        mk(window=1, budget=40)
