@@ -658,6 +658,9 @@ class PageTables:
         return len(changed) > 0
 
 
+kUploads = 8     # uploads of a PagedLayer under way together: a step has one, with an eviction two
+
+
 class PagedLayer:
     """One resident layer: its pool of pages, page tables and buffers.
 
@@ -676,8 +679,9 @@ class PagedLayer:
     again and some inside it are dropped: a window over kept tokens, which is
     another model than the one without evictions, so the layer warns of it.
 
-    The host knows every length (an eviction leaves budget tokens), so nothing
-    waits for the device. place(counts) does the host's part (its copies are on
+    The host knows every length (an eviction leaves budget tokens) and uploads
+    from pinned memory, so it queues steps without waiting for the device, up to
+    kUploads uploads ahead of it. place(counts) does the host's part (its copies are on
     the current stream, before the kernels of launch), launch(q, rows) the
     step's kernels, trim() the eviction; a launch of the same T may be captured
     and replayed, the tables and lengths being read in place (the kernels' forms
@@ -709,10 +713,15 @@ class PagedLayer:
         dev = dict(device=device)
         self.pool = torch.zeros((n_pages * page_size, 576), dtype=torch.bfloat16, **dev)
         self.device = self.pool.device      # with its index: the current device may change
-        self.table = torch.from_numpy(self.pages.table).to(**dev)
         self.lens = np.zeros(B, np.int64)
-        self.row0 = torch.zeros(B + 1, dtype=torch.int32, **dev)
-        self.seq_len = torch.zeros(B, dtype=torch.int32, **dev)
+        # [row0 | seq_len | table]: the host's copy, the device's, and what is on its way between them
+        n, per = 2 * B + 1, self.pages.per_seq
+        self._image = np.zeros(n + B * per, np.int32)
+        self._image[n:] = -1
+        self.pages.table = self._image[n:].reshape(B, per)
+        self._meta = torch.tensor(self._image, **dev)
+        self.row0, self.seq_len, self.table = self._meta[:B + 1], self._meta[B + 1:n], self._meta[n:].view(B, per)
+        self._ring, self._turn = [], 0
         self.status = torch.zeros(1, dtype=torch.int32, **dev)
         self.acc = torch.zeros((B, max_len), dtype=torch.float32, **dev) if budget is not None else None
         self.kept = torch.empty((B, budget), dtype=torch.int32, **dev) if budget is not None else None
@@ -747,7 +756,7 @@ class PagedLayer:
                 s.wait_stream(self._stream)
         self._last, self._stream, self._done = raw, s, None
         # the layer's memory is not another's before s is done with it
-        for t in (self.pool, self.table, self.row0, self.seq_len, self.status, self.acc, self.kept, self.evict_ws,
+        for t in (self.pool, self._meta, self.status, self.acc, self.kept, self.evict_ws,
                   *self._ws.values(), *(t for pair in self._bufs.values() for t in pair)):
             if t is not None:
                 t.record_stream(s)
@@ -758,6 +767,34 @@ class PagedLayer:
         before the next call: it is marked now."""
         if self._last and not capturing and self._stream.stream_id == self._last:
             self._done = self._stream.record_event()
+
+    def _upload(self, first: int, last: int) -> None:
+        """Numbers first .. last - 1 of [row0 | seq_len | table] go to the device,
+        on the current stream. They leave from pinned memory, kUploads blocks in
+        turn, so that the host waits only if the device is that many behind."""
+        if self.device.type != 'cuda':
+            self._meta[first:last].copy_(torch.from_numpy(self._image[first:last]))
+            return
+        if len(self._ring) < kUploads:
+            pinned = torch.empty(len(self._image), dtype=torch.int32, pin_memory=True)
+            self._ring.append((pinned, pinned.numpy(), torch.cuda.Event()))
+            self._turn = len(self._ring) - 1
+        pinned, block, done = self._ring[self._turn]
+        self._turn = (self._turn + 1) % kUploads
+        done.synchronize()                  # the copy that this block was last used for
+        block[first:last] = self._image[first:last]
+        self._meta[first:last].copy_(pinned[first:last], non_blocking=True)
+        done.record(torch.cuda.current_stream(self.device))
+
+    def _place_lens(self) -> None:
+        self._image[self.B + 1:2 * self.B + 1] = self.lens
+
+    def _not_captured(self, stream=None) -> None:
+        """The host's part of a step is not a graph's: a replay would upload
+        what the blocks hold by then."""
+        if self.device.type == 'cuda' and (torch.cuda.is_current_stream_capturing() if stream is None else
+                                           _capturing(_as_stream(stream, self.device))):
+            raise RuntimeError('place, trim and release cannot be captured')
 
     def _bounds(self, capturing: bool) -> Tuple[int, int]:
         """Host bounds of the placed step's rows a sequence and lengths, by which
@@ -825,6 +862,7 @@ class PagedLayer:
         for, where that is to be more than the largest count. A launch captured
         after it is valid for steps that are placed with the same max_rows (1:
         decoding); one captured after a place without it for any step."""
+        self._not_captured()
         counts = np.asarray(counts, np.int64)
         most = self.max_rows if max_rows is None else max_rows
         if most > self.max_rows:
@@ -837,13 +875,10 @@ class PagedLayer:
         moved = self.pages.resize(lens)
         self.lens, self._placed = lens, int(counts.sum())
         self._most, self._fixed, self._long = int(counts.max()), max_rows, self._len_bound()
-        off = np.zeros(self.B + 1, np.int32)
-        np.cumsum(counts, out=off[1:])
+        np.cumsum(counts, out=self._image[1:self.B + 1])
+        self._place_lens()
         _, capturing = self._enter()
-        if moved:
-            self.table.copy_(torch.from_numpy(self.pages.table))
-        self.row0.copy_(torch.from_numpy(off))
-        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        self._upload(0, len(self._image) if moved else 2 * self.B + 1)
         self._leave(capturing)
         return self._placed
 
@@ -875,15 +910,17 @@ class PagedLayer:
         that are longer than budget go with them); True if any was."""
         if self.budget is None or not np.any(self.lens > self.budget + self.slack):
             return False
+        self._not_captured(stream)
         s, capturing = self._enter(stream)
         # weights at and past every length are 0 as they are: none is behind the bound
         ech_paged_evict(self.acc, self.seq_len, self._len_bound(), self.budget, self.n_sink, self.n_recent, self.kept,
                         self.seq_len, acc_out=self.acc, pool=self.pool, src_table=self.table, dst_table=self.table,
                         page_size=self.pages.page_size, ws=self.evict_ws, stream=stream)
         self.lens = np.minimum(self.lens, self.budget)
+        self._place_lens()                  # as the eviction leaves them on the device
         if self.pages.resize(self.lens):
             with torch.cuda.stream(s):
-                self.table.copy_(torch.from_numpy(self.pages.table))
+                self._upload(2 * self.B + 1, len(self._image))
         self._leave(capturing)
         return True
 
@@ -900,13 +937,14 @@ class PagedLayer:
 
     def release(self, b: int) -> None:
         """Sequence b ends: its pages are free and its place starts empty."""
+        self._not_captured()
         lens = self.lens.copy()
         lens[b] = 0
         self.pages.resize(lens)
         self.lens = lens
+        self._place_lens()
         _, capturing = self._enter()
-        self.table.copy_(torch.from_numpy(self.pages.table))
-        self.seq_len.copy_(torch.from_numpy(lens.astype(np.int32)))
+        self._upload(self.B + 1, len(self._image))
         if self.acc is not None:
             self.acc[b].zero_()
         self._leave(capturing)

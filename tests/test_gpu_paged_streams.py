@@ -95,3 +95,59 @@ def test_streams_by_handle():
         for name in ('acc', 'seq_len', 'table', 'pool'):
             assert torch.equal(getattr(a, name), getattr(b, name)), (i, name)
     assert (a._done is None) == (a._last in (0, None))
+
+
+def test_the_host_does_not_wait_for_the_device():
+    """Steps with new pages and evictions are queued behind a busy device; its
+    lengths, tables and results are those of steps that are waited for, after
+    more uploads than can be under way as well."""
+    need_gpu()
+    r = np.random.default_rng(24)
+    a, b = (PagedLayer(2, 16, n_pages=60, max_len=400, max_rows=80, page_size=16, budget=64, n_recent=8)
+            for _ in range(2))
+    steps = [[70, 3], [1, 62], [1, 20], [3, 30]]
+    rows = [(bits(r, sum(c), 16, 576), bits(r, sum(c), 576)) for c in steps]
+    for q, x in rows:                       # the blocks and buffers exist
+        a.step(q, x, [len(x) - 1, 1])
+        b.step(q, x, [len(x) - 1, 1])
+    torch.cuda.synchronize()
+    busy = torch.cuda.Event()
+    torch.cuda._sleep(60 * WAIT)
+    busy.record()
+    got = []
+    for counts, (q, x) in zip(steps[:3], rows):
+        got.append(a.step(q, x, counts))
+        assert a.lens.max() <= 64
+    assert not busy.query()                 # three steps, three evictions: all queued, none begun
+    for i in range(30):
+        counts, (q, x) = steps[i % 4], rows[i % 4]
+        got.append(a.step(q, x, counts))
+    torch.cuda.synchronize()
+    order = list(zip(steps[:3], rows)) + [(steps[i % 4], rows[i % 4]) for i in range(30)]
+    for i, (counts, (q, x)) in enumerate(order):
+        out, lse = b.step(q, x, counts)
+        torch.cuda.synchronize()
+        assert torch.equal(out, got[i][0]) and torch.equal(lse, got[i][1]), i
+    for name in ('acc', 'seq_len', 'table', 'pool', 'row0'):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    assert a.seq_len.tolist() == a.lens.tolist() and np.array_equal(a.table.cpu().numpy(), a.pages.table)
+
+
+def test_the_hosts_part_is_not_captured():
+    need_gpu()
+    r = np.random.default_rng(25)
+    layer = PagedLayer(2, 16, n_pages=60, max_len=400, max_rows=80, page_size=16, budget=64)
+    layer.place([80, 0])
+    layer.launch(bits(r, 80, 16, 576), bits(r, 80, 576))
+    q, x = bits(r, 1, 16, 576), bits(r, 1, 576)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in (lambda: layer.place([1, 0]), layer.trim, lambda: layer.release(0), lambda: layer.step(q, x, [0, 1])):
+            with pytest.raises(RuntimeError, match='captured'):
+                call()
+        y = q * 2
+    assert layer.lens.tolist() == [80, 0] and layer.seq_len.tolist() == [80, 0]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, q * 2) and layer.trim() and layer.lens.tolist() == [64, 0]
