@@ -541,3 +541,46 @@ def test_refusals_on_the_gpu():
         c.attn(table=dev(c.table).expand(2, -1))
     with pytest.raises(ech.EchError):
         c.attn(scale=float('nan'))
+
+
+def test_a_workspace_too_small_is_refused_on_the_gpu():
+    """Every call that needs a workspace at these sizes refuses one that is a
+    byte short, missing or not aligned, and leaves its outputs as they were."""
+    need_gpu()
+    c = Case([1], [1000], 16, 16, seed=41)
+    need = ech.ech_paged_attn_ws_bytes(1, 1, 16, 1, c.max_len)
+    assert need > 8
+    out = torch.full((1, 16, 512), 7.0, dtype=torch.bfloat16, device='cuda')
+    lse = torch.full((1, 16), 7.0, dtype=torch.float32, device='cuda')
+    room = torch.empty(need + 256, dtype=torch.uint8, device='cuda')
+    for ws in (room[:8], room[:need - 1], room[16:16 + need]):
+        with pytest.raises(ech.EchError):
+            c.attn(out=out, lse=lse, ws=ws)
+    args = (dev(c.pool).view(torch.int16), dev(c.table), c.page, dev(c.row0), dev(c.seq_len), 1, c.max_len, SCALE)
+    with pytest.raises(ech.EchError):
+        ech.ech_paged_attn(dev(c.q), *args, out, lse)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0) and torch.all(lse == 7.0)
+    c.attn(out=out, lse=lse, ws=room[:need])
+    assert not torch.any(out == 7.0)
+    # received weight of a chunk, in parts; eviction of a long row
+    T, ml = 512, 200
+    q = torch.zeros((T, 16, 576), dtype=torch.bfloat16, device='cuda')
+    need = ech.ech_paged_weight_ws_bytes(1, T, 16, T, ml)
+    assert need > 8
+    acc = torch.full((1, ml), 7.0, device='cuda')
+    for ws in (None, room[:8], torch.empty(need - 1, dtype=torch.uint8, device='cuda')):
+        with pytest.raises(ech.EchError):
+            ech.ech_paged_weight(q, torch.zeros((T, 16), device='cuda'), dev(c.pool), dev(c.table), c.page,
+                                 torch.tensor([0, T], dtype=torch.int32, device='cuda'), dev(c.seq_len), T, ml, SCALE, None,
+                                 acc, ws=ws)
+    n, keep = 20000, 64
+    need = ech.ech_paged_evict_ws_bytes(1, n, keep)
+    assert need > 8
+    w = torch.zeros((1, n), device='cuda')
+    kept, n_out = (torch.full(s, 7, dtype=torch.int32, device='cuda') for s in ((1, keep), (1,)))
+    for ws in (None, room[:8], torch.empty(need - 1, dtype=torch.uint8, device='cuda')):
+        with pytest.raises(ech.EchError):
+            ech.ech_paged_evict(w, torch.tensor([n], dtype=torch.int32, device='cuda'), n, keep, 0, 0, kept, n_out, ws=ws)
+    torch.cuda.synchronize()
+    assert torch.all(acc == 7.0) and torch.all(kept == 7) and torch.all(n_out == 7)
