@@ -151,3 +151,30 @@ def test_the_hosts_part_is_not_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, q * 2) and layer.trim() and layer.lens.tolist() == [64, 0]
+
+
+def test_a_chunks_workspace_lives_until_its_stream_is_done():
+    """The layer drops a chunk's workspace when launch returns, while the side
+    stream has not begun: allocations of its size, filled at once, must not get
+    its memory. Against a second layer on the current stream."""
+    need_gpu()
+    r = np.random.default_rng(26)
+    a, b = (PagedLayer(2, 16, n_pages=100, max_len=700, max_rows=64, page_size=16, budget=600) for _ in range(2))
+    side = torch.cuda.Stream()
+    for counts in ([64, 30], [64, 3], [64, 64], [64, 0], [40, 2], [33, 1], [17, 64], [64, 64]):
+        T = sum(counts)
+        q, x = bits(r, T, 16, 576), bits(r, T, 576)
+        a.place(counts)
+        size = a._ws_bytes(T, *a._bounds(False))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(10 * WAIT)
+        out, lse = a.launch(q, x, stream=side)
+        junk = [torch.full((max(size, 1),), 0xff, dtype=torch.uint8, device='cuda') for _ in range(3)]   # NaN patterns
+        torch.cuda.current_stream().synchronize()
+        want = b.step(q, x, counts)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(a.acc, b.acc)
+        assert a.lens.max() < 128 or size > 0
+        del junk
+    assert torch.equal(a.pool, b.pool) and not a._ws
