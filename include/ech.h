@@ -497,9 +497,12 @@ int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, int page_si
  *   s_t = sm_scale * q[r,h,:] . pool[slot_t, :]        (visible t with a page)
  *   out[r,h,:] = sum_t softmax(s)_t * pool[slot_t, 0:512]
  *   lse[r,h] = log sum_t exp(s_t)
- * A row that sees nothing gets out = 0 and lse = -inf. Infinities and NaN in
- * rows that a query does not see do not reach its output. Scores, maxima and
- * sums are fp32; the softmax weights enter the value product as bf16.
+ * A row that sees nothing gets out = 0 and lse = -inf, and so does one whose
+ * scores are all -inf. Infinities and NaN in rows that a query does not see do
+ * not reach its output; in those that it sees they do as by the formula (a
+ * score of NaN or +inf: all of out is NaN; of -inf: the columns in which the row
+ * is not finite, by 0 x inf). Scores, maxima and sums are fp32; the softmax
+ * weights enter the value product as bf16.
  *  q     [T, H, 576] bf16; strides in values between rows and heads, multiples
  *        of 8; 16-byte aligned. H 1 .. 128, any.
  *  pool  [n_slots, 576] bf16, 16-byte aligned.

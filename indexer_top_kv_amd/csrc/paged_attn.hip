@@ -51,6 +51,35 @@ __device__ __forceinline__ bf16x8_t ld_tr8(const uint8_t* p0, const uint8_t* p1)
   return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// Where a score that does not count is not finite, its row holds infinities or
+// NaN, and 0 x inf is NaN: the step's values that are not finite become 0 before
+// the value product. What that product would have made of them for the queries
+// that do see them is put in by an indicator product: A = 1 where a value is not
+// finite, B = 1 where the query sees the token, and NaN where the sum is not 0
+// (a weight of its own is NaN already, or 0 beside a score of -inf).
+__device__ __forceinline__ bf16x8_t not_finite(bf16x8_t v) {
+  u32x4_t w = __builtin_bit_cast(u32x4_t, v);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = ((w[j] & 0x7f80u) == 0x7f80u ? 0x3f80u : 0u) | ((w[j] & 0x7f800000u) == 0x7f800000u ? 0x3f800000u : 0u);
+  return __builtin_bit_cast(bf16x8_t, w);
+}
+__device__ __forceinline__ bf16x8_t seen_ones(uint32_t lo4, uint32_t hi4) {   // elements 0..3, 4..7 by bits 0..3 of each
+  u32x4_t w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t two = (j < 2 ? lo4 : hi4) >> (2 * (j & 1));
+    w[j] = (two & 1 ? 0x3f80u : 0u) | (two & 2 ? 0x3f800000u : 0u);
+  }
+  return __builtin_bit_cast(bf16x8_t, w);
+}
+__device__ __forceinline__ void zero_not_finite(uint8_t* piece) {   // 16 bytes in LDS
+  uint16_t* e = reinterpret_cast<uint16_t*>(piece);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+}
+
 // This workgroup's place among tiles of their own: 8 neighbours, which read much
 // the same rows, to each of the 8 XCDs in turn (all of an XCD's in one piece
 // would leave a prompt's long tiles to one of them). Two chunks of 2048 rows,
@@ -148,7 +177,7 @@ __global__ void __launch_bounds__(256, 1)
   if (nsteps <= 0) {
     // nothing to see (a table without pages for it, a span past the end)
     for (int x = threadIdx.x; x < kMT; x += 256) {
-      if (nsp > 1) my_ml[x] = make_float2(-__builtin_inff(), 0.f);
+      if (nsp > 1) my_ml[x] = make_float2(-__builtin_inff(), -1.f);   // no output of this span's is written
       else if (lse && x < M - m0) lse[mg0 + x] = -__builtin_inff();
     }
     if (nsp == 1)
@@ -298,7 +327,7 @@ __global__ void __launch_bounds__(256, 1)
   // what the weights of a step change before its value product: accumulators of
   // grown maxima (none in the first step, they are 0), values that are not
   // finite; true if values changed
-  auto adjust = [&](int cur, bool first) -> bool {
+  auto adjust = [&](int cur, bool first, int t0, uint32_t ok) -> bool {
     int flags[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) flags[r] = __builtin_amdgcn_readfirstlane(s_flag[r]);
@@ -320,15 +349,28 @@ __global__ void __launch_bounds__(256, 1)
     }
     asm volatile("s_nop 7");
     if (!(any & 2)) return false;
-    // A weight of zero must add nothing, but 0 x inf is NaN: values that
-    // are not finite become 0 in this wave's columns of the step. A query
-    // that sees such a row has a score, so a weight, that is NaN already.
-    for (int x = lane; x < kStepTok * 16; x += 64) {
-      uint16_t* e = reinterpret_cast<uint16_t*>(tiles + cur * kTileB + (x >> 4) * kVPitch + wave * 256 + (x & 15) * 16);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+    for (int r = 0; r < 4; ++r) {
+      const int p = sr.pos0 + min(m0 + r * 32 + col, M - 1) / H;
+      const uint32_t seen = (sees_bits(p, t0, window, n_sink) & ok) >> (4 * g);
+      const bf16x8_t one0 = seen_ones(seen & 15u, (seen >> 8) & 15u), one1 = seen_ones((seen >> 16) & 15u, (seen >> 24) & 15u);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f32x16_t n;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) n[v] = 0.f;
+        n = mfma32(not_finite(vload(cur, 0, c)), one0, n);
+        n = mfma32(not_finite(vload(cur, 1, c)), one1, n);
+        asm volatile("" : "+a"(acc[c][r]));
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[c][r][v] = n[v] != 0.f ? __builtin_nanf("") : acc[c][r][v];
+        asm volatile("" : "+a"(acc[c][r]));
+      }
     }
+    asm volatile("s_nop 7");
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    for (int x = lane; x < kStepTok * 16; x += 64)   // in this wave's columns
+      zero_not_finite(tiles + cur * kTileB + (x >> 4) * kVPitch + wave * 256 + (x & 15) * 16);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     return true;
   };
@@ -396,7 +438,7 @@ __global__ void __launch_bounds__(256, 1)
       if (s + kKD < kKs16) kb[s % kKD] = kload(kbuf, s + kKD);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (adjust(cur, i == 0)) {
+    if (adjust(cur, i == 0, t0, ok0)) {
       vf[0] = vload(cur, 0, 0);
       vf[1] = vload(cur, 0, 1);
     }
@@ -533,7 +575,9 @@ __global__ void __launch_bounds__(256, 1)
   __shared__ __align__(16) uint8_t s_p[4 * 1024];   // P: per wave's tokens, a lane's 16 bytes
   __shared__ int s_page[4][2][64];   // per wave: page-table entries of two rounds' tokens
   __shared__ float s_x[4][kNM];      // per wave: a round's maximum of each query; at the end its sum
-  __shared__ int s_poison[2][4];     // by the round's parity: a wave may write the next round's while another reads
+  __shared__ int s_poison[2][4];     // per wave: its tokens with a slot, and whether (bit 16) a score that does not count
+                                     // is not finite; by the round's parity: a wave may write the next round's while
+                                     // another reads
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, c16 = lane & 15, grp = lane >> 4, col = lane & 31, g = lane >> 5;
@@ -679,7 +723,7 @@ __global__ void __launch_bounds__(256, 1)
         }
       }
       s_x[wave][col] = QT == 2 && hi ? tmax[QT - 1] : tmax[0];   // lanes l and l ^ 32 write the same
-      s_poison[i & 1][wave] = __any(poison);
+      s_poison[i & 1][wave] = (int)ok | (__any(poison) ? 0x10000 : 0);
       __syncthreads();
       // every wave has left round i - 1: its buffer takes round i + 1
       int next = -1;
@@ -732,16 +776,27 @@ __global__ void __launch_bounds__(256, 1)
       }
       __syncthreads();                            // P, and every wave's rows, are there
       const int* const bad = s_poison[i & 1];
-      if (bad[0] | bad[1] | bad[2] | bad[3]) {
-        // as in the 128-query kernel: values that are not finite become 0, each
-        // wave in its columns
-        uint8_t* wbuf = tiles + (i & 1) * kNTile + wave * 256;
-        for (int y = lane; y < kNRound * 16; y += 64) {
-          uint16_t* e = reinterpret_cast<uint16_t*>(wbuf + (y >> 4) * kVPitch + (y & 15) * 16);
+      if ((bad[0] | bad[1] | bad[2] | bad[3]) & 0x10000) {
+        // as in the 128-query kernel, each wave in its columns
+        const int p = sr.pos0 + min(col, M - 1) / H;
+#pragma unroll 1   // rare: nothing of it is kept in registers across rounds
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t seen = (sees_bits(p, t0 + (kk - wave) * kNTok, window, n_sink) & (uint32_t)bad[kk] & 0xffffu) >> (8 * g);
+          const bf16x8_t ones = seen_ones(seen & 15u, (seen >> 4) & 15u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
+          for (int c = 0; c < 4; ++c) {
+            f32x16_t n;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) n[v] = 0.f;
+            n = mfma32(not_finite(vload(buf, kk, c)), ones, n);
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[c][v] = n[v] != 0.f ? __builtin_nanf("") : acc[c][v];
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        uint8_t* wbuf = tiles + (i & 1) * kNTile + wave * 256;
+        for (int y = lane; y < kNRound * 16; y += 64) zero_not_finite(wbuf + (y >> 4) * kVPitch + (y & 15) * 16);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
       bf16x8_t pf[4], vf[4];
@@ -824,7 +879,7 @@ __global__ void __launch_bounds__(256)
     f32x4_t x[kG];
 #pragma unroll
     for (int u = 0; u < kG; ++u) {
-      a[u] = make_float2(-__builtin_inff(), 0.f);
+      a[u] = make_float2(-__builtin_inff(), -1.f);
       x[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if (s0 + u < n) {                                     // uniform: no load is repeated, none waits
         a[u] = ml[(int64_t)(s0 + u) * kMT];
@@ -840,7 +895,7 @@ __global__ void __launch_bounds__(256)
     o *= f;
 #pragma unroll
     for (int u = 0; u < kG; ++u) {
-      if (a[u].y != 0.f) {                    // a span that saw nothing wrote no output
+      if (!(a[u].y < 0.f)) {                  // below 0: a span without steps, which wrote no output
         const float w = exp2f((a[u].x == -__builtin_inff() ? ref : a[u].x) - ref);
         den += w * a[u].y;
         o += w * x[u];

@@ -18,6 +18,7 @@ import pytest
 import torch
 
 import oracle
+from oracle.numerics import bf16_to_f64
 import workloads as wk
 from gpu_util import dev, host, need_gpu
 import indexer_top_kv_amd as ech
@@ -584,3 +585,77 @@ def test_a_workspace_too_small_is_refused_on_the_gpu():
             ech.ech_paged_evict(w, torch.tensor([n], dtype=torch.int32, device='cuda'), n, keep, 0, 0, kept, n_out, ws=ws)
     torch.cuda.synchronize()
     assert torch.all(acc == 7.0) and torch.all(kept == 7) and torch.all(n_out == 7)
+
+
+def inf_case(rows, ctx, H, page, window, sink, seed, one):
+    """Infinities in rows that some queries see and others do not, in few value
+    columns or behind them, and in slots that none sees (slot 0 among them): a
+    score of +inf or NaN makes all of a query's output NaN, one of -inf a weight
+    of 0, whose product with an infinite value is NaN in that column alone."""
+    c = Case(rows, ctx, H, page, window, sink, seed=seed)
+    used = np.zeros(c.n_slots, bool)
+    for b in range(c.B):
+        sl = oracle.paged.slots(c.table[b], page, c.n_slots, int(c.seq_len[b]))
+        used[sl] = True
+        n, own = int(c.seq_len[b]), c.rows[b]
+        # cached tokens, and some of the sequence's own rows
+        at = np.unique(np.concatenate([c.r.integers(0, n, 2), n - 1 - c.r.integers(0, max(own, 1), 2)]))
+        for t in at[-1:] if one else at:
+            cols = c.r.integers(0, 500, 1) if one else c.r.integers(0, 576, 2)
+            c.pool[sl[t], cols] = c.r.choice(np.array([0x7f80, 0xff80], np.uint16))
+    c.pool[~used] = 0x7fc0
+    return c
+
+
+@pytest.mark.parametrize('rows,ctx,H,page,window,sink', [
+    ([40], [300], 2, 16, 0, 0), ([70, 33], [45, 333], 4, 16, 0, 0), ([70, 33], [45, 333], 4, 16, 20, 3),
+    ([1, 1, 1], [77, 1000, 40], 16, 24, 0, 0), ([1, 1], [500, 2001], 32, 16, 0, 0), ([2, 1, 2], [90, 700, 63], 16, 16, 30, 2),
+    ([3], [50], 8, 16, 0, 0), ([1], [3000], 128, 16, 0, 0), ([300], [10], 128, 16, 0, 0)])
+def test_attention_infinities_in_sight(rows, ctx, H, page, window, sink):
+    need_gpu()
+    whole = columns = 0
+    for seed in range(8):
+        c = inf_case(rows, ctx, H, page, window, sink, seed, one=seed >= 4)
+        with np.errstate(invalid='ignore'):
+            o, l, _, _ = c.ref()
+        out, lse = c.attn()
+        assert np.array_equal(np.isnan(out), np.isnan(o)), seed
+        assert np.array_equal(np.isnan(lse), np.isnan(l)) and np.isfinite(l[~np.isnan(l)]).all(), seed
+        # the columns that are finite: the bound of check_attn with the largest finite value and products
+        clean = np.where((c.pool & 0x7f80) == 0x7f80, np.uint16(0), c.pool)
+        de = np.max(c.ref(pool=clean)[3]) * 576 * U
+        de += 8 * U * (1 + de / (576 * U))
+        vmax, fin = np.abs(bf16_to_f64(clean[:, :512])).max(), np.isfinite(o)
+        bound = (2.0 ** -8 * (1 + 2.0 ** -8) + 2 * de + 2 * c.max_len * U) * vmax + 2.0 ** -8 * np.abs(o[fin])
+        assert np.all(np.abs(out[fin] - o[fin]) <= bound), seed
+        fin = np.isfinite(l)
+        assert np.all(np.abs(lse[fin] - l[fin]) <= de + c.max_len * U + 2 * U * np.abs(l[fin])), seed
+        whole += int(np.isnan(o).all(axis=2).sum())
+        columns += int((np.isnan(o).any(axis=2) & ~np.isnan(o).all(axis=2)).sum())
+    assert whole and columns
+
+
+@pytest.mark.parametrize('H,rows', [(16, 1), (128, 1), (16, 5)])
+def test_attention_spans_whose_scores_are_all_minus_infinity(H, rows):
+    """Tokens 0 .. 1999 hold -inf in value column 5, where every query is
+    positive: whole spans of a split sequence weigh nothing, and column 5 is NaN
+    by their 0 x -inf. A sequence of nothing else: out 0 (NaN in that column),
+    lse -inf."""
+    need_gpu()
+    c = Case([rows, rows], [2500, 300], H, 16, seed=7)
+    c.q[..., 5] = 0x3f80
+    for b, n in ((0, 2000), (1, 300 + rows)):
+        c.pool[oracle.paged.slots(c.table[b], 16, c.n_slots, n), 5] = 0xff80
+    with np.errstate(invalid='ignore'):
+        o, l, a, mag = c.ref()
+    clean = np.where((c.pool & 0x7f80) == 0x7f80, np.uint16(0), c.pool)
+    out, lse = c.attn()
+    first, second = slice(0, rows), slice(rows, 2 * rows)
+    assert np.isnan(out[first, :, 5]).all() and np.isnan(o[first, :, 5]).all()
+    rest = np.arange(512) != 5
+    assert np.array_equal(np.isnan(out[first][..., rest]), np.isnan(o[first][..., rest])) and np.isfinite(l[first]).all()
+    mag = c.ref(pool=clean)[3]
+    for x in (o, a, out):                   # check_attn takes NaN in lse for rows of no sequence
+        x[first, :, 5] = 0.0
+    check_attn((out[first], lse[first]), (o[first], l[first], a[first], mag[first]), c.max_len)
+    assert np.isnan(out[second, :, 5]).all() and np.all(out[second][..., rest] == 0) and np.all(np.isneginf(lse[second]))
