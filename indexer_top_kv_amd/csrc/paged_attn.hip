@@ -215,21 +215,18 @@ __global__ void __launch_bounds__(256, 1)
   };
   // This wave's eight tokens of a step: 8 wave .. +7. A token without a slot
   // brings slot 0's row, which no query weighs.
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ECH_LDS_PTR(&tiles[0])));
+  const uint32_t lds0 = lds_addr(tiles);
   auto issue_row = [&](int slot, int buf, int j) {
-    const uint32_t voff = lane * 16;
     const int tok = wave * 8 + j;
     const int sl = max(__builtin_amdgcn_readlane(slot, tok), 0);
     const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2);
-    const uint32_t lds = lds0 + static_cast<uint32_t>(buf * kTileB + tok * kVPitch);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(src) : "memory", "m0");
+    lds_load_row(lds0 + static_cast<uint32_t>(buf * kTileB + tok * kVPitch), lane * 16, src);
   };
   auto issue_tails = [&](int slot, int buf) {
     const int k = lane >> 3, tok = wave * 8 + k;
     const int sl = max(__shfl(slot, tok, 64), 0);
     const uint8_t* src = pool + (uint64_t)(uint32_t)sl * (kPagedRow * 2) + kPagedVal * 2 + (((lane & 7) ^ k) * 16);
-    const uint32_t lds = lds0 + static_cast<uint32_t>(buf * kTileB + kTailAt + wave * 1024);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+    lds_load_lanes(lds0 + static_cast<uint32_t>(buf * kTileB + kTailAt + wave * 1024), src);
   };
   auto issue = [&](int slot, int buf) {
     issue_tails(slot, buf);

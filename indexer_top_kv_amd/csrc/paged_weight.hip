@@ -33,11 +33,6 @@ constexpr int kBufs = 3;
 constexpr int kLoads = 9;                    // row loads of a wave per step
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float sum_pair(float x) {   // over lanes l, l ^ 32
-  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
-}
-
 // Fragment s (16 values) of row `col` of a step buffer: piece 2 s + g.
 __device__ __forceinline__ bf16x8_t row_frag(const uint8_t* buf, int col, int g, int s) {
   return s < 32 ? ld_bf16x8(buf + col * kVPitch + g * 16 + s * 32)
@@ -229,7 +224,7 @@ __global__ void __launch_bounds__(256, 1)
       }
     }
     if (i > 0) {
-      const float w = sum_pair(sum[0] + sum[1]);
+      const float w = pair_sum(sum[0] + sum[1]);
       s_w[wave][((i - 1) % kChunk) * kStepTok + col] = w;   // both lanes of a token write the same
     }
     if (i < nsteps) {
@@ -433,7 +428,7 @@ __global__ void __launch_bounds__(256, 1)
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float x = sum_pair(w[h]);
+    const float x = pair_sum(w[h]);
     const float sum = nsteps > 0 && there[h] ? x : 0.f;   // a token without a page receives nothing
     if (g != 0 || t_of[h] > te) continue;
     if (parts > 1)
