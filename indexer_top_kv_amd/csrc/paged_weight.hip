@@ -15,13 +15,14 @@
 //    a whole sequence per workgroup 962 us).
 //  - More queries (chunks), which this form would have to pass the rows by more
 //    than once: 256 tokens' rows stay in registers (64 a wave, 288 registers)
-//    and the queries stream past; bound by the matrix cores: 4 chunks of 64 rows
-//    at 64 heads over 10K tokens 211-218 us, 880 TF/s. A step's products are 2304
-//    of its 4338 cycles, but fewer cycles do not help: with the row loads and the
-//    weights' instructions spread between the products it takes 3761, and the
-//    call as long, at a lower clock (1.8 GHz against the card's 2.4 while it
-//    runs over and over). What bounds it is the power the products, LDS reads
-//    and exponentials draw; without the exponentials it takes 172 us.
+//    and the queries stream past. 4 chunks of 64 rows at 64 heads over 10K tokens
+//    213-218 us, 880 TF/s: 480 workgroups in two rounds on 256 CUs, each with 22K
+//    cycles to start and 43 steps of 4300 (the products 2304), at 2.3 GHz while
+//    the call runs over and over (1.9 in the first 20 calls, 250 us each). Those
+//    of the last tokens look at the mask in every step and take 5350: two of them
+//    in a row on a CU end the kernel at 210 us, the others end at 181. With the
+//    row loads and the weights' instructions spread between the products a step
+//    takes 3774 cycles, but 5290 with the mask and at 2.16 GHz: 215 us.
 #include <algorithm>
 
 #include "common.hpp"
