@@ -727,7 +727,8 @@ class PagedLayer:
         self.kept = torch.empty((B, budget), dtype=torch.int32, **dev) if budget is not None else None
         self.evict_ws = (torch.empty(ech_paged_evict_ws_bytes(B, max_len, budget), dtype=torch.uint8, **dev)
                          if budget is not None else None)
-        self._bufs, self._ws = {}, {}       # of decoding steps: by T; by size
+        # of decoding steps: outputs by T, the largest workspace so far, those that graphs hold
+        self._bufs, self._ws, self._held = {}, None, []
         self._placed, self._most, self._fixed, self._long, self._sizes = 0, 0, None, 0, {}
         self._last = self._stream = self._done = None
         self._leave(self._enter()[1])       # the zeros above come before the first call
@@ -757,7 +758,7 @@ class PagedLayer:
         self._last, self._stream, self._done = raw, s, None
         # the layer's memory is not another's before s is done with it
         for t in (self.pool, self._meta, self.status, self.acc, self.kept, self.evict_ws,
-                  *self._ws.values(), *(t for pair in self._bufs.values() for t in pair)):
+                  self._ws, *(t for pair in self._bufs.values() for t in pair)):
             if t is not None:
                 t.record_stream(s)
         return (None if raw == now else s), False
@@ -820,20 +821,22 @@ class PagedLayer:
                 self._sizes[T, R, L] = n
         return n
 
-    def _buffers(self, T: int, ws_bytes: int, s):
+    def _buffers(self, T: int, ws_bytes: int, s, capturing: bool):
         dev, keep = dict(device=self.device), T <= self.B
-        got, ws = (self._bufs.get(T), self._ws.get(ws_bytes)) if keep else (None, None)
+        got, ws = (self._bufs.get(T), self._ws) if keep else (None, None)
         new = []
         if got is None:
             got = new = [torch.empty((T, self.H, 512), dtype=torch.bfloat16, **dev),
                          torch.empty((T, self.H), dtype=torch.float32, **dev)]
             if keep:
                 self._bufs[T] = got
-        if ws is None:
+        if ws is None or ws.numel() < ws_bytes:
             ws = torch.empty(ws_bytes, dtype=torch.uint8, **dev)
             new = [*new, ws]
             if keep:
-                self._ws[ws_bytes] = ws
+                self._ws = ws
+        if keep and capturing and not any(ws is w for w in self._held):
+            self._held.append(ws)
         if s is not None:                   # freed when dropped: not before that stream is done with them
             for t in new:
                 t.record_stream(s)
@@ -895,7 +898,7 @@ class PagedLayer:
             raise ValueError(f'{self._placed} rows were placed, q has {T}')
         s, capturing = self._enter(stream)
         R, L = self._bounds(capturing)
-        out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s)
+        out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s, capturing)
         ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
         ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
                        window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)

@@ -288,3 +288,41 @@ def test_window_of_the_model_survives_evictions(window, sink, budget, slack):
         ref = oracle.paged.attention(q, pool, table, page, row0, lens, SCALE, window, sink)
         check_attn((out.float().cpu().numpy(), host(lse)), ref, int(lens.max()), f'step {i}')
     assert trimmed >= 2 and lens.max() > budget + 40
+
+
+def test_decoding_keeps_one_workspace():
+    """Growing contexts and counts ask for workspaces of many sizes: the layer
+    keeps the largest, and those that a captured launch holds, whose replays
+    still give an eager step's bits."""
+    need_gpu()
+    r = np.random.default_rng(19)
+    bits = lambda *s: dev(wk.to_bf16_bits(r.standard_normal(s).astype(np.float32))).view(torch.bfloat16)  # noqa: E731
+    B, H = 6, 16
+    a, b = (PagedLayer(B, H, n_pages=6 * 200, max_len=3000, max_rows=400, page_size=16, budget=3000) for _ in range(2))
+    q, x = bits(B, H, 576), bits(B, 576)
+    for layer in (a, b):
+        layer.step(q, x, [1] * B)
+    a.place([1] * B, max_rows=1)
+    b.place([1] * B)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = a.launch(q, x)
+    g.replay()
+    b.launch(q, x)
+    first, sizes = a._ws, set()
+    for i in range(12):
+        n = 220
+        q1, x1 = bits(n, H, 576), bits(n, 576)
+        for layer in (a, b):
+            layer.step(q1, x1, [n, 0, 0, 0, 0, 0])          # a chunk: a workspace of its own
+            for counts in ([6, 0, 0, 0, 0, 0], [0, 2, 1, 0, 1, 2], [3, 1, 0, 0, 0, 0]):
+                T = sum(counts)
+                layer.step(q1[:T], x1[:T], counts)
+                sizes.add(layer._ws_bytes(T, *layer._bounds(False)))
+        a.place([1] * B, max_rows=1)
+        g.replay()
+        o2, l2 = b.step(q, x, [1] * B)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o2) and torch.equal(lse, l2) and torch.equal(a.acc, b.acc), i
+    assert len(sizes) > 2 and a._ws.numel() >= max(sizes)
+    assert a._held[0] is first and len(a._held) == 1 and not b._held
