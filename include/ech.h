@@ -469,8 +469,9 @@ int ech_kv_append(void* host_pool, int64_t P, int64_t row_bytes, void* kcache, i
  *             lengths beyond max_len or the table are cut there, and of a
  *             sequence with more than max_rows new rows only the first
  *             max_rows are computed.
- *  B 1 .. 65535; T*H < 2^30; n_slots < 2^31 (offsets are 64-bit). All four
- *  calls may be captured; replays follow row0, seq_len and the table in place.
+ *  B 1 .. 65535; T*H < 2^30; max_len <= 2^30; n_slots < 2^31 (offsets are
+ *  64-bit). All four calls may be captured; replays follow row0, seq_len and
+ *  the table in place.
  */
 
 /*
@@ -524,7 +525,8 @@ int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, c
  * with the masks, q, pool and lse of the step's ech_paged_attn call. Entries
  * t >= seq_len[b] are neither read nor written, so a new token's acc_in entry
  * must have been set (0) by the caller. A token without a page receives 0. The
- * additions of a token have one order: the same call gives the same bits.
+ * additions of a token have one order: the same call gives the same bits. A row
+ * whose scores are all -inf (lse -inf) gives NaN to the tokens that it sees.
  *  acc_in [B, acc_ld] fp32 or NULL (all 0); acc_out [B, acc_ld] fp32, may be
  *  acc_in. acc_ld >= max_len.
  *  ws ech_paged_weight_ws_bytes(...) bytes, as for ech_paged_attn.

@@ -658,7 +658,7 @@ class PageTables:
         return len(changed) > 0
 
 
-kUploads = 8     # uploads of a PagedLayer under way together: a step has one, with an eviction two
+UPLOADS = 8     # uploads of a PagedLayer under way together: a step has one, with an eviction two
 
 
 class PagedLayer:
@@ -681,15 +681,15 @@ class PagedLayer:
 
     The host knows every length (an eviction leaves budget tokens) and uploads
     from pinned memory, so it queues steps without waiting for the device, up to
-    kUploads uploads ahead of it. place(counts) does the host's part (its copies are on
-    the current stream, before the kernels of launch), launch(q, rows) the
-    step's kernels, trim() the eviction; a launch of the same T may be captured
-    and replayed, the tables and lengths being read in place (the kernels' forms
-    are chosen by the step's largest count and length; for a captured launch by
-    the max_rows that place was given, else by the layer's). Buffers and
-    workspace of a step of at most B rows (decoding) are the layer's, and the
-    next step of the same T writes them again; those of more rows are new each
-    time.
+    UPLOADS uploads ahead of it. place(counts) does the host's part (its copies
+    are on the current stream, before the kernels of launch), launch(q, rows)
+    the step's kernels, trim() the eviction; a launch of the same T may be
+    captured and replayed, the tables and lengths being read in place (the
+    kernels' forms are chosen by the step's largest count and length; for a
+    captured launch by the max_rows that place was given, else by the layer's).
+    Buffers and workspace of a step of at most B rows (decoding) are the
+    layer's, and the next step of the same T writes them again; those of more
+    rows are new each time.
 
     Steps of one layer run in the order of their calls, whatever streams these
     name: each call's stream waits for the layer's last one, and a stream other
@@ -744,6 +744,7 @@ class PagedLayer:
         now = _raw_stream(self.device.index)
         raw = now if stream is None else _stream(stream)
         if raw == now == self._last:
+            self._done = None               # if this call fails half-way, the next one waits for all of it
             return None, torch.cuda.is_current_stream_capturing()
         s = torch.cuda.current_stream(self.device) if raw == now else _as_stream(stream, self.device)
         if _capturing(s):
@@ -771,17 +772,17 @@ class PagedLayer:
 
     def _upload(self, first: int, last: int) -> None:
         """Numbers first .. last - 1 of [row0 | seq_len | table] go to the device,
-        on the current stream. They leave from pinned memory, kUploads blocks in
+        on the current stream. They leave from pinned memory, UPLOADS blocks in
         turn, so that the host waits only if the device is that many behind."""
         if self.device.type != 'cuda':
             self._meta[first:last].copy_(torch.from_numpy(self._image[first:last]))
             return
-        if len(self._ring) < kUploads:
+        if len(self._ring) < UPLOADS:
             pinned = torch.empty(len(self._image), dtype=torch.int32, pin_memory=True)
             self._ring.append((pinned, pinned.numpy(), torch.cuda.Event()))
             self._turn = len(self._ring) - 1
         pinned, block, done = self._ring[self._turn]
-        self._turn = (self._turn + 1) % kUploads
+        self._turn = (self._turn + 1) % UPLOADS
         done.synchronize()                  # the copy that this block was last used for
         block[first:last] = self._image[first:last]
         self._meta[first:last].copy_(pinned[first:last], non_blocking=True)
@@ -853,8 +854,8 @@ class PagedLayer:
                 continue
             steps = [st for n, st in zip(t.shape[:-1], t.stride()) if n > 1]
             if t.stride(-1) != 1 or any(st % 8 for st in steps) or t.data_ptr() % 16:
-                raise ValueError(f'{name}: strides {t.stride()} at {t.data_ptr():#x}, expected a dense last dimension and '
-                                 f'multiples of 16 bytes')
+                raise ValueError(f'{name}: strides {t.stride()} at {t.data_ptr():#x}, expected a dense last dimension '
+                                 f'and multiples of 16 bytes')
         if T > 1 and rows.stride(0) < 576:
             raise ValueError(f'rows: strides {rows.stride()}, the rows overlap')
 
@@ -867,7 +868,7 @@ class PagedLayer:
         decoding); one captured after a place without it for any step."""
         self._not_captured()
         counts = np.asarray(counts, np.int64)
-        most = self.max_rows if max_rows is None else max_rows
+        most = self.max_rows if max_rows is None else int(max_rows)
         if most > self.max_rows:
             raise ValueError(f'max_rows {max_rows}, the layer has {self.max_rows}')
         if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > most):
@@ -877,7 +878,7 @@ class PagedLayer:
             raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
         moved = self.pages.resize(lens)
         self.lens, self._placed = lens, int(counts.sum())
-        self._most, self._fixed, self._long = int(counts.max()), max_rows, self._len_bound()
+        self._most, self._fixed, self._long = int(counts.max()), None if max_rows is None else most, self._len_bound()
         np.cumsum(counts, out=self._image[1:self.B + 1])
         self._place_lens()
         _, capturing = self._enter()

@@ -213,9 +213,9 @@ def test_layer_calls_take_the_steps_own_bounds():
     assert tight(1, 1024, B) != tight(32, 131072, B)
     layer.place([24] + [0] * 31, max_rows=30)
     assert layer._bounds(False) == (30, 1280) and layer._bounds(True) == (30, 131072)
-    layer.place([1] * B, max_rows=1)
+    layer.place([1] * B, max_rows=np.int64(1))
     assert layer._bounds(False) == (1, 1280) and layer._bounds(True) == (1, 131072)
-    assert layer._ws_bytes(B, *layer._bounds(True)) == tight(1, 131072, B)
+    assert layer._ws_bytes(B, *layer._bounds(True)) == tight(1, 131072, B) and type(layer._fixed) is int
     lens = layer.lens.copy()
     for n in (0, 1, 256, 257, 5000, 10071, 65535, 65536, 131072):
         layer.lens = np.array([n // 2] * 31 + [n])
