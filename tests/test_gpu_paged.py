@@ -659,3 +659,26 @@ def test_attention_spans_whose_scores_are_all_minus_infinity(H, rows):
         x[first, :, 5] = 0.0
     check_attn((out[first], lse[first]), (o[first], l[first], a[first], mag[first]), c.max_len)
     assert np.isnan(out[second, :, 5]).all() and np.all(out[second][..., rest] == 0) and np.all(np.isneginf(lse[second]))
+
+
+@pytest.mark.parametrize('rows,ctx,H,page,window,sink', [
+    ([1, 1, 1], [77, 1000, 40], 16, 24, 0, 0), ([2, 1, 2], [90, 700, 63], 16, 16, 30, 2), ([70, 33], [45, 333], 4, 16, 0, 0),
+    ([70, 33], [45, 333], 4, 16, 20, 3), ([1], [3000], 128, 16, 0, 0)])
+def test_weight_infinities_in_sight(rows, ctx, H, page, window, sink):
+    """Sums are NaN where the formula's are: tokens that a row with an lse of NaN
+    sees, or one with scores of -inf alone; a single score of -inf adds nothing."""
+    need_gpu()
+    for seed in range(4, 8):
+        c = inf_case(rows, ctx, H, page, window, sink, seed, one=True)
+        if seed == 7:                       # a sequence whose scores are all -inf
+            c.q[:rows[0], :, 5] = 0x3f80
+            c.pool[oracle.paged.slots(c.table[0], page, c.n_slots, int(c.seq_len[0])), 5] = 0xff80
+        out, lse = c.attn()
+        if seed == 7:
+            assert np.isneginf(lse[:rows[0]]).any()
+        acc = np.ones((c.B, c.max_len), np.float32)
+        with np.errstate(invalid='ignore'):
+            ref = oracle.paged.received(c.q, lse, c.pool, c.table, page, c.row0, c.seq_len, SCALE, acc, 0.5, window, sink)
+        got = c.weight(lse, acc, 0.5)
+        for b, n in enumerate(c.seq_len):
+            assert np.array_equal(np.isnan(got[b, :n]), np.isnan(ref[b, :n])), (seed, b)
