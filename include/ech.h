@@ -518,6 +518,27 @@ int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, c
                    float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * ech_paged_tree_attn - ech_paged_attn for a step of drafted rows that form
+ * trees: row i of a sequence's n new rows follows its row parent[row0[b] + i]
+ * (-1: the cached tokens before the step, of which there are c = seq_len[b] - n).
+ * Its line is itself, its parent, that one's parent and so on; its position is
+ * c + (rows in its line - 1), its slot that of token c + i as everywhere
+ * (append the rows first). It sees the c cached tokens and its line, and with a
+ * window of those only what is at positions > its own - window or < n_sink. A
+ * chain (parent i - 1) gives ech_paged_attn. Several rows may follow the cached
+ * tokens.
+ *  parent [T] int32, device, -1 <= parent[row0[b] + i] < i; anything else counts
+ *         as -1. Rows of no sequence are not read.
+ *  max_rows at most 256 (ECH_EINVAL). Everything else as in ech_paged_attn.
+ */
+size_t ech_paged_tree_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink);
+int ech_paged_tree_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool, int64_t n_slots,
+                        int page_size, const int32_t* page_table, int64_t pt_ld, const int32_t* row0,
+                        const int32_t* seq_len, const int32_t* parent, int B, int T, int H, int max_rows, int max_len,
+                        int window, int n_sink, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/*
  * ech_paged_weight - the attention weight each cached token received from a
  * step's new rows, added to a decayed running sum. For t < seq_len[b]:
  *   acc_out[b,t] = decay * acc_in[b,t] + sum over the new rows r of b that see

@@ -24,7 +24,7 @@ from ._native import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, ECH_KEY_BF16, ECH_KEY_F
 __all__ = ['ech_kv_append', 'ech_sparse_attn', 'ech_sparse_attn_ws_bytes', 'ech_index_logits', 'ech_index_logits_causal', 'ech_topk', 'ech_topk_noalloc', 'ech_topk_ws_bytes', 'ech_cache_reset',
            'ech_cache_step', 'ech_cache_step_ws_bytes', 'ech_recall', 'ech_index_logits_early',
            'ech_index_logits_early_ws_bytes', 'ech_recall_early_live', 'ech_recall_rest', 'ech_topk_early', 'ech_paged_append',
-           'ech_paged_attn', 'ech_paged_attn_ws_bytes', 'ech_paged_weight', 'ech_paged_weight_ws_bytes',
+           'ech_paged_attn', 'ech_paged_attn_ws_bytes', 'ech_paged_tree_attn', 'ech_paged_tree_attn_ws_bytes', 'ech_paged_weight', 'ech_paged_weight_ws_bytes',
            'ech_paged_evict', 'ech_paged_evict_ws_bytes', 'EchError', 'LayerState', 'lib']
 
 
@@ -360,12 +360,8 @@ def ech_paged_attn_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int,
     return int(lib().ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink))
 
 
-def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows: int, max_len: int, sm_scale: float,
-                   out, lse=None, window: int = 0, n_sink: int = 0, ws=None, stream=None) -> None:
-    """Causal attention of a step's new rows over their sequences' pages, with
-    an optional sliding window and n_sink first tokens that stay visible: q
-    [T, H, 576] bf16 (or its bits; rows and heads may be strided), pool [slots,
-    576] bf16 -> out [T, H, 512] bf16, lse [T, H] fp32 (optional)."""
+def _attn(fn: str, q, pool, page_table, page_size, row0, seq_len, parent, max_rows, max_len, sm_scale, out, lse, window,
+          n_sink, ws, stream) -> None:
     _fits(page_size, max_rows, max_len, window, n_sink, q.shape[0], seq_len.numel())
     _arg('pool', pool, _BITS16, (pool.shape[0], 576), pool.get_device())
     dev, B = _batch_args(pool, page_table, row0, seq_len)
@@ -374,10 +370,39 @@ def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows:
     _arg('out', out, _BITS16, (T, H, 512), dev)
     if lse is not None:
         _arg('lse', lse, _F32, (T, H), dev)
+    tree = ()
+    if fn == 'ech_paged_tree_attn':
+        _arg('parent', parent, _I32, (T,), dev)
+        tree = (parent.data_ptr(),)
     wp, wb = _ws_arg(ws, dev)
-    _call('ech_paged_attn', dev, stream, q.data_ptr(), *_steps(q, T, H), pool.data_ptr(), pool.shape[0],
-          page_size, page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, T, H, max_rows,
+    _call(fn, dev, stream, q.data_ptr(), *_steps(q, T, H), pool.data_ptr(), pool.shape[0], page_size,
+          page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), *tree, B, T, H, max_rows,
           max_len, window, n_sink, sm_scale, out.data_ptr(), _ptr(lse), wp, wb)
+
+
+def ech_paged_attn(q, pool, page_table, page_size: int, row0, seq_len, max_rows: int, max_len: int, sm_scale: float,
+                   out, lse=None, window: int = 0, n_sink: int = 0, ws=None, stream=None) -> None:
+    """Causal attention of a step's new rows over their sequences' pages, with
+    an optional sliding window and n_sink first tokens that stay visible: q
+    [T, H, 576] bf16 (or its bits; rows and heads may be strided), pool [slots,
+    576] bf16 -> out [T, H, 512] bf16, lse [T, H] fp32 (optional)."""
+    _attn('ech_paged_attn', q, pool, page_table, page_size, row0, seq_len, None, max_rows, max_len, sm_scale, out, lse,
+          window, n_sink, ws, stream)
+
+
+def ech_paged_tree_attn_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int, window: int = 0,
+                                 n_sink: int = 0) -> int:
+    _fits(B, T, H, max_rows, max_len, window, n_sink)
+    return int(lib().ech_paged_tree_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink))
+
+
+def ech_paged_tree_attn(q, pool, page_table, page_size: int, row0, seq_len, parent, max_rows: int, max_len: int,
+                        sm_scale: float, out, lse=None, window: int = 0, n_sink: int = 0, ws=None, stream=None) -> None:
+    """ech_paged_attn for drafted rows that form trees: parent [T] i32 names the
+    row of its sequence that each row follows (-1: the cached tokens). A row
+    sees the cached tokens and its own line; its position is its depth."""
+    _attn('ech_paged_tree_attn', q, pool, page_table, page_size, row0, seq_len, parent, max_rows, max_len, sm_scale, out,
+          lse, window, n_sink, ws, stream)
 
 
 def ech_paged_weight_ws_bytes(B: int, T: int, H: int, max_rows: int, max_len: int) -> int:

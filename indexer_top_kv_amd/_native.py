@@ -77,6 +77,9 @@ SIGNATURES = {
     'ech_paged_attn_ws_bytes': (_sz, [ctypes.c_int] * 7),
     'ech_paged_attn': (ctypes.c_int, [_p, _i64, _i64, _p, _i64, ctypes.c_int, _p, _i64, _p, _p, *[ctypes.c_int] * 7,
                                       ctypes.c_float, _p, _p, _p, _sz, _p]),
+    'ech_paged_tree_attn_ws_bytes': (_sz, [ctypes.c_int] * 7),
+    'ech_paged_tree_attn': (ctypes.c_int, [_p, _i64, _i64, _p, _i64, ctypes.c_int, _p, _i64, _p, _p, _p,
+                                           *[ctypes.c_int] * 7, ctypes.c_float, _p, _p, _p, _sz, _p]),
     'ech_paged_weight_ws_bytes': (_sz, [ctypes.c_int] * 5),
     'ech_paged_weight': (ctypes.c_int, [_p, _i64, _i64, _p, _p, _i64, ctypes.c_int, _p, _i64, _p, _p,
                                         *[ctypes.c_int] * 7, ctypes.c_float, _p, _p, _i64, ctypes.c_float, _p, _sz,

@@ -80,6 +80,65 @@ __device__ __forceinline__ void zero_not_finite(uint8_t* piece) {   // 16 bytes 
     if ((e[j] & 0x7f80u) == 0x7f80u) e[j] = 0;
 }
 
+// ------------------------------------------------------------------ trees
+// With TREE a sequence's new rows are the nodes of a tree (ech_paged_tree_attn):
+// parent[i] < i, and row i, at the position c + (how many rows it descends from)
+// behind the c cached tokens, sees those and its own line. A tile's queries each
+// keep their line as bits in LDS, made once a workgroup by following parents
+// there; the steps that hold cached tokens alone do not read it, so a tree costs
+// what a chunk of as many rows does.
+constexpr int kTreeMost = 256;               // rows of a tree
+constexpr int kLineWords = kTreeMost / 32;
+constexpr int kLinePitch = kLineWords + 1;   // the position behind the bits; odd: banks
+
+__device__ __forceinline__ int parent_of(const int32_t* parent, int i) {   // one that does not precede its row: none
+  const int p = parent[i];
+  return p < i ? max(p, -1) : -1;
+}
+// Row i's line into `line`. A window leaves out the nodes whose positions are out
+// of it (the position is c where it is not asked for).
+__device__ __forceinline__ void tree_line(uint32_t* line, const int* parents, int i, int c, int window, int n_sink) {
+  int depth = 0;
+  if (window != 0)
+    for (int a = parents[i]; a >= 0; a = parents[a]) ++depth;
+#pragma unroll
+  for (int w = 0; w < kLineWords; ++w) line[w] = 0u;
+  uint32_t bits = 0;
+  int at = i >> 5, up = 0;
+  for (int a = i; a >= 0; a = parents[a], ++up) {          // descends: a word is done when the next begins
+    if ((a >> 5) != at) {
+      line[at] = bits;
+      bits = 0;
+      at = a >> 5;
+    }
+    if (window == 0 || up < window || c + depth - up < n_sink) bits |= 1u << (a & 31);
+  }
+  line[at] = bits;
+  line[kLineWords] = (uint32_t)(c + depth);
+}
+// Bits of the tokens t0 .. t0 + 31 that a node sees: of the cached ones, then of its line.
+__device__ __forceinline__ uint32_t cached_bits(int p, int t0, int c, int window, int n_sink) {
+  const int n = c - t0;
+  return sees_bits(p, t0, window, n_sink) & (n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* line, int t0, int c, int window, int n_sink) {
+  const int o = t0 - c;                                    // the node at t0
+  uint32_t own = 0;
+  if (o >= 0 && o < kTreeMost) {
+    const int w = o >> 5;
+    own = (uint32_t)(((uint64_t)(w + 1 < kLineWords ? line[w + 1] : 0u) << 32 | line[w]) >> (o & 31));
+  } else if (o < 0 && o > -32) {
+    own = line[0] << -o;
+  }
+  return own | cached_bits((int)line[kLineWords], t0, c, window, n_sink);
+}
+
+__device__ __forceinline__ uint32_t small_tree_bits(uint32_t line, int p, int t0, int c, int window, int n_sink) {
+  const int o = t0 - c;                                    // as above, for trees of at most 32 rows
+  const uint32_t own = o >= 32 || o <= -32 ? 0u : o >= 0 ? line >> o : line << -o;
+  return own | cached_bits(p, t0, c, window, n_sink);
+}
+
 // This workgroup's place among tiles of their own: 8 neighbours, which read much
 // the same rows, to each of the 8 XCDs in turn (all of an XCD's in one piece
 // would leave a prompt's long tiles to one of them). Two chunks of 2048 rows,
@@ -139,15 +198,18 @@ __device__ __forceinline__ void store_part(float* part, int wg, int row_tiles, c
 // them over the banks. They are issued from inline asm, so that the compiler
 // does not wait for them before every LDS read; they write no register, and a
 // wave waits for all of its loads before the barrier that opens their step.
+template <bool TREE>
 __global__ void __launch_bounds__(256, 1)
     paged_attn_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool, Pages pg,
                       const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B, int T, int H,
                       int max_rows, int max_len, int window, int n_sink, float scale2, int planned, int row_tiles,
                       uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part_o,
-                      float2* __restrict__ part_ml, PartInfo* __restrict__ info) {
+                      float2* __restrict__ part_ml, PartInfo* __restrict__ info, const int32_t* __restrict__ parent) {
   __shared__ __align__(128) uint8_t tiles[kBufs * kTileB];
   __shared__ __align__(16) uint8_t ps[kMT * kPPitch];
   __shared__ float s_alpha[kMT], s_l[kMT];
+  __shared__ uint32_t s_line[TREE ? kMT * kLinePitch : 1];
+  __shared__ int s_parent[TREE ? kTreeMost : 1];
   __shared__ int s_flag[4];   // per row tile: 1 = its maximum grew, 2 = a score that does not count is not finite
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -168,7 +230,7 @@ __global__ void __launch_bounds__(256, 1)
   if (planned) note_tile(info, wk, wg, mg0, min(kMT, M - m0), planned);
   if (b < 0) return;
   const int r_lo = m0 / H, r_hi = (min(m0 + kMT, M) - 1) / H;
-  const int p_lo = sr.pos0 + r_lo, p_hi = sr.pos0 + r_hi;
+  const int p_lo = TREE ? sr.pos0 : sr.pos0 + r_lo, p_hi = sr.pos0 + r_hi;   // of a tree: bounds
   const Ranges rg = ranges_of<kStepTok>(p_lo, p_hi, window, n_sink);
   const int per = (rg.steps + nsp - 1) / nsp;
   const int step0 = min(sp * per, rg.steps), nsteps = min(step0 + per, rg.steps) - step0;
@@ -315,10 +377,13 @@ __global__ void __launch_bounds__(256, 1)
   };
   // the tokens of a step that this lane's query sees, as bits for its 16 scores
   auto seen_bits = [&](int t0, uint32_t ok) -> uint32_t {
-    return (sees_bits(p_row, t0, window, n_sink) & ok) >> (4 * g);
+    uint32_t bits;
+    if constexpr (TREE) bits = tree_bits(s_line + (wave * 32 + col) * kLinePitch, t0, sr.pos0, window, n_sink);
+    else bits = sees_bits(p_row, t0, window, n_sink);
+    return (bits & ok) >> (4 * g);
   };
   auto whole_step = [&](int t0, uint32_t ok) -> bool {
-    return ok == 0xffffffffu && t0 + kStepTok - 1 <= p_lo &&
+    return ok == 0xffffffffu && t0 + kStepTok - 1 <= (TREE ? sr.pos0 - 1 : p_lo) &&
            (window == 0 || t0 > p_hi - window || t0 + kStepTok <= n_sink);
   };
   // what the weights of a step change before its value product: accumulators of
@@ -348,8 +413,10 @@ __global__ void __launch_bounds__(256, 1)
     if (!(any & 2)) return false;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int p = sr.pos0 + min(m0 + r * 32 + col, M - 1) / H;
-      const uint32_t seen = (sees_bits(p, t0, window, n_sink) & ok) >> (4 * g);
+      uint32_t seen;
+      if constexpr (TREE) seen = tree_bits(s_line + (r * 32 + col) * kLinePitch, t0, sr.pos0, window, n_sink);
+      else seen = sees_bits(sr.pos0 + min(m0 + r * 32 + col, M - 1) / H, t0, window, n_sink);
+      seen = (seen & ok) >> (4 * g);
       const bf16x8_t one0 = seen_ones(seen & 15u, (seen >> 8) & 15u), one1 = seen_ones((seen >> 16) & 15u, (seen >> 24) & 15u);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -395,9 +462,14 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
     for (int s = 0; s < kKs16; ++s) qf[s] = ld_bf16x8(qp + s * 32);
   }
+  if constexpr (TREE) {
+    if ((int)threadIdx.x <= r_hi) s_parent[threadIdx.x] = parent_of(parent + sr.first, threadIdx.x);
+  }
   __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
   __syncthreads();
   issue(slot2, 2);                 // read a round later: the queries do not wait for it
+  // read by these lanes, and by other waves behind the round's first barrier
+  if constexpr (TREE) tree_line(s_line + (wave * 32 + col) * kLinePitch, s_parent, mr, sr.pos0, window, n_sink);
   f32x16_t st, nx;
 #pragma unroll
   for (int v = 0; v < 16; ++v) st[v] = 0.f;
@@ -561,15 +633,17 @@ __device__ __forceinline__ float quad_sum(float x) {
   return pair_sum(__uint_as_float(p[0]) + __uint_as_float(p[1]));
 }
 
-template <int QT>
+template <int QT, bool TREE>
 __global__ void __launch_bounds__(256, 1)
     paged_attn_narrow_kernel(const uint16_t* __restrict__ q, int64_t q_rs, int64_t q_hs, const uint8_t* __restrict__ pool,
                              Pages pg, const int32_t* __restrict__ row0, const int32_t* __restrict__ seq_len, int B,
                              int T, int H, int max_rows, int max_len, int window, int n_sink, float scale2, int planned,
                              int row_tiles, uint16_t* __restrict__ out, float* __restrict__ lse,
-                             float* __restrict__ part_o, float2* __restrict__ part_ml, PartInfo* __restrict__ info) {
+                             float* __restrict__ part_o, float2* __restrict__ part_ml, PartInfo* __restrict__ info,
+                             const int32_t* __restrict__ parent) {
   __shared__ __align__(128) uint8_t tiles[2 * kNTile];
   __shared__ __align__(16) uint8_t s_p[4 * 1024];   // P: per wave's tokens, a lane's 16 bytes
+  __shared__ uint2 s_line[TREE ? kNM : 1];   // a tree's: each query's line and position
   __shared__ int s_page[4][2][64];   // per wave: page-table entries of two rounds' tokens
   __shared__ float s_x[4][kNM];      // per wave: a round's maximum of each query; at the end its sum
   __shared__ int s_poison[2][4];     // per wave: its tokens with a slot, and whether (bit 16) a score that does not count
@@ -662,6 +736,7 @@ __global__ void __launch_bounds__(256, 1)
 
   if (rounds > 0) {
     int p_row[QT];
+    uint32_t line[QT];
     bf16x8_t qf[QT][kNKs];
     int slot;
     {
@@ -678,6 +753,32 @@ __global__ void __launch_bounds__(256, 1)
       const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + grp * 16;
 #pragma unroll
       for (int s = 0; s < kNKs; ++s) qf[h][s] = ld_bf16x8(qp + s * 64);
+    }
+    if constexpr (TREE) {
+      // at most 32 rows: a lane holds a row's parent, every wave follows them alike
+      const int mine = lane < sr.n ? parent_of(parent + sr.first, lane) : -1;
+#pragma unroll
+      for (int h = 0; h < QT; ++h) {
+        const int i = p_row[h] - sr.pos0;
+        int a = i, depth = 0;
+        if (window != 0) {
+          while (__any(a >= 0)) {
+            const int next = __shfl(mine, max(a, 0), 64);   // by every lane: the source has to be active
+            a = a >= 0 ? next : -1;
+            depth += a >= 0;
+          }
+          a = i;
+        }
+        uint32_t bits = 0;
+        for (int up = 0; __any(a >= 0); ++up) {
+          if (a >= 0 && (window == 0 || up < window || sr.pos0 + depth - up < n_sink)) bits |= 1u << a;
+          const int next = __shfl(mine, max(a, 0), 64);
+          a = a >= 0 ? next : -1;
+        }
+        line[h] = bits;
+        p_row[h] = sr.pos0 + depth;
+        if (grp == 0) s_line[16 * h + c16] = make_uint2(bits, (uint32_t)p_row[h]);   // every wave writes the same
+      }
     }
     for (int i = 0; i < rounds; ++i) {
       __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's rows of round i, the entries of round i + 1
@@ -702,11 +803,15 @@ __global__ void __launch_bounds__(256, 1)
       float tmax[QT];
       bool poison = false;   // a score that does not count is not finite: its row holds infinities or NaN
       {
-        const bool whole = ok == 0xffffu && t0 + kNTok - 1 <= sr.pos0 &&
+        const bool whole = ok == 0xffffu && t0 + kNTok - 1 <= (TREE ? sr.pos0 - 1 : sr.pos0) &&
                            (window == 0 || t0 > sr.pos0 + sr.n - 1 - window || t0 + kNTok <= n_sink);
 #pragma unroll
         for (int h = 0; h < QT; ++h) {
-          const uint32_t bits = whole ? 0xffffu : (sees_bits(p_row[h], t0, window, n_sink) & ok);
+          uint32_t bits = 0xffffu;
+          if (!whole) {
+            if constexpr (TREE) bits = small_tree_bits(line[h], p_row[h], t0, sr.pos0, window, n_sink) & ok;
+            else bits = sees_bits(p_row[h], t0, window, n_sink) & ok;
+          }
           tmax[h] = -__builtin_inff();
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
@@ -778,7 +883,15 @@ __global__ void __launch_bounds__(256, 1)
         const int p = sr.pos0 + min(col, M - 1) / H;
 #pragma unroll 1   // rare: nothing of it is kept in registers across rounds
         for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t seen = (sees_bits(p, t0 + (kk - wave) * kNTok, window, n_sink) & (uint32_t)bad[kk] & 0xffffu) >> (8 * g);
+          const int tk = t0 + (kk - wave) * kNTok;
+          uint32_t seen;
+          if constexpr (TREE) {
+            const uint2 ln = s_line[QT == 2 ? col : c16];
+            seen = small_tree_bits(ln.x, (int)ln.y, tk, sr.pos0, window, n_sink);
+          } else {
+            seen = sees_bits(p, tk, window, n_sink);
+          }
+          seen = (seen & (uint32_t)bad[kk] & 0xffffu) >> (8 * g);
           const bf16x8_t ones = seen_ones(seen & 15u, (seen >> 4) & 15u);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -962,11 +1075,12 @@ extern "C" size_t ech_paged_attn_ws_bytes(int B, int T, int H, int max_rows, int
   return split_of(B, T, H, max_rows, max_len, window, n_sink).bytes;
 }
 
-extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool,
-                              int64_t n_slots, int page_size, const int32_t* page_table, int64_t pt_ld,
-                              const int32_t* row0, const int32_t* seq_len, int B, int T, int H, int max_rows,
-                              int max_len, int window, int n_sink, float sm_scale, void* out, float* lse, void* ws,
-                              size_t ws_bytes, void* stream) {
+// ech_paged_attn, and ech_paged_tree_attn with the rows' parents.
+static int attn_call(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool, int64_t n_slots,
+                     int page_size, const int32_t* page_table, int64_t pt_ld, const int32_t* row0,
+                     const int32_t* seq_len, const int32_t* parent, int B, int T, int H, int max_rows, int max_len,
+                     int window, int n_sink, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                     void* stream) {
   if (!pool || !row0 || !seq_len || (T > 0 && (!q || !out))) return ECH_EINVAL;
   if (!shape_ok(B, T, H, max_rows, max_len, window, n_sink) || !pages_ok(n_slots, page_size, page_table, pt_ld))
     return ECH_EINVAL;
@@ -986,11 +1100,15 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
   PartInfo* info = sp.planned ? reinterpret_cast<PartInfo*>(w + sp.info) : nullptr;
   const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
   const int64_t queries = (int64_t)std::min(max_rows, T) * H;
-  const auto kernel = !sp.narrow ? paged_attn_kernel : queries <= 16 ? paged_attn_narrow_kernel<1> : paged_attn_narrow_kernel<2>;
+  const bool one = queries <= 16;
+  const auto kernel = !sp.narrow ? (parent ? paged_attn_kernel<true> : paged_attn_kernel<false>)
+                      : one      ? (parent ? paged_attn_narrow_kernel<1, true> : paged_attn_narrow_kernel<1, false>)
+                                 : (parent ? paged_attn_narrow_kernel<2, true> : paged_attn_narrow_kernel<2, false>);
   hipLaunchKernelGGL(kernel, dim3((unsigned)(sp.planned ? kCus : sp.tiles)), dim3(256), 0, s,
                      static_cast<const uint16_t*>(q), q_row_stride, q_head_stride, static_cast<const uint8_t*>(pool), pg,
                      row0, seq_len, B, T, H, max_rows, max_len, window, n_sink, sm_scale * 1.4426950408889634f,
-                     sp.planned ? (int)sp.tiles : 0, sp.row_tiles, static_cast<uint16_t*>(out), lse, part_o, part_ml, info);
+                     sp.planned ? (int)sp.tiles : 0, sp.row_tiles, static_cast<uint16_t*>(out), lse, part_o, part_ml, info,
+                     parent);
   ECH_LAUNCH_CHECK();
   if (sp.planned) {
     hipLaunchKernelGGL(paged_attn_merge_kernel, dim3((unsigned)sp.tiles, 16 * sp.row_tiles), dim3(256), 0, s, part_o, part_ml, info,
@@ -998,4 +1116,28 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
     ECH_LAUNCH_CHECK();
   }
   return ECH_OK;
+}
+
+extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool,
+                              int64_t n_slots, int page_size, const int32_t* page_table, int64_t pt_ld,
+                              const int32_t* row0, const int32_t* seq_len, int B, int T, int H, int max_rows,
+                              int max_len, int window, int n_sink, float sm_scale, void* out, float* lse, void* ws,
+                              size_t ws_bytes, void* stream) {
+  return attn_call(q, q_row_stride, q_head_stride, pool, n_slots, page_size, page_table, pt_ld, row0, seq_len, nullptr, B,
+                   T, H, max_rows, max_len, window, n_sink, sm_scale, out, lse, ws, ws_bytes, stream);
+}
+
+extern "C" size_t ech_paged_tree_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
+  if (max_rows > kTreeMost) return 0;
+  return ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink);
+}
+
+extern "C" int ech_paged_tree_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool,
+                                   int64_t n_slots, int page_size, const int32_t* page_table, int64_t pt_ld,
+                                   const int32_t* row0, const int32_t* seq_len, const int32_t* parent, int B, int T,
+                                   int H, int max_rows, int max_len, int window, int n_sink, float sm_scale, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if ((T > 0 && !parent) || max_rows > kTreeMost) return ECH_EINVAL;
+  return attn_call(q, q_row_stride, q_head_stride, pool, n_slots, page_size, page_table, pt_ld, row0, seq_len, parent, B,
+                   T, H, max_rows, max_len, window, n_sink, sm_scale, out, lse, ws, ws_bytes, stream);
 }

@@ -20,6 +20,8 @@ against the pages:
                   selects through sel_slot (the consumer of the path).
 - ``paged``     - the resident paged cache: append, attention of a step's new
                   rows, received attention weight, eviction.
+- ``drafts``    - drafted tokens over it: attention of trees, verification, the
+                  accepted rows' move.
 
 Sources: the ECHO explainer page ("One layer, one step: free -> allocate ->
 recall", "Decode: fetch above a predicted threshold", "Prefill: one-round
@@ -31,7 +33,7 @@ Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 brute force on tiny inputs, library routines and invariants; none is marked
 "parity unpinned".
 """
-from . import numerics, indexer, select, slotmap, attention, append, paged  # noqa: F401
+from . import numerics, indexer, select, slotmap, attention, append, paged, drafts  # noqa: F401
 from .numerics import bf16_to_f64, e4m3fn_to_f64, e4m3fn_table  # noqa: F401
 from .indexer import index_logits, index_logit_at, dequant_keys  # noqa: F401
 from .select import topk_row, topk_rows, theta_next, theta_rows  # noqa: F401
