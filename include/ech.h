@@ -25,7 +25,9 @@
  *      the key cache (growing contexts).
  * Next to it, layers that keep their rows resident (contexts below k tokens,
  * windowed layers, budgeted caches) hold them in pages of a device pool:
- * ech_paged_append, ech_paged_attn, ech_paged_weight, ech_paged_evict.
+ * ech_paged_append, ech_paged_attn, ech_paged_weight, ech_paged_evict. Steps over
+ * drafted tokens: ech_paged_tree_attn, ech_draft_verify, ech_paged_accept; pages
+ * are copied by ech_paged_copy.
  *
  * Conventions
  *  - Ownership: the caller owns every buffer (device memory, the pinned host
@@ -68,6 +70,10 @@ extern "C" {
 /* ---- key dtypes */
 #define ECH_KEY_BF16 0        /* keys [P, D] bf16, no scale */
 #define ECH_KEY_FP8  1        /* keys [P, D] OCP e4m3fn, one fp32 scale per token */
+
+/* ---- types of a target's logits */
+#define ECH_LOGIT_BF16 0
+#define ECH_LOGIT_F32  1
 
 /* ---- cache-step phases */
 #define ECH_EARLY   0         /* decode: fetch tokens scoring above theta, up to cap */
@@ -586,6 +592,92 @@ int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* seq_len, in
                     int n_recent, int32_t* kept, float* acc_out, int32_t* len_out, void* pool, int64_t n_slots,
                     int64_t row_bytes, int page_size, const int32_t* src_table, const int32_t* dst_table,
                     int64_t pt_ld, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Drafted tokens. A step over drafts brings each sequence the rows of a tree:
+ * row 0 the last token that is certain, the others drafts, each of which
+ * follows an earlier row. ech_paged_append and ech_paged_tree_attn run the
+ * layers over them; the target's logits then say which drafts stay
+ * (ech_draft_verify), and the rows of those move together behind the cached
+ * tokens (ech_paged_accept).
+ */
+
+/*
+ * ech_draft_verify - which drafted tokens the target's probabilities accept,
+ * from given random numbers, and the token that follows them. The output has the
+ * target's distribution whatever the drafts are. Row r of a sequence has the
+ * token tokens[row0[b] + r] and the target's logits for what follows it, and
+ *   p_r(v) = exp(logits[r,v] / temperature) / sum_w exp(logits[r,w] / temperature).
+ * The branch starts at row 0 (its token is taken). At row r, unless `most` rows
+ * are kept, r's children (the rows that follow it) are tried in order. With
+ * p = p_r, child c of token x:
+ *   draft NULL: accepted iff p(x) > 0 and u[c] sum(p) < p(x); else p(x) = 0
+ *               (a token that was tried is not accepted a second time)
+ *   draft q:    accepted iff p(x) > 0 and u[c] q(x) < p(x); else
+ *               p = max(p - q, 0) / its sum, or p where that is 0 everywhere
+ * An accepted child is the branch's next row. Where none is, the sequence's next
+ * token is the first v with sum_{w <= v} p(w) > u[row0[b]] sum(p), over what is
+ * left of p (all of it where no child was tried).
+ * A sequence at temperature 0 (or below, or NaN) is greedy: the child whose token
+ * is the row's largest logit (the lowest such token) is accepted, and the next
+ * token is that token; u and draft play no part. Sums are in 64 bits.
+ *  logits [T, V], ltype ECH_LOGIT_BF16 or _F32, rows ld values apart (ld >= V).
+ *         NaN counts as -inf, +inf as the largest finite float. A row whose
+ *         logits are all -inf accepts nothing and has the next token -1.
+ *  tokens [T] int32; one outside 0 .. V-1 is not accepted.
+ *  row0   [B+1] int32, as for the paged calls. A sequence without rows has
+ *         n_kept 0 and the next token -1.
+ *  parent [T] int32 as for ech_paged_tree_attn, or NULL: chains, row i follows
+ *         row i - 1. Rows that follow no row are never kept, row 0 apart.
+ *  draft  [T, V] fp32, rows draft_ld values apart, or NULL: row r's probabilities
+ *         from which its child was drawn. Chains only (parent NULL). Negative
+ *         values and NaN count as 0.
+ *  u      [T] fp32 in [0, 1) (others count as the nearest, NaN as 0): of a
+ *         sequence's first row for its next token, of the others for themselves.
+ *  temperature [B] fp32, or NULL: 1.
+ *  kept   [B, most] int32: the branch's rows, ascending (0 first), then -1.
+ *  n_kept [B] int32: how many; next_token [B] int32.
+ *  max_rows >= every row0[b+1] - row0[b], at most 256; of a sequence with more
+ *  only the first max_rows rows are looked at. V <= 2^24, T ceil((V + 7) / 2048)
+ *  < 2^31 - 4.
+ *  ws     ech_draft_verify_ws_bytes(...) bytes, 256-byte aligned, uninitialised
+ *         OK. Calls that share it must be ordered. May be captured.
+ */
+size_t ech_draft_verify_ws_bytes(int B, int T, int V, int max_rows, int most);
+int ech_draft_verify(const void* logits, int ltype, int64_t ld, int V, const int32_t* tokens, const int32_t* row0,
+                     const int32_t* parent, const float* draft, int64_t draft_ld, const float* u,
+                     const float* temperature, int B, int T, int max_rows, int most, int32_t* kept, int32_t* n_kept,
+                     int32_t* next_token, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ech_paged_accept - the accepted rows of a step's drafts move together. Of
+ * sequence b's n new rows, behind c = seq_len[b] - n cached tokens, row
+ * kept[b,j] (j < n_kept[b]) goes to the slot of token c + j, in place, and
+ *   len_out[b] = c + n_kept[b]        (may be seq_len)
+ * Pages from ceil(len_out / page_size) on are free. kept ascends within a
+ * sequence and names rows below n; one that does not is not moved. A row without
+ * a slot on either side is not moved. Sequences that share pages must not share
+ * those of their new rows.
+ *  kept [B, most], n_kept [B]: those of ech_draft_verify (cut to 0 .. min(most, n)).
+ *  row0, seq_len, max_rows, max_len and the pages as above, as for the step's
+ *  append; row_bytes a multiple of 16, at most 2^20, pool 16-byte aligned.
+ */
+int ech_paged_accept(void* pool, int64_t n_slots, int64_t row_bytes, int page_size, const int32_t* page_table,
+                     int64_t pt_ld, const int32_t* row0, const int32_t* seq_len, int B, int max_rows, int max_len,
+                     const int32_t* kept, int most, const int32_t* n_kept, int32_t* len_out, void* stream);
+
+/*
+ * ech_paged_copy - page src[i] of the pool is copied to page dst[i], its first
+ * rows[i] rows or (rows NULL) all of it: a forked sequence's last, partly filled
+ * page, a page of its own before shared ones are written, a pool that is packed.
+ *  src, dst, rows [n] int32, device. A dst may be no other's dst and no src. A
+ *  page outside the pool is not copied; of one that the pool's end cuts only the
+ *  rows before it.
+ *  row_bytes a multiple of 16, at most 2^20, page_size row_bytes / 16 < 2^31, pool
+ *  16-byte aligned. May be captured.
+ */
+int ech_paged_copy(void* pool, int64_t n_slots, int64_t row_bytes, int page_size, const int32_t* src,
+                   const int32_t* dst, const int32_t* rows, int n, void* stream);
 
 #ifdef __cplusplus
 }

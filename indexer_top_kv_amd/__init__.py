@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from . import _native
-from ._native import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, ECH_KEY_BF16, ECH_KEY_FP8,  # noqa: F401
+from ._native import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, ECH_KEY_BF16, ECH_KEY_FP8, ECH_LOGIT_BF16, ECH_LOGIT_F32,  # noqa: F401
                       CTR_HEAD, CTR_EPOCH, CTR_NMISS, CTR_NEVICT, CTR_RECALLED, CTR_STATUS, CTR_NWANT,
                       CTR_NPINNED, CTR_NMISS_EARLY, CTR_TICKET, CTR_NCOPIED_EARLY, CTR_LIVE,
                       CTR_NCOPIED_FINAL, CTR_FINAL_READY, CTR_FINAL_DONE, CTR_EARLY_WALK, CTR_LEN, ST_OVERFLOW, ST_BADTOK,
@@ -25,7 +25,8 @@ __all__ = ['ech_kv_append', 'ech_sparse_attn', 'ech_sparse_attn_ws_bytes', 'ech_
            'ech_cache_step', 'ech_cache_step_ws_bytes', 'ech_recall', 'ech_index_logits_early',
            'ech_index_logits_early_ws_bytes', 'ech_recall_early_live', 'ech_recall_rest', 'ech_topk_early', 'ech_paged_append',
            'ech_paged_attn', 'ech_paged_attn_ws_bytes', 'ech_paged_tree_attn', 'ech_paged_tree_attn_ws_bytes', 'ech_paged_weight', 'ech_paged_weight_ws_bytes',
-           'ech_paged_evict', 'ech_paged_evict_ws_bytes', 'EchError', 'LayerState', 'lib']
+           'ech_paged_evict', 'ech_paged_evict_ws_bytes', 'ech_paged_accept', 'ech_paged_copy', 'ech_draft_verify',
+           'ech_draft_verify_ws_bytes', 'EchError', 'LayerState', 'lib']
 
 
 class EchError(RuntimeError):
@@ -466,3 +467,76 @@ def ech_paged_evict(acc, seq_len, max_len: int, keep: int, n_sink: int, n_recent
     _call('ech_paged_evict', dev, stream, acc.data_ptr(), ld, seq_len.data_ptr(), B, max_len, keep, n_sink, n_recent,
           kept.data_ptr(), _ptr(acc_out), len_out.data_ptr(), _ptr(pool), n_slots, row_bytes, page_size,
           _ptr(src_table) if pool is not None else None, _ptr(dst_table) if pool is not None else None, pt_ld, wp, wb)
+
+
+# ------------------------------------------------------------------ drafted tokens
+def ech_draft_verify_ws_bytes(B: int, T: int, V: int, max_rows: int, most: int) -> int:
+    _fits(B, T, V, max_rows, most)
+    return int(lib().ech_draft_verify_ws_bytes(B, T, V, max_rows, most))
+
+
+def ech_draft_verify(logits, tokens, row0, max_rows: int, u, kept, n_kept, next_token, parent=None, draft=None,
+                     temperature=None, ws=None, stream=None) -> None:
+    """Which drafts the target accepts, and the token that follows: logits [T,
+    V] bf16 or fp32 (rows may be strided), tokens [T] i32, row0 [B+1] i32, u
+    [T] fp32 in [0, 1), parent [T] i32 or None (chains), draft [T, V] fp32 or
+    None (chains only: the probabilities that drafts were drawn from),
+    temperature [B] fp32 or None (1; 0: greedy) -> kept [B, most] i32
+    (ascending, -1 padded), n_kept [B] i32, next_token [B] i32."""
+    T, V = _pair('logits', logits)
+    B, most = _pair('kept', kept)
+    _fits(max_rows, T, V, B, most)
+    dev = logits.get_device()
+    _arg('logits', logits, (torch.bfloat16, torch.float32), (T, V), dev, rows=True)
+    _arg('tokens', tokens, _I32, (T,), dev)
+    _arg('row0', row0, _I32, (B + 1,), dev)
+    _arg('u', u, _F32, (T,), dev)
+    _arg('kept', kept, _I32, (B, most), dev)
+    _arg('n_kept', n_kept, _I32, (B,), dev)
+    _arg('next_token', next_token, _I32, (B,), dev)
+    if parent is not None:
+        _arg('parent', parent, _I32, (T,), dev)
+    if draft is not None:
+        if parent is not None:
+            raise ValueError('draft: only chains are drawn from probabilities (parent has to be None)')
+        _arg('draft', draft, _F32, (T, V), dev, rows=True)
+    if temperature is not None:
+        _arg('temperature', temperature, _F32, (B,), dev)
+    wp, wb = _ws_arg(ws, dev)
+    _call('ech_draft_verify', dev, stream, logits.data_ptr(), ECH_LOGIT_BF16 if logits.dtype == torch.bfloat16 else ECH_LOGIT_F32,
+          logits.stride(0) if T > 1 else V, V, tokens.data_ptr(), row0.data_ptr(), _ptr(parent), _ptr(draft),
+          0 if draft is None else draft.stride(0) if T > 1 else V, u.data_ptr(), _ptr(temperature), B, T, max_rows, most,
+          kept.data_ptr(), n_kept.data_ptr(), next_token.data_ptr(), wp, wb)
+
+
+def ech_paged_accept(pool, page_table, page_size: int, row0, seq_len, kept, n_kept, max_rows: int, max_len: int, len_out,
+                     stream=None) -> None:
+    """The accepted rows of a step's drafts (kept [B, most] i32, n_kept [B]
+    i32) move together behind the cached tokens; len_out [B] i32 (may be
+    seq_len) = cached tokens + n_kept. pool [slots, row] of any type."""
+    dev, B = _batch_args(pool, page_table, row0, seq_len)
+    most = _pair('kept', kept)[1]
+    _fits(page_size, max_rows, max_len, B, most)
+    n_slots, width = have = _pair('pool', pool)
+    _arg('pool', pool, (pool.dtype,), have, dev)
+    _arg('kept', kept, _I32, (B, most), dev)
+    _arg('n_kept', n_kept, _I32, (B,), dev)
+    _arg('len_out', len_out, _I32, (B,), dev)
+    _call('ech_paged_accept', dev, stream, pool.data_ptr(), n_slots, width * pool.element_size(), page_size,
+          page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, max_rows, max_len,
+          kept.data_ptr(), most, n_kept.data_ptr(), len_out.data_ptr())
+
+
+def ech_paged_copy(pool, page_size: int, src, dst, rows=None, stream=None) -> None:
+    """Pages src [n] i32 of a pool [slots, row] (any type) to pages dst [n] i32,
+    their first rows [n] i32 or (None) all rows."""
+    dev, n = pool.get_device(), src.numel()
+    _fits(page_size, n)
+    n_slots, width = have = _pair('pool', pool)
+    _arg('pool', pool, (pool.dtype,), have, dev)
+    _arg('src', src, _I32, (n,), dev)
+    _arg('dst', dst, _I32, (n,), dev)
+    if rows is not None:
+        _arg('rows', rows, _I32, (n,), dev)
+    _call('ech_paged_copy', dev, stream, pool.data_ptr(), n_slots, width * pool.element_size(), page_size, src.data_ptr(),
+          dst.data_ptr(), _ptr(rows), n)

@@ -20,6 +20,9 @@ ECH_TOPK_SCRATCH_BYTES = 16 << 20
 ECH_KEY_BF16 = 0
 ECH_KEY_FP8 = 1
 
+ECH_LOGIT_BF16 = 0
+ECH_LOGIT_F32 = 1
+
 ECH_EARLY = 0
 ECH_FINAL = 1
 ECH_PREFILL = 2
@@ -84,6 +87,12 @@ SIGNATURES = {
     'ech_paged_weight': (ctypes.c_int, [_p, _i64, _i64, _p, _p, _i64, ctypes.c_int, _p, _i64, _p, _p,
                                         *[ctypes.c_int] * 7, ctypes.c_float, _p, _p, _i64, ctypes.c_float, _p, _sz,
                                         _p]),
+    'ech_paged_accept': (ctypes.c_int, [_p, _i64, _i64, ctypes.c_int, _p, _i64, _p, _p, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_int, _p, ctypes.c_int, _p, _p, _p]),
+    'ech_paged_copy': (ctypes.c_int, [_p, _i64, _i64, ctypes.c_int, _p, _p, _p, ctypes.c_int, _p]),
+    'ech_draft_verify_ws_bytes': (_sz, [ctypes.c_int] * 5),
+    'ech_draft_verify': (ctypes.c_int, [_p, ctypes.c_int, _i64, ctypes.c_int, _p, _p, _p, _p, _i64, _p, _p,
+                                        *[ctypes.c_int] * 4, _p, _p, _p, _p, _sz, _p]),
     'ech_paged_evict_ws_bytes': (_sz, [ctypes.c_int] * 3),
     'ech_paged_evict': (ctypes.c_int, [_p, _i64, _p, *[ctypes.c_int] * 5, _p, _p, _p, _p, _i64, _i64, ctypes.c_int, _p,
                                        _p, _i64, _p, _sz, _p]),

@@ -1,6 +1,8 @@
 // Rows that join and leave a resident paged cache: ech_paged_append puts a
 // step's new rows into their sequences' pages, ech_paged_evict keeps `keep`
-// tokens of each sequence and moves their rows together.
+// tokens of each sequence and moves their rows together, ech_paged_accept does
+// so with the accepted ones of a step's drafted rows, and ech_paged_copy copies
+// pages.
 #include <algorithm>
 
 #include "common.hpp"
@@ -532,6 +534,85 @@ __global__ void __launch_bounds__(kWithinThreads)
   }
 }
 
+// ------------------------------------------------------------------ accepted drafts
+// A workgroup per sequence, a thread per 16-byte column. A kept row's place is
+// never behind it, and a thread carries its column of all rows, in order: it
+// reads kAccept rows before it writes their places, which no later row comes
+// from, so nothing waits but for its own loads.
+constexpr int kAccept = 8;
+__global__ void __launch_bounds__(256)
+    paged_accept_kernel(uint4* __restrict__ pool, int row16, Pages pg, const int32_t* __restrict__ row0,
+                        const int32_t* seq_len, int max_rows, int max_len, const int32_t* __restrict__ kept, int most,
+                        const int32_t* __restrict__ n_kept, int32_t* len_out) {   // len_out may be seq_len
+  const int b = blockIdx.x;
+  const SeqRows sr = seq_rows(row0, seq_len, pg, b, INT32_MAX, max_rows, max_len);
+  const int count = min(min(max(n_kept[b], 0), most), sr.n);
+  const int32_t* kb = kept + (int64_t)b * most;
+  const int32_t* row = pg.table + (int64_t)b * pg.ld;
+  for (int c = threadIdx.x; c < row16; c += blockDim.x) {
+    for (int j0 = 0; j0 < count; j0 += kAccept) {
+      uint4 v[kAccept];
+      int to[kAccept];
+#pragma unroll
+      for (int u = 0; u < kAccept; ++u) {
+        const int j = j0 + u, from = j < count ? kb[j] : -1;
+        to[u] = -1;
+        if (from > j && from < sr.n && sr.pos0 + j >= 0) {   // in its place already, or none of the step's
+          const int s = slot_of(pg, row, sr.pos0 + from);
+          if (s >= 0) {
+            to[u] = slot_of(pg, row, sr.pos0 + j);
+            v[u] = pool[(int64_t)s * row16 + c];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAccept; ++u)
+        if (to[u] >= 0) pool[(int64_t)to[u] * row16 + c] = v[u];
+    }
+  }
+  __syncthreads();                                         // every thread has read the length
+  if (threadIdx.x == 0) len_out[b] = max(sr.pos0 + count, 0);
+}
+
+// ------------------------------------------------------------------ copied pages
+// The copies' pieces of 16 bytes one after another, kCopyEach * 256 a workgroup;
+// a piece's page by the workgroup's first one, which 64 bits name, and a
+// division in 32.
+constexpr int kCopyEach = 4, kCopyX = 1 << 22;
+__global__ void __launch_bounds__(256)
+    paged_copy_kernel(u32x4_t* __restrict__ pool, int row16, uint32_t n_slots, int page_size, uint32_t n_pages,
+                      const int32_t* __restrict__ src, const int32_t* __restrict__ dst, const int32_t* __restrict__ rows, int n,
+                      int64_t page16) {
+  const int64_t first = ((int64_t)blockIdx.y * kCopyX + blockIdx.x) * (256 * kCopyEach);
+  const int64_t p0 = first / page16;
+  const uint32_t in0 = (uint32_t)(first - p0 * page16);    // < page16 < 2^31
+  u32x4_t v[kCopyEach];
+  int64_t to[kCopyEach];
+#pragma unroll
+  for (int u = 0; u < kCopyEach; ++u) {
+    uint32_t in = in0 + u * 256 + threadIdx.x;
+    int64_t p = p0;
+    if (in >= (uint32_t)page16) {
+      const uint32_t more = in / (uint32_t)page16;
+      p += more;
+      in -= more * (uint32_t)page16;
+    }
+    to[u] = -1;
+    if (p < n) {
+      const uint32_t a = (uint32_t)src[p], d = (uint32_t)dst[p], off = in / (uint32_t)row16;
+      const uint32_t limit = rows ? (uint32_t)max(rows[p], 0) : (uint32_t)page_size;
+      if (a < n_pages && d < n_pages && off < limit && a * (uint32_t)page_size + off < n_slots &&
+          d * (uint32_t)page_size + off < n_slots) {
+        v[u] = pool[(int64_t)a * page16 + in];
+        to[u] = (int64_t)d * page16 + in;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kCopyEach; ++u)
+    if (to[u] >= 0) pool[to[u]] = v[u];
+}
+
 }  // namespace
 
 extern "C" int ech_paged_append(void* pool, int64_t n_slots, int64_t row_bytes, int page_size,
@@ -654,6 +735,39 @@ extern "C" int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* 
                        keep);
   else
     hipLaunchKernelGGL(paged_move_kernel<0>, mgrid, dim3(256), 0, s, static_cast<u32x4_t*>(pool), row16, a, d, kept, keep);
+  ECH_LAUNCH_CHECK();
+  return ECH_OK;
+}
+
+extern "C" int ech_paged_accept(void* pool, int64_t n_slots, int64_t row_bytes, int page_size,
+                                const int32_t* page_table, int64_t pt_ld, const int32_t* row0, const int32_t* seq_len,
+                                int B, int max_rows, int max_len, const int32_t* kept, int most, const int32_t* n_kept,
+                                int32_t* len_out, void* stream) {
+  if (!pool || !row0 || !seq_len || !kept || !n_kept || !len_out) return ECH_EINVAL;
+  if (!batch_ok(B, 0, max_rows, max_len) || most < 1 || !pages_ok(n_slots, page_size, page_table, pt_ld)) return ECH_EINVAL;
+  if (row_bytes < 16 || row_bytes % 16 || row_bytes > (1 << 20) || !aligned16_(pool)) return ECH_EINVAL;
+  const Pages pg = make_pages(page_table, pt_ld, n_slots, page_size);
+  const int row16 = (int)(row_bytes / 16);
+  hipLaunchKernelGGL(paged_accept_kernel, dim3(B), dim3(std::min(256, (row16 + 63) / 64 * 64)), 0,
+                     reinterpret_cast<hipStream_t>(stream), static_cast<uint4*>(pool), row16, pg, row0, seq_len, max_rows,
+                     max_len, kept, most, n_kept, len_out);
+  ECH_LAUNCH_CHECK();
+  return ECH_OK;
+}
+
+extern "C" int ech_paged_copy(void* pool, int64_t n_slots, int64_t row_bytes, int page_size, const int32_t* src,
+                              const int32_t* dst, const int32_t* rows, int n, void* stream) {
+  if (!pool || n < 0 || (n > 0 && (!src || !dst))) return ECH_EINVAL;
+  if (n_slots < 1 || n_slots >= (1ll << 31) || page_size < 1 || page_size > (1 << 20)) return ECH_EINVAL;
+  if (row_bytes < 16 || row_bytes % 16 || row_bytes > (1 << 20) || !aligned16_(pool)) return ECH_EINVAL;
+  const int64_t page16 = (int64_t)page_size * (row_bytes / 16);
+  const int64_t each = 256 * kCopyEach;
+  if (page16 >= (1ll << 31) || page16 * n >= (1ll << 22) * 65535 * each) return ECH_EINVAL;
+  if (n == 0) return ECH_OK;
+  const int64_t wgs = (page16 * n + each - 1) / each;
+  hipLaunchKernelGGL(paged_copy_kernel, dim3((unsigned)std::min<int64_t>(wgs, kCopyX), (unsigned)((wgs + kCopyX - 1) / kCopyX)),
+                     dim3(256), 0, reinterpret_cast<hipStream_t>(stream), static_cast<u32x4_t*>(pool), (int)(row_bytes / 16),
+                     (uint32_t)n_slots, page_size, (uint32_t)((n_slots + page_size - 1) / page_size), src, dst, rows, n, page16);
   ECH_LAUNCH_CHECK();
   return ECH_OK;
 }

@@ -62,10 +62,10 @@ def attention(q_bits, pool_bits, table, page, row0, seq_len, parent, sm_scale, w
 
 def weights(logits, temperature):
     """Unnormalised probabilities of one row (the largest is 1). NaN weighs
-    nothing, of infinities each weighs the same; temperature 0, below or NaN: the
-    first largest alone."""
+    nothing, an infinite logit counts as the largest finite float; temperature 0,
+    below or NaN: the first largest alone."""
     x = np.asarray(logits, np.float64)
-    x = np.where(np.isnan(x), -np.inf, x)
+    x = np.where(np.isnan(x), -np.inf, np.minimum(x, np.finfo(np.float32).max))
     top = x.max()
     if top == -np.inf:
         return np.zeros(len(x))
@@ -75,7 +75,7 @@ def weights(logits, temperature):
         return w
     with np.errstate(invalid='ignore', over='ignore'):
         w = np.exp((x - top) / float(np.float32(temperature)))
-    return np.where(x == top, 1.0, np.where(x == -np.inf, 0.0, w))
+    return np.where(x == -np.inf, 0.0, w)
 
 
 def pick(w, u):
