@@ -622,7 +622,7 @@ int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* seq_len, in
  * is the row's largest logit (the lowest such token) is accepted, and the next
  * token is that token; u and draft play no part. Sums are in 64 bits.
  *  logits [T, V], ltype ECH_LOGIT_BF16 or _F32, rows ld values apart (ld >= V).
- *         NaN counts as -inf, +inf as the largest finite float. A row whose
+ *         NaN counts as -inf, +inf as the type's largest finite value. A row whose
  *         logits are all -inf accepts nothing and has the next token -1.
  *  tokens [T] int32; one outside 0 .. V-1 is not accepted.
  *  row0   [B+1] int32, as for the paged calls. A sequence without rows has
