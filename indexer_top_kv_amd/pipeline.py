@@ -34,7 +34,9 @@ Resident layers (PagedLayer): a layer whose rows all stay on the device, in
 pages of a pool (contexts below k tokens, where a selection would take every
 token anyway; windowed layers; caches held to a budget of tokens). One step
 takes any mix of prompt chunks and single tokens: append, attention over the
-pages, and with a budget the received weights and the eviction by them.
+pages, and with a budget the received weights and the eviction by them. Steps
+over drafted tokens bring trees of rows (draft), which DraftStep decides once
+for all layers of a model and accept compacts; sequences fork with shared pages.
 
 Nothing here computes: this module sizes buffers with torch, chooses the
 order of the C-ABI calls and the stream events between them.
@@ -42,7 +44,7 @@ order of the C-ABI calls and the stream events between them.
 from __future__ import annotations
 
 import warnings
-from typing import List, Optional, Tuple
+from typing import List, NamedTuple, Optional, Tuple
 
 import numpy as np
 import torch
@@ -52,7 +54,8 @@ from . import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, LayerState, ech_cache_reset, e
                ech_index_logits_early_ws_bytes, ech_kv_append, ech_recall, ech_recall_early_live, ech_recall_rest,
                ech_topk, ech_topk_early, ech_topk_ws_bytes, ech_paged_append, ech_paged_attn,
                ech_paged_attn_ws_bytes, ech_paged_evict, ech_paged_evict_ws_bytes, ech_paged_weight,
-               ech_paged_weight_ws_bytes, _raw_stream, _stream)
+               ech_paged_weight_ws_bytes, ech_paged_tree_attn, ech_paged_accept, ech_paged_copy, ech_draft_verify,
+               ech_draft_verify_ws_bytes, _raw_stream, _stream)
 
 
 def round_up(x: int, m: int) -> int:
@@ -624,13 +627,15 @@ class PageTables:
     """Host side of a paged pool: which pages each sequence holds, in token
     order, and which are free. `table` [B, per_seq] int32 is what the kernels
     read (a copy of it goes to the device); entries past a sequence's pages are
-    -1."""
+    -1. Forked sequences hold the same full pages, each until the last of them
+    returns it."""
 
     def __init__(self, B: int, n_pages: int, page_size: int, per_seq: int):
         self.page_size, self.n_pages, self.per_seq = page_size, n_pages, per_seq
         self.table = np.full((B, per_seq), -1, np.int32)
         self.held = np.zeros(B, np.int64)
         self.free = list(range(n_pages - 1, -1, -1))
+        self.more = np.zeros(n_pages, np.int64)     # how many sequences hold a page beside the first
 
     def need(self, lens) -> np.ndarray:
         """Pages that sequences of these lengths hold."""
@@ -643,19 +648,48 @@ class PageTables:
         need = self.need(lens)
         if np.any(need > self.per_seq):
             raise ValueError(f'a sequence needs {int(need.max())} pages, its table has {self.per_seq}')
-        if int((need - self.held).sum()) > len(self.free):
-            raise ValueError(f'{int((need - self.held).sum())} more pages needed, {len(self.free)} are free')
+        extra = int((need - self.held).sum())
+        if self.more.any():                         # a shared page that is returned is free with its last holder
+            back = [p for b in np.flatnonzero(need < self.held) for p in self.table[b, need[b]:self.held[b]]]
+            pages, times = np.unique(np.array(back, np.int64), return_counts=True)
+            extra += len(back) - int(np.sum(times > self.more[pages]))
+        if extra > len(self.free):
+            raise ValueError(f'{extra} more pages needed, {len(self.free)} are free')
         changed = np.flatnonzero(need != self.held)
         for b in changed[np.argsort((need - self.held)[changed])]:     # those that shrink first
             have, n = int(self.held[b]), int(need[b])
             if n < have:
-                self.free.extend(int(p) for p in self.table[b, n:have][::-1])
+                for p in self.table[b, n:have][::-1]:
+                    if self.more[p]:
+                        self.more[p] -= 1
+                    else:
+                        self.free.append(int(p))
                 self.table[b, n:have] = -1
             else:
                 for i in range(have, n):
                     self.table[b, i] = self.free.pop()
             self.held[b] = n
         return len(changed) > 0
+
+    def fork(self, src: int, dst, length: int, share: bool = True):
+        """The sequences dst, which hold nothing, get src's pages: its full ones
+        shared (share=False: none), the others as pages of their own. Returns
+        the copies that makes: (pages of src, pages, their rows that are
+        used). Raises, with nothing changed, if the pool cannot hold them."""
+        held = int(self.held[src])
+        full = length // self.page_size if share else 0
+        if len(dst) * (held - full) > len(self.free):
+            raise ValueError(f'{len(dst) * (held - full)} more pages needed, {len(self.free)} are free')
+        copies = []
+        for b in dst:
+            self.table[b, :full] = self.table[src, :full]
+            self.more[self.table[src, :full]] += 1
+            for i in range(full, held):
+                self.table[b, i] = self.free.pop()
+                copies.append((int(self.table[src, i]), int(self.table[b, i]),
+                               min(self.page_size, length - i * self.page_size)))
+            self.held[b] = held
+        return copies
 
 
 UPLOADS = 8     # uploads of a PagedLayer under way together: a step has one, with an eviction two
@@ -690,6 +724,18 @@ class PagedLayer:
     Buffers and workspace of a step of at most B rows (decoding) are the
     layer's, and the next step of the same T writes them again; those of more
     rows are new each time.
+
+    Drafted tokens: draft(q, rows, parent, counts) is a step whose rows are
+    trees (parent [T] int32, as in ech_paged_tree_attn; None: chains), or place
+    with drafts=True and launch with parent. The rows are in the cache until
+    accept(kept, n_kept, counts) leaves the accepted ones of each sequence
+    (those of ech_draft_verify); nothing else may be placed, forked or released
+    before it. DraftStep does both for a model's layers. A layer with a budget takes no
+    drafts: the weights that rejected rows hand out would stay.
+
+    fork(src, dst) lets the empty sequences dst go on from src's tokens: they
+    share its full pages (with a budget, whose evictions move rows, they get
+    copies), and own a copy of the last one.
 
     Steps of one layer run in the order of their calls, whatever streams these
     name: each call's stream waits for the layer's last one, and a stream other
@@ -730,6 +776,7 @@ class PagedLayer:
         # of decoding steps: outputs by T, the largest workspace so far, those that graphs hold
         self._bufs, self._ws, self._held = {}, None, []
         self._placed, self._most, self._fixed, self._long, self._sizes = 0, 0, None, 0, {}
+        self._drafts = None                 # rows a sequence of the drafts that are placed and not accepted
         self._last = self._stream = self._done = None
         self._leave(self._enter()[1])       # the zeros above come before the first call
 
@@ -796,7 +843,11 @@ class PagedLayer:
         what the blocks hold by then."""
         if self.device.type == 'cuda' and (torch.cuda.is_current_stream_capturing() if stream is None else
                                            _capturing(_as_stream(stream, self.device))):
-            raise RuntimeError('place, trim and release cannot be captured')
+            raise RuntimeError('place, trim, accept, fork and release cannot be captured')
+
+    def _no_drafts(self) -> None:
+        if self._drafts is not None:
+            raise RuntimeError('drafts are placed: accept has to come first')
 
     def _bounds(self, capturing: bool) -> Tuple[int, int]:
         """Host bounds of the placed step's rows a sequence and lengths, by which
@@ -843,8 +894,12 @@ class PagedLayer:
                 t.record_stream(s)
         return (*got, ws)
 
-    def _check_rows(self, q: torch.Tensor, rows: torch.Tensor) -> None:
+    def _check_rows(self, q: torch.Tensor, rows: torch.Tensor, parent: Optional[torch.Tensor] = None) -> None:
         """Refuse a step's tensors before anything of it is done."""
+        if parent is not None and (parent.shape != q.shape[:1] or parent.dtype != torch.int32 or
+                                   parent.device != self.device or not parent.is_contiguous()):
+            raise ValueError(f'parent: {tuple(parent.shape)} {parent.dtype} on {parent.device}, expected '
+                             f'{tuple(q.shape[:1])} int32 on {self.device}, dense')
         T, bits = q.shape[0], (torch.bfloat16, torch.int16, torch.uint16)
         for name, t, shape, types in (('q', q, (T, self.H, 576), bits), ('rows', rows, (T, 576), bits[:1])):
             if t.shape != shape or t.dtype not in types or t.device != self.device:
@@ -859,14 +914,18 @@ class PagedLayer:
         if T > 1 and rows.stride(0) < 576:
             raise ValueError(f'rows: strides {rows.stride()}, the rows overlap')
 
-    def place(self, counts, max_rows: Optional[int] = None) -> int:
+    def place(self, counts, max_rows: Optional[int] = None, drafts: bool = False) -> int:
         """Pages and lengths of a step that brings counts[b] rows to sequence
         b; returns T. Raises, with nothing changed, if they do not fit.
         max_rows: the number of rows a sequence that the step's launch is made
         for, where that is to be more than the largest count. A launch captured
         after it is valid for steps that are placed with the same max_rows (1:
-        decoding); one captured after a place without it for any step."""
+        decoding); one captured after a place without it for any step.
+        drafts: the rows are drafts, which accept has to follow."""
         self._not_captured()
+        self._no_drafts()
+        if drafts and self.budget is not None:
+            raise ValueError('a layer with a budget takes no drafts')
         counts = np.asarray(counts, np.int64)
         most = self.max_rows if max_rows is None else int(max_rows)
         if most > self.max_rows:
@@ -878,6 +937,7 @@ class PagedLayer:
             raise ValueError(f'a sequence would have {int(lens.max())} tokens, max_len is {self.max_len}')
         moved = self.pages.resize(lens)
         self.lens, self._placed = lens, int(counts.sum())
+        self._drafts = counts.copy() if drafts else None
         self._most, self._fixed, self._long = int(counts.max()), None if max_rows is None else most, self._len_bound()
         np.cumsum(counts, out=self._image[1:self.B + 1])
         self._place_lens()
@@ -886,23 +946,34 @@ class PagedLayer:
         self._leave(capturing)
         return self._placed
 
-    def launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
+    def launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None, parent: Optional[torch.Tensor] = None):
         """The kernels of the step that place() prepared: q [T, H, 576], rows
         [T, 576] bf16 -> (out, lse). T is at least the number of rows placed;
-        those behind are no sequence's, and their outputs mean nothing."""
-        self._check_rows(q, rows)
-        return self._launch(q, rows, stream)
+        those behind are no sequence's, and their outputs mean nothing. parent
+        [T] int32: the rows are trees (at most 256 rows a sequence; a captured
+        launch needs a place with such a max_rows before it)."""
+        self._check_rows(q, rows, parent)
+        return self._launch(q, rows, stream, parent)
 
-    def _launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None):
+    def _launch(self, q: torch.Tensor, rows: torch.Tensor, stream=None, parent: Optional[torch.Tensor] = None):
         T, ps = q.shape[0], self.pages.page_size
         if T < self._placed:
             raise ValueError(f'{self._placed} rows were placed, q has {T}')
+        if parent is not None and self._drafts is None:
+            raise ValueError('parent: the rows were not placed as drafts')
         s, capturing = self._enter(stream)
         R, L = self._bounds(capturing)
+        if parent is not None and R > 256:
+            self._leave(capturing)
+            raise ValueError(f'trees of up to {R} rows a sequence, 256 are possible')
         out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s, capturing)
         ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
-        ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
-                       window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+        if parent is None:
+            ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
+                           window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
+        else:
+            ech_paged_tree_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, parent, R, L, self.sm_scale, out,
+                                lse, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
         if self.budget is not None:
             ech_paged_weight(q, lse, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, self.acc,
                              self.acc, decay=self.decay, window=self.window, n_sink=self.n_sink, ws=ws, stream=stream)
@@ -939,9 +1010,71 @@ class PagedLayer:
         self.trim()
         return got
 
+    def draft(self, q: torch.Tensor, rows: torch.Tensor, parent: Optional[torch.Tensor], counts):
+        """place and launch of a step of drafts on the current stream; returns
+        (out, lse). accept follows."""
+        T = int(np.sum(counts))
+        if q.shape[0] != T or rows.shape[0] != T:
+            raise ValueError(f'counts name {T} rows, q has {q.shape[0]} and rows {rows.shape[0]}')
+        self._check_rows(q, rows, parent)
+        if parent is not None and np.max(counts, initial=0) > 256:
+            raise ValueError(f'a tree of {int(np.max(counts))} rows, 256 are possible')
+        self.place(counts, drafts=True)
+        return self._launch(q, rows, None, parent)
+
+    def _accept_launch(self, kept: torch.Tensor, n_kept: torch.Tensor, stream=None):
+        s, capturing = self._enter(stream)
+        ech_paged_accept(self.pool, self.table, self.pages.page_size, self.row0, self.seq_len, kept, n_kept, self._most,
+                         self.max_len, self.seq_len, stream=stream)
+        return s, capturing
+
+    def _accept_host(self, counts: np.ndarray, s, capturing: bool) -> None:
+        self.lens = self.lens - self._drafts + counts
+        self._drafts = None
+        self._place_lens()                  # as the call leaves them on the device
+        if self.pages.resize(self.lens):
+            with torch.cuda.stream(s):
+                self._upload(2 * self.B + 1, len(self._image))
+        self._leave(capturing)
+
+    def accept(self, kept: torch.Tensor, n_kept: torch.Tensor, counts, stream=None) -> None:
+        """The placed drafts' accepted rows stay, the others leave the cache: kept
+        [B, most], n_kept [B] int32 on the device, as ech_draft_verify writes
+        them; counts [B]: n_kept's numbers, on the host."""
+        if self._drafts is None:
+            raise RuntimeError('no drafts are placed')
+        self._not_captured(stream)
+        counts = np.asarray(counts, np.int64)
+        if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > self._drafts):
+            raise ValueError(f'counts must be {self.B} numbers from 0 to the rows placed')
+        self._accept_host(counts, *self._accept_launch(kept, n_kept, stream))
+
+    def fork(self, src: int, dst) -> None:
+        """The empty sequences dst (a number or several) go on from src's tokens."""
+        self._not_captured()
+        self._no_drafts()
+        dst = [int(b) for b in np.atleast_1d(dst)]
+        if len(set(dst)) < len(dst) or any(not 0 <= b < self.B or b == src or self.lens[b] for b in dst):
+            raise ValueError(f'{dst} have to be different empty sequences')
+        copies = self.pages.fork(src, dst, int(self.lens[src]), share=self.budget is None)
+        self.lens = self.lens.copy()
+        self.lens[dst] = self.lens[src]
+        self._place_lens()
+        _, capturing = self._enter()
+        self._upload(self.B + 1, len(self._image))
+        if copies and self.device.type == 'cuda':
+            host = torch.tensor(copies, dtype=torch.int32).t().contiguous().pin_memory()
+            which = host.to(self.device, non_blocking=True)
+            ech_paged_copy(self.pool, self.pages.page_size, which[0], which[1], which[2])
+        if self.acc is not None:
+            for b in dst:
+                self.acc[b].copy_(self.acc[src])
+        self._leave(capturing)
+
     def release(self, b: int) -> None:
         """Sequence b ends: its pages are free and its place starts empty."""
         self._not_captured()
+        self._no_drafts()
         lens = self.lens.copy()
         lens[b] = 0
         self.pages.resize(lens)
@@ -952,6 +1085,75 @@ class PagedLayer:
         if self.acc is not None:
             self.acc[b].zero_()
         self._leave(capturing)
+
+
+class Accepted(NamedTuple):
+    """What a step of drafts came to, on the host: rows kept a sequence, which
+    (ascending within the sequence's rows, -1 padded), and the tokens that follow."""
+    counts: np.ndarray
+    kept: np.ndarray
+    next_token: np.ndarray
+
+
+class DraftStep:
+    """The end of a step of drafts, for all resident layers of a model: which
+    drafts the target accepts is decided once, and every layer keeps those rows.
+
+    The layers hold the same sequences, and each had its draft() or launch() of
+    the step. finish(logits, tokens, u) takes the target's logits [T, V] for
+    what follows each row, the rows' tokens and random numbers (as in
+    ech_draft_verify), and waits for the decision: the next step's tokens are
+    the host's. The layers' rows move while it waits. `most`: rows that a branch
+    may keep (its depth + 1)."""
+
+    def __init__(self, layers, most: int):
+        self.layers = list(layers)
+        self.B, self.most, self.device = self.layers[0].B, int(most), self.layers[0].device
+        if any(x.B != self.B or x.device != self.device for x in self.layers) or self.most < 1:
+            raise ValueError('the layers hold the same sequences on one device; most is at least 1')
+        B, n = self.B, self.B * (self.most + 2)
+        self._out = torch.empty(n, dtype=torch.int32, device=self.device)
+        self._host = torch.empty(n, dtype=torch.int32, pin_memory=self.device.type == 'cuda')
+        self.kept, self.n_kept, self.next_token = self._split(self._out)
+        self._ws, self._last = None, None
+
+    def _split(self, x: torch.Tensor):
+        B = self.B
+        return x[:B * self.most].view(B, self.most), x[B * self.most:B * self.most + B], x[B * self.most + B:]
+
+    def finish(self, logits: torch.Tensor, tokens: torch.Tensor, u: torch.Tensor, parent: Optional[torch.Tensor] = None,
+               draft: Optional[torch.Tensor] = None, temperature: Optional[torch.Tensor] = None) -> Accepted:
+        placed = [x._drafts for x in self.layers]
+        if any(p is None or not np.array_equal(p, placed[0]) for p in placed):
+            raise RuntimeError('every layer has to have the same drafts placed')
+        first = self.layers[0]
+        first._not_captured()
+        if logits.dim() != 2 or logits.shape[0] < first._placed:
+            raise ValueError(f'{first._placed} rows were placed, logits has shape {tuple(logits.shape)}')
+        T, V = logits.shape
+        s = torch.cuda.current_stream(self.device)
+        if self._last is not None and self._last != s:
+            s.wait_stream(self._last)       # the buffers' last use
+        need = ech_draft_verify_ws_bytes(self.B, T, V, first._most, self.most)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        if self._last != s:
+            self._out.record_stream(s)
+            self._ws.record_stream(s)
+        self._last = s
+        for x in self.layers:               # the first one's offsets are read: behind its own last call
+            x._enter()
+        ech_draft_verify(logits, tokens, first.row0, first._most, u, self.kept, self.n_kept, self.next_token, parent=parent,
+                         draft=draft, temperature=temperature, ws=self._ws)
+        self._host.copy_(self._out, non_blocking=True)
+        done = torch.cuda.Event()
+        done.record(s)
+        under_way = [x._accept_launch(self.kept, self.n_kept) for x in self.layers]
+        done.synchronize()
+        kept, counts, nxt = (x.numpy().copy() for x in self._split(self._host))
+        for x, w in zip(self.layers, under_way):
+            x._accept_host(counts.astype(np.int64), *w)
+        return Accepted(counts, kept, nxt)
 
 
 def _as_stream(stream, device):

@@ -148,3 +148,80 @@ def test_oracle_accept():
     assert lens == [7, 6]
     np.testing.assert_array_equal(pool[[0, 1, 2, 3, 4]][:, 0], [0, 2, 3, 3, 4])
     np.testing.assert_array_equal(pool[5:, 0], np.arange(5, 24))
+
+
+def test_page_tables_of_forks():
+    """Shared pages are free with their last holder; a request that does not fit
+    changes nothing."""
+    from indexer_top_kv_amd.pipeline import PageTables
+    r = np.random.default_rng(6)
+    t, lens = PageTables(5, 24, 8, 9), np.zeros(5, int)
+    refused = forks = 0
+    for _ in range(2000):
+        before = (t.table.copy(), list(t.free), t.more.copy(), t.held.copy())
+        try:
+            if r.random() < 0.3 and (lens == 0).any() and lens.any():
+                src = int(r.choice(np.flatnonzero(lens)))
+                dst = [int(b) for b in np.flatnonzero(lens == 0)[:int(r.integers(1, 3))]]
+                share = bool(r.random() < 0.8)
+                copies = t.fork(src, dst, int(lens[src]), share)
+                forks += 1
+                for b in dst:
+                    lens[b] = lens[src]
+                    full = lens[src] // 8 if share else 0
+                    mine = [c for c in copies if c[1] in t.table[b, :t.held[b]]]
+                    assert np.array_equal(t.table[b, :full], t.table[src, :full]) and len(mine) == -(-lens[src] // 8) - full
+                    assert sum(c[2] for c in mine) == lens[src] - 8 * full
+            else:
+                want = np.where(r.random(5) < 0.15, 0, np.clip(lens + r.integers(-6, 14, 5), 0, 80))
+                want = np.where(want < lens, np.where(want == 0, 0, lens), want)   # sequences grow or end
+                t.resize(want)
+                lens = want
+        except ValueError:
+            refused += 1
+            for x, y in zip(before, (t.table, t.free, t.more, t.held)):
+                assert np.array_equal(x, y)
+        used = t.table[t.table >= 0]
+        pages, times = np.unique(used, return_counts=True)
+        assert np.array_equal(times - 1, t.more[pages]) and t.more.sum() == (times - 1).sum()
+        assert sorted(pages.tolist() + t.free) == list(range(24))
+        assert np.array_equal(t.held, t.need(lens))
+    assert refused > 50 and forks > 50
+
+
+def test_layer_refuses_what_drafts_do_not_allow():
+    """Out of turn, with a budget, of wrong shapes: nothing moves."""
+    from indexer_top_kv_amd.pipeline import PagedLayer
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)  # noqa: E731
+    layer = PagedLayer(2, 4, n_pages=20, max_len=600, max_rows=300, page_size=16, device='cpu')
+    q, rows = z(6, 4, 576, dt=torch.bfloat16), z(6, 576, dt=torch.bfloat16)
+    for call in (lambda: layer.accept(z(2, 2), z(2), [0, 0]),):
+        with pytest.raises(RuntimeError, match='no drafts'):
+            call()
+    for bad in (dict(parent=z(5)), dict(parent=z(6, dt=torch.int64)), dict(parent=z(12)[::2]), dict(counts=[3, 2])):
+        a = {**dict(parent=z(6), counts=[3, 3]), **bad}
+        with pytest.raises(ValueError):
+            layer.draft(q, rows, a['parent'], a['counts'])
+        assert layer.lens.tolist() == [0, 0] and layer._drafts is None
+    with pytest.raises(ValueError, match='256'):
+        layer.draft(z(257, 4, 576, dt=torch.bfloat16), z(257, 576, dt=torch.bfloat16), z(257), [257, 0])
+    with pytest.raises(ValueError, match='not placed as drafts'):
+        layer.place([3, 3])
+        layer.launch(q, rows, parent=z(6))
+    layer.place([3, 3], drafts=True)
+    for call in (lambda: layer.place([1, 1]), lambda: layer.release(0), lambda: layer.fork(0, 1)):
+        with pytest.raises(RuntimeError, match='accept'):
+            call()
+    for counts in ([4, 0], [-1, 0], [1]):
+        with pytest.raises(ValueError):
+            layer.accept(z(2, 3), z(2), counts)
+    assert layer.lens.tolist() == [6, 6]
+    with pytest.raises(ValueError, match='budget'):
+        PagedLayer(1, 4, n_pages=8, max_len=64, max_rows=8, page_size=16, budget=20, device='cpu').place([1], drafts=True)
+    layer = PagedLayer(4, 4, n_pages=20, max_len=600, max_rows=300, page_size=16, device='cpu')
+    layer.place([20, 0, 0, 5])
+    for dst in (0, [1, 1], 3, 4, -1, [1, 3]):
+        with pytest.raises(ValueError, match='empty'):
+            layer.fork(0, dst)
+    layer.fork(0, [1, 2])
+    assert layer.lens.tolist() == [20, 20, 20, 5] and layer.pages.more.sum() == 2

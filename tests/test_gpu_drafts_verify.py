@@ -1,7 +1,8 @@
-"""Verification of drafted tokens (ech_draft_verify) against the oracle. Both
-compute in 64 bits with sums of another order (at most some 1e-12 of a sum of
-so few tokens apart), so every number has to be equal wherever no decision lies
-within 1e-9 of its border, which the oracle says and the tests ask for."""
+"""Verification of drafted tokens (ech_draft_verify) against the oracle. Weights
+are within 4e-11 of the formula's, relatively, and so are their sums (nothing is
+subtracted), so both sides of a decision are within 1e-10: every number has to be
+equal where no decision lies within 1e-9 of its border, which the oracle says and
+the tests ask for."""
 import numpy as np
 import pytest
 import torch
