@@ -531,8 +531,8 @@ int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, c
  * c + (rows in its line - 1), its slot that of token c + i as everywhere
  * (append the rows first). It sees the c cached tokens and its line, and with a
  * window of those only what is at positions > its own - window or < n_sink. A
- * chain (parent i - 1) gives ech_paged_attn. Several rows may follow the cached
- * tokens.
+ * chain (parent i - 1) is ech_paged_attn up to the order of sums. Several rows
+ * may follow the cached tokens.
  *  parent [T] int32, device, -1 <= parent[row0[b] + i] < i; anything else counts
  *         as -1. Rows of no sequence are not read.
  *  max_rows at most 256 (ECH_EINVAL). Everything else as in ech_paged_attn.

@@ -91,10 +91,7 @@ constexpr int kTreeMost = 256;               // rows of a tree
 constexpr int kLineWords = kTreeMost / 32;
 constexpr int kLinePitch = kLineWords + 1;   // the position behind the bits; odd: banks
 
-__device__ __forceinline__ int parent_of(const int32_t* parent, int i) {   // one that does not precede its row: none
-  const int p = parent[i];
-  return p < i ? max(p, -1) : -1;
-}
+__device__ __forceinline__ int parent_of(int p, int i) { return p < i ? max(p, -1) : -1; }   // one not before its row: none
 // Row i's line into `line`. A window leaves out the nodes whose positions are out
 // of it (the position is c where it is not asked for).
 __device__ __forceinline__ void tree_line(uint32_t* line, const int* parents, int i, int c, int window, int n_sink) {
@@ -131,12 +128,6 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* line, int t0, int 
     own = line[0] << -o;
   }
   return own | cached_bits((int)line[kLineWords], t0, c, window, n_sink);
-}
-
-__device__ __forceinline__ uint32_t small_tree_bits(uint32_t line, int p, int t0, int c, int window, int n_sink) {
-  const int o = t0 - c;                                    // as above, for trees of at most 32 rows
-  const uint32_t own = o >= 32 || o <= -32 ? 0u : o >= 0 ? line >> o : line << -o;
-  return own | cached_bits(p, t0, c, window, n_sink);
 }
 
 // This workgroup's place among tiles of their own: 8 neighbours, which read much
@@ -440,6 +431,8 @@ __global__ void __launch_bounds__(256, 1)
   };
   auto pload = [&](int c, int r) -> bf16x8_t { return ld_bf16x8(pall + r * 32 * kPPitch + c * 32); };
 
+  int up = -1;                     // a row's parent, asked for before the rows: loads arrive in their order
+  if constexpr (TREE) up = parent[sr.first + min((int)threadIdx.x, r_hi)];
   int page, off;                   // of the step to load next
   int slot2;                       // of step 2
   uint32_t ok0, ok1, ok2;          // tokens with a slot of steps i, i + 1, i + 2
@@ -462,14 +455,15 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
     for (int s = 0; s < kKs16; ++s) qf[s] = ld_bf16x8(qp + s * 32);
   }
-  if constexpr (TREE) {
-    if ((int)threadIdx.x <= r_hi) s_parent[threadIdx.x] = parent_of(parent + sr.first, threadIdx.x);
+  if constexpr (TREE) {            // while the rows and queries arrive
+    if ((int)threadIdx.x <= r_hi) s_parent[threadIdx.x] = parent_of(up, threadIdx.x);
+    __syncthreads();
+    // read by these lanes, and by other waves behind the round's first barrier
+    tree_line(s_line + (wave * 32 + col) * kLinePitch, s_parent, mr, sr.pos0, window, n_sink);
   }
   __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's loads have landed
   __syncthreads();
   issue(slot2, 2);                 // read a round later: the queries do not wait for it
-  // read by these lanes, and by other waves behind the round's first barrier
-  if constexpr (TREE) tree_line(s_line + (wave * 32 + col) * kLinePitch, s_parent, mr, sr.pos0, window, n_sink);
   f32x16_t st, nx;
 #pragma unroll
   for (int v = 0; v < 16; ++v) st[v] = 0.f;
@@ -643,7 +637,8 @@ __global__ void __launch_bounds__(256, 1)
                              const int32_t* __restrict__ parent) {
   __shared__ __align__(128) uint8_t tiles[2 * kNTile];
   __shared__ __align__(16) uint8_t s_p[4 * 1024];   // P: per wave's tokens, a lane's 16 bytes
-  __shared__ uint2 s_line[TREE ? kNM : 1];   // a tree's: each query's line and position
+  __shared__ uint32_t s_line[TREE ? kNM * kLinePitch : 1];
+  __shared__ int s_parent[TREE ? kTreeMost : 1];
   __shared__ int s_page[4][2][64];   // per wave: page-table entries of two rounds' tokens
   __shared__ float s_x[4][kNM];      // per wave: a round's maximum of each query; at the end its sum
   __shared__ int s_poison[2][4];     // per wave: its tokens with a slot, and whether (bit 16) a score that does not count
@@ -659,11 +654,13 @@ __global__ void __launch_bounds__(256, 1)
   else wk = tile_work(row0, seq_len, pg, B, T, H, max_rows, max_len, kNM, (int)blockIdx.x);
   const int b = wk.b, sp = wk.sp, nsp = wk.n_span;
   const SeqRows sr = wk.sr;
-  const int M = sr.n * H;                                  // 1 .. 16 QT
-  const int64_t mg0 = (int64_t)sr.first * H;
+  const int m0 = TREE ? wk.mt * kNM : 0;                   // first query; of a tree's, several tiles may be
+  const int M = TREE ? min(sr.n * H - m0, kNM) : sr.n * H; // queries: 1 .. 16 QT
+  const int64_t mg0 = (int64_t)sr.first * H + m0;
   if (planned) note_tile(info, wk, wg, mg0, M, planned);
   if (b < 0) return;
-  const Ranges rg = ranges_of<kNRound>(sr.pos0, sr.pos0 + sr.n - 1, window, n_sink);
+  const int r_hi = TREE ? (m0 + M - 1) / H : sr.n - 1;
+  const Ranges rg = ranges_of<kNRound>(sr.pos0, sr.pos0 + r_hi, window, n_sink);
   const int per = (rg.steps + nsp - 1) / nsp;
   const int round0 = min(sp * per, rg.steps), rounds = min(round0 + per, rg.steps) - round0;
 
@@ -736,9 +733,10 @@ __global__ void __launch_bounds__(256, 1)
 
   if (rounds > 0) {
     int p_row[QT];
-    uint32_t line[QT];
     bf16x8_t qf[QT][kNKs];
     int slot;
+    int up = -1;                                  // a row's parent, asked for before the rows: loads arrive in their order
+    if constexpr (TREE) up = parent[sr.first + min((int)threadIdx.x, r_hi)];
     {
       int off0;
       const int page = *entry_of(0, off0);
@@ -748,37 +746,20 @@ __global__ void __launch_bounds__(256, 1)
     }
 #pragma unroll
     for (int h = 0; h < QT; ++h) {
-      const int m = min(16 * h + c16, M - 1), mr = m / H, mh = m - mr * H;   // past the end: the last one again
+      const int m = m0 + min(16 * h + c16, M - 1), mr = m / H, mh = m - mr * H;   // past the end: the last one again
       p_row[h] = sr.pos0 + mr;
       const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + grp * 16;
 #pragma unroll
       for (int s = 0; s < kNKs; ++s) qf[h][s] = ld_bf16x8(qp + s * 64);
     }
     if constexpr (TREE) {
-      // at most 32 rows: a lane holds a row's parent, every wave follows them alike
-      const int mine = lane < sr.n ? parent_of(parent + sr.first, lane) : -1;
-#pragma unroll
-      for (int h = 0; h < QT; ++h) {
-        const int i = p_row[h] - sr.pos0;
-        int a = i, depth = 0;
-        if (window != 0) {
-          while (__any(a >= 0)) {
-            const int next = __shfl(mine, max(a, 0), 64);   // by every lane: the source has to be active
-            a = a >= 0 ? next : -1;
-            depth += a >= 0;
-          }
-          a = i;
-        }
-        uint32_t bits = 0;
-        for (int up = 0; __any(a >= 0); ++up) {
-          if (a >= 0 && (window == 0 || up < window || sr.pos0 + depth - up < n_sink)) bits |= 1u << a;
-          const int next = __shfl(mine, max(a, 0), 64);
-          a = a >= 0 ? next : -1;
-        }
-        line[h] = bits;
-        p_row[h] = sr.pos0 + depth;
-        if (grp == 0) s_line[16 * h + c16] = make_uint2(bits, (uint32_t)p_row[h]);   // every wave writes the same
+      if ((int)threadIdx.x <= r_hi) s_parent[threadIdx.x] = parent_of(up, threadIdx.x);
+      __syncthreads();
+      if (lane < kNM / 4) {                        // this wave's eight queries
+        const int x = wave * (kNM / 4) + lane;
+        tree_line(s_line + x * kLinePitch, s_parent, (m0 + min(x, M - 1)) / H, sr.pos0, window, n_sink);
       }
+      __syncthreads();
     }
     for (int i = 0; i < rounds; ++i) {
       __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's rows of round i, the entries of round i + 1
@@ -804,12 +785,12 @@ __global__ void __launch_bounds__(256, 1)
       bool poison = false;   // a score that does not count is not finite: its row holds infinities or NaN
       {
         const bool whole = ok == 0xffffu && t0 + kNTok - 1 <= (TREE ? sr.pos0 - 1 : sr.pos0) &&
-                           (window == 0 || t0 > sr.pos0 + sr.n - 1 - window || t0 + kNTok <= n_sink);
+                           (window == 0 || t0 > sr.pos0 + r_hi - window || t0 + kNTok <= n_sink);
 #pragma unroll
         for (int h = 0; h < QT; ++h) {
           uint32_t bits = 0xffffu;
           if (!whole) {
-            if constexpr (TREE) bits = small_tree_bits(line[h], p_row[h], t0, sr.pos0, window, n_sink) & ok;
+            if constexpr (TREE) bits = tree_bits(s_line + (16 * h + c16) * kLinePitch, t0, sr.pos0, window, n_sink) & ok;
             else bits = sees_bits(p_row[h], t0, window, n_sink) & ok;
           }
           tmax[h] = -__builtin_inff();
@@ -886,8 +867,7 @@ __global__ void __launch_bounds__(256, 1)
           const int tk = t0 + (kk - wave) * kNTok;
           uint32_t seen;
           if constexpr (TREE) {
-            const uint2 ln = s_line[QT == 2 ? col : c16];
-            seen = small_tree_bits(ln.x, (int)ln.y, tk, sr.pos0, window, n_sink);
+            seen = tree_bits(s_line + col * kLinePitch, tk, sr.pos0, window, n_sink);
           } else {
             seen = sees_bits(p, tk, window, n_sink);
           }
@@ -1039,6 +1019,7 @@ int64_t tiles_of(int B, int T, int H, int64_t per_seq, int per) {
 // at most 16 its form with one query a lane (13.1, with two 13.6). Up to 256
 // tiles are split (32 tokens of 128 heads over 8K to 16K 151 us, not split 881;
 // 12 chunks of 77 rows 71, 282; window 1024 31, 50); more fill the CUs unsplit.
+constexpr bool kForceNarrow = true;
 struct Split {
   bool narrow;        // at most 32 queries a sequence
   bool planned;
@@ -1046,9 +1027,9 @@ struct Split {
   int row_tiles;      // of 32 queries a partial holds
   size_t part_o, part_ml, info, bytes;
 };
-Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
+Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink, bool tree = false) {
   Split sp{};
-  sp.narrow = (int64_t)std::min(max_rows, T) * H <= kNM;
+  sp.narrow = (int64_t)std::min(max_rows, T) * H <= kNM || (tree && kForceNarrow);
   const int per = sp.narrow ? kNM : kMT;
   const int64_t per_seq = ((int64_t)std::min(max_rows, T) * H + per - 1) / per;
   sp.tiles = tiles_of(B, T, H, per_seq, per);
@@ -1057,6 +1038,7 @@ Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n
   sp.planned = sp.tiles <= kCus && seen > kMinSpan * kStepTok && plan_fits(B, B * per_seq, seen);
   if (!sp.planned) return sp;
   sp.row_tiles = (int)((std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H) + 31) / 32);
+  if (sp.narrow) sp.row_tiles = 1;
   sp.part_ml = (size_t)kCus * sp.row_tiles * 32 * kPagedVal * sizeof(float);
   sp.info = sp.part_ml + (size_t)kCus * kMT * sizeof(float2);
   sp.bytes = sp.info + (size_t)kCus * sizeof(PartInfo);
@@ -1087,12 +1069,12 @@ static int attn_call(const void* q, int64_t q_row_stride, int64_t q_head_stride,
   if (!(sm_scale == sm_scale) || !aligned16_(q) || !aligned16_(pool) || !aligned16_(out) || q_row_stride < 0 ||
       q_head_stride < 0 || q_row_stride % 8 || q_head_stride % 8)
     return ECH_EINVAL;
-  const size_t need = ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink);
+  const size_t need = T == 0 || max_rows == 0 ? 0 : split_of(B, T, H, max_rows, max_len, window, n_sink, parent != nullptr).bytes;
   if (ws_bytes < need || (need && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)))) return ECH_EINVAL;
   if (T == 0 || max_rows == 0) return ECH_OK;
   if (window >= max_len) window = 0;                       // no position has more tokens behind it
   n_sink = std::min(n_sink, max_len);
-  const Split sp = split_of(B, T, H, max_rows, max_len, window, n_sink);
+  const Split sp = split_of(B, T, H, max_rows, max_len, window, n_sink, parent != nullptr);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
   float* part_o = reinterpret_cast<float*>(w);
@@ -1128,8 +1110,8 @@ extern "C" int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_hea
 }
 
 extern "C" size_t ech_paged_tree_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
-  if (max_rows > kTreeMost) return 0;
-  return ech_paged_attn_ws_bytes(B, T, H, max_rows, max_len, window, n_sink);
+  if (!shape_ok(B, T, H, max_rows, max_len, window, n_sink) || T == 0 || max_rows == 0 || max_rows > kTreeMost) return 0;
+  return split_of(B, T, H, max_rows, max_len, window, n_sink, true).bytes;
 }
 
 extern "C" int ech_paged_tree_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool,

