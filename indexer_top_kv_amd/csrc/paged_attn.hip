@@ -1019,26 +1019,37 @@ int64_t tiles_of(int B, int T, int H, int64_t per_seq, int per) {
 // at most 16 its form with one query a lane (13.1, with two 13.6). Up to 256
 // tiles are split (32 tokens of 128 heads over 8K to 16K 151 us, not split 881;
 // 12 chunks of 77 rows 71, 282; window 1024 31, 50); more fill the CUs unsplit.
-constexpr bool kForceNarrow = true;
+//
+// Trees. Tiles of 32 queries by the narrow kernel also for more queries, where
+// these and the tokens are so few that the start and the partials of a 128-query
+// tile cost more than its rows save: up to kSmall rounds of 64 tokens for each CU.
+// One sequence, 8 rows of 16 heads over 4000 tokens (1 round) 27 us, by the wide
+// kernel 34; 60 rows (7.5) 37 and 43; 16 trees of up to 27 rows, 32 heads, window
+// 1024 (12) 59 and 45.
+constexpr int kSmall = 8;
 struct Split {
-  bool narrow;        // at most 32 queries a sequence
+  bool narrow;        // at most 32 queries a tile
   bool planned;
   int64_t tiles;
   int row_tiles;      // of 32 queries a partial holds
   size_t part_o, part_ml, info, bytes;
 };
-Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink, bool tree = false) {
+Split split_of(int B, int T, int H, int max_rows, int max_len, int window, int n_sink, bool tree) {
   Split sp{};
-  sp.narrow = (int64_t)std::min(max_rows, T) * H <= kNM || (tree && kForceNarrow);
-  const int per = sp.narrow ? kNM : kMT;
-  const int64_t per_seq = ((int64_t)std::min(max_rows, T) * H + per - 1) / per;
-  sp.tiles = tiles_of(B, T, H, per_seq, per);
+  const int64_t queries = (int64_t)std::min(max_rows, T) * H;
   int64_t seen = max_len;                                  // tokens a tile can read
-  if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + kMT / H + 1 + kStepTok);
+  if (window > 0) seen = std::min<int64_t>(seen, (int64_t)window + n_sink + (tree ? kTreeMost : kMT / H + 1) + kStepTok);
+  sp.narrow = queries <= kNM;
+  if (tree && !sp.narrow) {
+    const int64_t tiles = tiles_of(B, T, H, (queries + kNM - 1) / kNM, kNM);
+    sp.narrow = tiles <= kCus && tiles * ((seen + kNRound - 1) / kNRound) <= kSmall * kCus;
+  }
+  const int per = sp.narrow ? kNM : kMT;
+  const int64_t per_seq = (queries + per - 1) / per;
+  sp.tiles = tiles_of(B, T, H, per_seq, per);
   sp.planned = sp.tiles <= kCus && seen > kMinSpan * kStepTok && plan_fits(B, B * per_seq, seen);
   if (!sp.planned) return sp;
-  sp.row_tiles = (int)((std::min<int64_t>(per, (int64_t)std::min(max_rows, T) * H) + 31) / 32);
-  if (sp.narrow) sp.row_tiles = 1;
+  sp.row_tiles = (int)((std::min<int64_t>(per, queries) + 31) / 32);
   sp.part_ml = (size_t)kCus * sp.row_tiles * 32 * kPagedVal * sizeof(float);
   sp.info = sp.part_ml + (size_t)kCus * kMT * sizeof(float2);
   sp.bytes = sp.info + (size_t)kCus * sizeof(PartInfo);
@@ -1054,7 +1065,7 @@ bool shape_ok(int B, int T, int H, int max_rows, int max_len, int window, int n_
 
 extern "C" size_t ech_paged_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink) {
   if (!shape_ok(B, T, H, max_rows, max_len, window, n_sink) || T == 0 || max_rows == 0) return 0;
-  return split_of(B, T, H, max_rows, max_len, window, n_sink).bytes;
+  return split_of(B, T, H, max_rows, max_len, window, n_sink, false).bytes;
 }
 
 // ech_paged_attn, and ech_paged_tree_attn with the rows' parents.

@@ -54,7 +54,7 @@ from . import (ECH_EARLY, ECH_FINAL, ECH_PREFILL, LayerState, ech_cache_reset, e
                ech_index_logits_early_ws_bytes, ech_kv_append, ech_recall, ech_recall_early_live, ech_recall_rest,
                ech_topk, ech_topk_early, ech_topk_ws_bytes, ech_paged_append, ech_paged_attn,
                ech_paged_attn_ws_bytes, ech_paged_evict, ech_paged_evict_ws_bytes, ech_paged_weight,
-               ech_paged_weight_ws_bytes, ech_paged_tree_attn, ech_paged_accept, ech_paged_copy, ech_draft_verify,
+               ech_paged_weight_ws_bytes, ech_paged_tree_attn, ech_paged_tree_attn_ws_bytes, ech_paged_accept, ech_paged_copy, ech_draft_verify,
                ech_draft_verify_ws_bytes, _raw_stream, _stream)
 
 
@@ -863,14 +863,15 @@ class PagedLayer:
         unit = max(256, (1 << n.bit_length()) // 16)
         return min(self.max_len, round_up(n, unit))
 
-    def _ws_bytes(self, T: int, R: int, L: int) -> int:
-        n = self._sizes.get((T, R, L))
+    def _ws_bytes(self, T: int, R: int, L: int, tree: bool) -> int:
+        n = self._sizes.get((T, R, L, tree))
         if n is None:
-            n = ech_paged_attn_ws_bytes(self.B, T, self.H, min(R, T), L, self.window, self.n_sink)
+            size = ech_paged_tree_attn_ws_bytes if tree else ech_paged_attn_ws_bytes
+            n = size(self.B, T, self.H, min(R, T), L, self.window, self.n_sink)
             if self.budget is not None:     # the two calls run one after the other: one workspace
                 n = max(n, ech_paged_weight_ws_bytes(self.B, T, self.H, min(R, T), L))
             if T <= self.B:
-                self._sizes[T, R, L] = n
+                self._sizes[T, R, L, tree] = n
         return n
 
     def _buffers(self, T: int, ws_bytes: int, s, capturing: bool):
@@ -966,7 +967,7 @@ class PagedLayer:
         if parent is not None and R > 256:
             self._leave(capturing)
             raise ValueError(f'trees of up to {R} rows a sequence, 256 are possible')
-        out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L), s, capturing)
+        out, lse, ws = self._buffers(T, self._ws_bytes(T, R, L, parent is not None), s, capturing)
         ech_paged_append(self.pool, self.table, ps, self.row0, self.seq_len, rows, self.status, stream=stream)
         if parent is None:
             ech_paged_attn(q, self.pool, self.table, ps, self.row0, self.seq_len, R, L, self.sm_scale, out, lse,
