@@ -250,8 +250,8 @@ __device__ __forceinline__ void sum_chunk(const Verify<E>& a, const Seq& q, int 
     uint32_t out = 0;                                      // child tokens among this lane's values
     const int first = a.parent ? 0 : i + 1, end = a.parent ? q.n : min(i + 2, q.n);
     for (int j0 = first; j0 < end; j0 += 64) {
-      const int j = j0 + lane;
-      const int tok = j < end && (!a.parent || parent_at(a.parent, q.r0, j) == i) ? a.tokens[q.r0 + j] : -1;
+      const int j = min(j0 + lane, end - 1), t = a.tokens[q.r0 + j];
+      const int tok = j0 + lane < end && (!a.parent || parent_at(a.parent, q.r0, j) == i) ? t : -1;
       unsigned long long hit = __ballot(tok >= max(e0, 0) && tok < min(e0 + kChunk, a.V));
       while (hit != 0ull) {
         const int rel = __builtin_amdgcn_readlane(tok, __builtin_ctzll(hit)) - e0;
@@ -320,17 +320,20 @@ __device__ __forceinline__ int decide(const Verify<E>& a, const Seq& q, int i, c
   // lane l holds rows l, 64 + l, ..: those that are children of i, their tokens and weights
   unsigned long long kids[kGroups];
   int tok[kGroups];
-  float x[kGroups];
+  float x[kGroups], u[kGroups];
   bool any = false;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     kids[g] = 0ull;
     tok[g] = -1;
+    u[g] = 0.f;
     if (g * 64 < q.n) {
-      const int j = g * 64 + lane;
-      const bool kid = j < q.n && parent_at(a.parent, q.r0, j) == i;
+      const int j = min(g * 64 + lane, q.n - 1);           // all three asked for at once
+      const int up = parent_at(a.parent, q.r0, j), t = a.tokens[q.r0 + j];
+      u[g] = a.u[q.r0 + j];
+      const bool kid = g * 64 + lane < q.n && up == i;
       kids[g] = __ballot(kid);
-      if (kid) tok[g] = a.tokens[q.r0 + j];
+      tok[g] = kid ? t : -1;
       any |= kids[g] != 0ull;
     }
   }
@@ -368,7 +371,8 @@ __device__ __forceinline__ int decide(const Verify<E>& a, const Seq& q, int i, c
     for (unsigned long long left = kids[g]; left != 0ull; left &= left - 1) {
       const int l = __builtin_ctzll(left);
       const double mine = lane_value(w[g], l), rest = r.base + lanes_sum((w[0] + w[1]) + (w[2] + w[3]));
-      if (mine > 0.0 && unit_of(a.u[q.r0 + g * 64 + l]) * rest < mine) return g * 64 + l;
+      const float here = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(u[g]), l));
+      if (mine > 0.0 && unit_of(here) * rest < mine) return g * 64 + l;
       if (lane == l) w[g] = 0.0;
     }
   }
@@ -576,10 +580,9 @@ __device__ __forceinline__ int pick_row(const Verify<E>& a, const Seq& q, int b,
     tok[g] = -1;
     w[g] = 0.0;
     if (g * 64 < q.n) {
-      const int j = g * 64 + lane;
-      const bool kid = j < q.n && (a.parent ? parent_at(a.parent, q.r0, j) == at : j == at + 1);
-      const int t = kid ? a.tokens[q.r0 + j] : -1;
-      if (t >= 0 && t < a.V) {
+      const int j = min(g * 64 + lane, q.n - 1), up = a.parent ? parent_at(a.parent, q.r0, j) : j - 1;
+      const int t = a.tokens[q.r0 + j];
+      if (g * 64 + lane < q.n && up == at && t >= 0 && t < a.V) {
         tok[g] = t;
         w[g] = weight_of(logit_at(row, t), r.top, q);
       }
