@@ -654,10 +654,10 @@ int ech_draft_verify(const void* logits, int ltype, int64_t ld, int V, const int
  * sequence b's n new rows, behind c = seq_len[b] - n cached tokens, row
  * kept[b,j] (j < n_kept[b]) goes to the slot of token c + j, in place, and
  *   len_out[b] = c + n_kept[b]        (may be seq_len)
- * Pages from ceil(len_out / page_size) on are free. kept ascends within a
- * sequence and names rows below n; one that does not is not moved. A row without
- * a slot on either side is not moved. Sequences that share pages must not share
- * those of their new rows.
+ * Pages from ceil(len_out / page_size) on are free. kept has to ascend within a
+ * sequence; numbers outside of j .. n - 1 are not moved. A row without a slot on
+ * either side is not moved. Sequences that share pages must not share those of
+ * their new rows.
  *  kept [B, most], n_kept [B]: those of ech_draft_verify (cut to 0 .. min(most, n)).
  *  row0, seq_len, max_rows, max_len and the pages as above, as for the step's
  *  append; row_bytes a multiple of 16, at most 2^20, pool 16-byte aligned.

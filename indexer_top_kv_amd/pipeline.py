@@ -636,6 +636,7 @@ class PageTables:
         self.held = np.zeros(B, np.int64)
         self.free = list(range(n_pages - 1, -1, -1))
         self.more = np.zeros(n_pages, np.int64)     # how many sequences hold a page beside the first
+        self.shared = 0                             # their sum
 
     def need(self, lens) -> np.ndarray:
         """Pages that sequences of these lengths hold."""
@@ -649,7 +650,7 @@ class PageTables:
         if np.any(need > self.per_seq):
             raise ValueError(f'a sequence needs {int(need.max())} pages, its table has {self.per_seq}')
         extra = int((need - self.held).sum())
-        if self.more.any():                         # a shared page that is returned is free with its last holder
+        if self.shared:                             # a shared page that is returned is free with its last holder
             back = [p for b in np.flatnonzero(need < self.held) for p in self.table[b, need[b]:self.held[b]]]
             pages, times = np.unique(np.array(back, np.int64), return_counts=True)
             extra += len(back) - int(np.sum(times > self.more[pages]))
@@ -659,11 +660,13 @@ class PageTables:
         for b in changed[np.argsort((need - self.held)[changed])]:     # those that shrink first
             have, n = int(self.held[b]), int(need[b])
             if n < have:
-                for p in self.table[b, n:have][::-1]:
-                    if self.more[p]:
-                        self.more[p] -= 1
-                    else:
-                        self.free.append(int(p))
+                back = self.table[b, n:have][::-1]
+                if self.shared:
+                    others = self.more[back] > 0
+                    self.more[back[others]] -= 1    # a sequence holds a page once
+                    self.shared -= int(others.sum())
+                    back = back[~others]
+                self.free.extend(int(p) for p in back)
                 self.table[b, n:have] = -1
             else:
                 for i in range(have, n):
@@ -684,6 +687,7 @@ class PageTables:
         for b in dst:
             self.table[b, :full] = self.table[src, :full]
             self.more[self.table[src, :full]] += 1
+            self.shared += full
             for i in range(full, held):
                 self.table[b, i] = self.free.pop()
                 copies.append((int(self.table[src, i]), int(self.table[b, i]),
@@ -863,7 +867,7 @@ class PagedLayer:
         unit = max(256, (1 << n.bit_length()) // 16)
         return min(self.max_len, round_up(n, unit))
 
-    def _ws_bytes(self, T: int, R: int, L: int, tree: bool) -> int:
+    def _ws_bytes(self, T: int, R: int, L: int, tree: bool = False) -> int:
         n = self._sizes.get((T, R, L, tree))
         if n is None:
             size = ech_paged_tree_attn_ws_bytes if tree else ech_paged_attn_ws_bytes
@@ -1055,8 +1059,9 @@ class PagedLayer:
         self._not_captured()
         self._no_drafts()
         dst = [int(b) for b in np.atleast_1d(dst)]
-        if len(set(dst)) < len(dst) or any(not 0 <= b < self.B or b == src or self.lens[b] for b in dst):
-            raise ValueError(f'{dst} have to be different empty sequences')
+        if not 0 <= src < self.B or len(set(dst)) < len(dst) or any(
+                not 0 <= b < self.B or b == src or self.lens[b] for b in dst):
+            raise ValueError(f'fork {src} to {dst}: these have to be different empty sequences')
         copies = self.pages.fork(src, dst, int(self.lens[src]), share=self.budget is None)
         self.lens = self.lens.copy()
         self.lens[dst] = self.lens[src]

@@ -158,7 +158,7 @@ def test_page_tables_of_forks():
     t, lens = PageTables(5, 24, 8, 9), np.zeros(5, int)
     refused = forks = 0
     for _ in range(2000):
-        before = (t.table.copy(), list(t.free), t.more.copy(), t.held.copy())
+        before = (t.table.copy(), list(t.free), t.more.copy(), t.held.copy(), t.shared)
         try:
             if r.random() < 0.3 and (lens == 0).any() and lens.any():
                 src = int(r.choice(np.flatnonzero(lens)))
@@ -179,11 +179,11 @@ def test_page_tables_of_forks():
                 lens = want
         except ValueError:
             refused += 1
-            for x, y in zip(before, (t.table, t.free, t.more, t.held)):
+            for x, y in zip(before, (t.table, t.free, t.more, t.held, t.shared)):
                 assert np.array_equal(x, y)
         used = t.table[t.table >= 0]
         pages, times = np.unique(used, return_counts=True)
-        assert np.array_equal(times - 1, t.more[pages]) and t.more.sum() == (times - 1).sum()
+        assert np.array_equal(times - 1, t.more[pages]) and t.more.sum() == (times - 1).sum() == t.shared
         assert sorted(pages.tolist() + t.free) == list(range(24))
         assert np.array_equal(t.held, t.need(lens))
     assert refused > 50 and forks > 50
@@ -220,8 +220,8 @@ def test_layer_refuses_what_drafts_do_not_allow():
         PagedLayer(1, 4, n_pages=8, max_len=64, max_rows=8, page_size=16, budget=20, device='cpu').place([1], drafts=True)
     layer = PagedLayer(4, 4, n_pages=20, max_len=600, max_rows=300, page_size=16, device='cpu')
     layer.place([20, 0, 0, 5])
-    for dst in (0, [1, 1], 3, 4, -1, [1, 3]):
+    for src, dst in ((0, 0), (0, [1, 1]), (0, 3), (0, 4), (0, -1), (0, [1, 3]), (-1, 1), (4, 1)):
         with pytest.raises(ValueError, match='empty'):
-            layer.fork(0, dst)
+            layer.fork(src, dst)
     layer.fork(0, [1, 2])
     assert layer.lens.tolist() == [20, 20, 20, 5] and layer.pages.more.sum() == 2

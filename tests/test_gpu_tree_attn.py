@@ -148,3 +148,46 @@ def test_absent_pages_and_short_lengths():
     check_attn(c.attn(table=dev(table)), c.ref(table=table), c.max_len)
     c.seq_len[:] = [7, 0]
     check_attn(c.attn(), c.ref(), c.max_len)
+
+
+@pytest.mark.parametrize('rows,H', [([5], 4), ([9], 16), ([40], 128)])
+def test_pages_behind_4_gib_of_pool(rows, H):
+    """The cached rows and the tree at the end of a pool of more than 2^32 bytes."""
+    need_gpu()
+    c = TreeCase(rows, [70], H, 16, seed=8)
+    n = 5 * 2 ** 30 // (16 * 1152)
+    pool = torch.zeros((n * 16, 576), dtype=torch.int16, device='cuda')
+    small = dev(c.pool)
+    far = n - len(c.pool) // 16
+    pool[far * 16:] = small
+    check_attn(c.attn(pool=pool, table=dev(c.table + far)), c.ref(), c.max_len)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each."""
+    need_gpu()
+    cs = [TreeCase([30, 12], [700, 40], 32, 16, seed=s) for s in (11, 12)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    bufs = []
+    for c in cs:
+        bufs.append([dev(x) for x in (c.q, c.pool, c.table, c.row0, c.seq_len, c.parent)] + [
+            torch.empty((c.T, c.H, 512), dtype=torch.bfloat16, device='cuda'), torch.empty((c.T, c.H), device='cuda'),
+            c.ws(ech.ech_paged_tree_attn_ws_bytes, c.B, c.T, c.H, c.max_rows, c.max_len, 0, 0)])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, b, s in zip(cs, bufs, streams):
+            ech.ech_paged_tree_attn(b[0], b[1], b[2], c.page, b[3], b[4], b[5], c.max_rows, c.max_len, SCALE, b[6], b[7], ws=b[8],
+                                    stream=s)
+    torch.cuda.synchronize()
+    for c, b in zip(cs, bufs):
+        check_attn((b[6].float().cpu().numpy(), b[7].cpu().numpy()), c.ref(), c.max_len)
+
+
+def test_strided_queries():
+    """Rows and heads of a wider tensor."""
+    need_gpu()
+    for rows, H in (([12], 16), ([3], 8), ([40], 24)):
+        c = TreeCase(rows, [100], H, 16, seed=13)
+        wide = torch.full((c.T, H + 2, 640), float('nan'), dtype=torch.bfloat16, device='cuda')
+        wide[:, 1:-1, 8:584] = dev(c.q).view(torch.bfloat16)
+        check_attn(c.attn(q=wide[:, 1:-1, 8:584]), c.ref(), c.max_len)

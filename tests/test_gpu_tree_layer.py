@@ -12,7 +12,7 @@ import oracle
 import workloads as wk
 from gpu_util import dev, host, need_gpu
 from indexer_top_kv_amd.pipeline import DraftStep, PagedLayer
-from test_gpu_drafts_tree import trees
+from test_gpu_tree_attn import trees
 from test_gpu_paged import SCALE, check_attn
 from test_gpu_paged_layer import Model
 
@@ -163,6 +163,7 @@ def test_captured_draft_launch():
     with pytest.raises(ValueError):
         a.place([10, 10], drafts=True)
         with torch.cuda.graph(torch.cuda.CUDAGraph()):          # made for any step: 300 rows a sequence
+            torch.zeros(1, device='cuda')
             a.launch(q, x, parent=parent)
     a.accept(torch.zeros((2, 1), dtype=torch.int32, device='cuda'), torch.zeros(2, dtype=torch.int32, device='cuda'), [0, 0])
     a.place([10, 10], max_rows=16, drafts=True)

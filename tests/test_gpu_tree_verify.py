@@ -11,7 +11,7 @@ import oracle
 from oracle.numerics import bf16_to_f64
 from gpu_util import dev, need_gpu
 import indexer_top_kv_amd as ech
-from test_gpu_drafts_tree import trees
+from test_gpu_tree_attn import trees
 import workloads as wk
 
 pytestmark = pytest.mark.gpu
@@ -34,7 +34,7 @@ class Drafts:
         before = np.array([int(self.row0[b]) + (i - 1 if kind is None else max(int(self.parent[self.row0[b] + i]), 0))
                            for b in range(self.B) for i in range(self.rows[b])], np.int64)
         before = np.concatenate([np.zeros(lead, np.int64), np.maximum(before, 0), np.zeros(tail, np.int64)])
-        top = np.argsort(-self.x, axis=1, kind='stable')[:, :3]
+        top = (np.argsort(-self.x, axis=1, kind='stable') if V < 20000 else np.argpartition(-self.x, 3, axis=1))[:, :3]
         self.tokens = np.where(r.random(self.T) < 0.8, top[before, r.integers(0, top.shape[1], self.T)],
                                r.integers(0, V, self.T)).astype(np.int32)
         self.draft = None
@@ -95,7 +95,16 @@ SHAPES = [
     ([7] * 5, 6001, None, True, [0.9], 4),
     ([3] * 70, 129, None, False, [0.7, 0.0], None),               # more sequences than a wave has lanes
     ([2] * 300, 64, 'star', False, None, None),
-    ([3], 70000, 'star', False, [0.7], None),                     # more chunks than a wave has lanes
+    ([3, 2], 140001, 'star', False, [0.7], None),                 # more chunks than a wave has lanes
+    ([3, 2, 1], 290000, None, True, [0.7, 1.0], None),
+    ([3, 2], 140000, None, False, [0.0], None),
+    # few rows of large batches: row by row
+    ([20, 0, 20, 20, 20, 20, 20, 25, 20], 70001, 'random', False, [0.8, 0.0, 1.0], 2),
+    ([20] * 8, 70000, None, True, [0.8, 0.0], 2),
+    ([60] * 6, 70001, 'binary', False, [0.8], 4),
+    ([64, 1, 64], 140001, 'forest', False, [1.0], 3),
+    ([16] * 5, 140001, None, True, [1.2], 2),
+    ([16] * 5, 140001, None, False, [1.2], 1),
 ]
 
 
