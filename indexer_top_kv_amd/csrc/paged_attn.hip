@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(256, 1)
 
 // ------------------------------------------------------------------ few queries
 // The same for sequences of at most 32 queries (a decoded token of up to 32
-// heads, two of 16): bound by the rows it reads, or, over short ranges, by the
+// heads, two of 16; of trees, also for tiles of 32 queries, see split_of): bound by the rows it reads, or, over short ranges, by the
 // chain of waits of a round. A round takes 64 tokens. Wave w loads tokens 16 w
 // .. +15 and forms their scores with all QT x 16 queries,
 //   S^T[token][m] = K . Q^T       v_mfma_f32_16x16x32_bf16
