@@ -470,6 +470,22 @@ def ech_paged_evict(acc, seq_len, max_len: int, keep: int, n_sink: int, n_recent
 
 
 # ------------------------------------------------------------------ drafted tokens
+# These calls are bound by the host at their smallest: numbers that fit are seen
+# by one shift, and what a shape says is asked for once.
+def _dense(name: str, t: torch.Tensor, dtypes, have, device: int) -> None:
+    """_arg for a tensor whose shape, `have`, is right."""
+    if not (t.dtype in dtypes and t.get_device() == device >= 0 and t.is_contiguous()):
+        _arg(name, t, dtypes, have, device)
+
+
+def _pool(pool: torch.Tensor):
+    """(device, slots, bytes of a row) of a pool of any type."""
+    have, dev = pool.shape, pool.get_device()
+    if len(have) != 2 or dev < 0 or not pool.is_contiguous():
+        _arg('pool', pool, (pool.dtype,), _pair('pool', pool), dev)
+    return dev, have[0], have[1] * pool.element_size()
+
+
 def ech_draft_verify_ws_bytes(B: int, T: int, V: int, max_rows: int, most: int) -> int:
     _fits(B, T, V, max_rows, most)
     return int(lib().ech_draft_verify_ws_bytes(B, T, V, max_rows, most))
@@ -483,27 +499,29 @@ def ech_draft_verify(logits, tokens, row0, max_rows: int, u, kept, n_kept, next_
     None (chains only: the probabilities that drafts were drawn from),
     temperature [B] fp32 or None (1; 0: greedy) -> kept [B, most] i32
     (ascending, -1 padded), n_kept [B] i32, next_token [B] i32."""
-    T, V = _pair('logits', logits)
-    B, most = _pair('kept', kept)
-    _fits(max_rows, T, V, B, most)
-    dev = logits.get_device()
-    _arg('logits', logits, (torch.bfloat16, torch.float32), (T, V), dev, rows=True)
-    _arg('tokens', tokens, _I32, (T,), dev)
+    T, V = have = _pair('logits', logits)
+    B, most = out = _pair('kept', kept)
+    if (max_rows | T | V | B | most) >> 31:
+        _fits(max_rows, T, V, B, most)
+    dev, rows, seqs = logits.get_device(), (T,), (B,)
+    bf16 = logits.dtype is torch.bfloat16
+    _arg('logits', logits, (torch.bfloat16, torch.float32), have, dev, rows=True)
+    _arg('tokens', tokens, _I32, rows, dev)
     _arg('row0', row0, _I32, (B + 1,), dev)
-    _arg('u', u, _F32, (T,), dev)
-    _arg('kept', kept, _I32, (B, most), dev)
-    _arg('n_kept', n_kept, _I32, (B,), dev)
-    _arg('next_token', next_token, _I32, (B,), dev)
+    _arg('u', u, _F32, rows, dev)
+    _dense('kept', kept, _I32, out, dev)
+    _arg('n_kept', n_kept, _I32, seqs, dev)
+    _arg('next_token', next_token, _I32, seqs, dev)
     if parent is not None:
-        _arg('parent', parent, _I32, (T,), dev)
+        _arg('parent', parent, _I32, rows, dev)
     if draft is not None:
         if parent is not None:
             raise ValueError('draft: only chains are drawn from probabilities (parent has to be None)')
-        _arg('draft', draft, _F32, (T, V), dev, rows=True)
+        _arg('draft', draft, _F32, have, dev, rows=True)
     if temperature is not None:
-        _arg('temperature', temperature, _F32, (B,), dev)
+        _arg('temperature', temperature, _F32, seqs, dev)
     wp, wb = _ws_arg(ws, dev)
-    _call('ech_draft_verify', dev, stream, logits.data_ptr(), ECH_LOGIT_BF16 if logits.dtype == torch.bfloat16 else ECH_LOGIT_F32,
+    _call('ech_draft_verify', dev, stream, logits.data_ptr(), ECH_LOGIT_BF16 if bf16 else ECH_LOGIT_F32,
           logits.stride(0) if T > 1 else V, V, tokens.data_ptr(), row0.data_ptr(), _ptr(parent), _ptr(draft),
           0 if draft is None else draft.stride(0) if T > 1 else V, u.data_ptr(), _ptr(temperature), B, T, max_rows, most,
           kept.data_ptr(), n_kept.data_ptr(), next_token.data_ptr(), wp, wb)
@@ -514,29 +532,37 @@ def ech_paged_accept(pool, page_table, page_size: int, row0, seq_len, kept, n_ke
     """The accepted rows of a step's drafts (kept [B, most] i32, n_kept [B]
     i32) move together behind the cached tokens; len_out [B] i32 (may be
     seq_len) = cached tokens + n_kept. pool [slots, row] of any type."""
-    dev, B = _batch_args(pool, page_table, row0, seq_len)
-    most = _pair('kept', kept)[1]
-    _fits(page_size, max_rows, max_len, B, most)
-    n_slots, width = have = _pair('pool', pool)
-    _arg('pool', pool, (pool.dtype,), have, dev)
-    _arg('kept', kept, _I32, (B, most), dev)
-    _arg('n_kept', n_kept, _I32, (B,), dev)
-    _arg('len_out', len_out, _I32, (B,), dev)
-    _call('ech_paged_accept', dev, stream, pool.data_ptr(), n_slots, width * pool.element_size(), page_size,
-          page_table.data_ptr(), page_table.shape[1], row0.data_ptr(), seq_len.data_ptr(), B, max_rows, max_len,
-          kept.data_ptr(), most, n_kept.data_ptr(), len_out.data_ptr())
+    dev, n_slots, row_bytes = _pool(pool)
+    table, have = _pair('page_table', page_table), _pair('kept', kept)
+    B, most = have
+    if (page_size | max_rows | max_len | B | most) >> 31:
+        _fits(page_size, max_rows, max_len, B, most)
+    seqs = (B,)
+    _arg('seq_len', seq_len, _I32, seqs, dev)
+    _arg('row0', row0, _I32, (B + 1,), dev)
+    _dense('kept', kept, _I32, have, dev)
+    if table[0] == B:
+        _dense('page_table', page_table, _I32, table, dev)
+    else:
+        _arg('page_table', page_table, _I32, (B, table[1]), dev)
+    _arg('n_kept', n_kept, _I32, seqs, dev)
+    _arg('len_out', len_out, _I32, seqs, dev)
+    _call('ech_paged_accept', dev, stream, pool.data_ptr(), n_slots, row_bytes, page_size, page_table.data_ptr(), table[1],
+          row0.data_ptr(), seq_len.data_ptr(), B, max_rows, max_len, kept.data_ptr(), most, n_kept.data_ptr(),
+          len_out.data_ptr())
 
 
 def ech_paged_copy(pool, page_size: int, src, dst, rows=None, stream=None) -> None:
     """Pages src [n] i32 of a pool [slots, row] (any type) to pages dst [n] i32,
     their first rows [n] i32 or (None) all rows."""
-    dev, n = pool.get_device(), src.numel()
-    _fits(page_size, n)
-    n_slots, width = have = _pair('pool', pool)
-    _arg('pool', pool, (pool.dtype,), have, dev)
-    _arg('src', src, _I32, (n,), dev)
-    _arg('dst', dst, _I32, (n,), dev)
+    dev, n_slots, row_bytes = _pool(pool)
+    n = src.numel()
+    if (page_size | n) >> 31:
+        _fits(page_size, n)
+    pages = (n,)
+    _arg('src', src, _I32, pages, dev)
+    _arg('dst', dst, _I32, pages, dev)
     if rows is not None:
-        _arg('rows', rows, _I32, (n,), dev)
-    _call('ech_paged_copy', dev, stream, pool.data_ptr(), n_slots, width * pool.element_size(), page_size, src.data_ptr(),
-          dst.data_ptr(), _ptr(rows), n)
+        _arg('rows', rows, _I32, pages, dev)
+    _call('ech_paged_copy', dev, stream, pool.data_ptr(), n_slots, row_bytes, page_size, src.data_ptr(), dst.data_ptr(),
+          _ptr(rows), n)
