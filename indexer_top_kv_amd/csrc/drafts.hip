@@ -301,20 +301,26 @@ __device__ __forceinline__ Joined join(const Verify<E>& a, const Seq& q, const E
   return r;
 }
 
-// The child that is accepted at row i of a tree or chain, or -1. By one wave.
+// The child that is accepted at row i of a tree or chain, or -1. By one wave. `end`:
+// a chain's largest logit there and its weight with the child's too.
 template <typename E>
-__device__ __forceinline__ int decide(const Verify<E>& a, const Seq& q, int i, const Stat* st, int lane) {
+__device__ __forceinline__ int decide(const Verify<E>& a, const Seq& q, int i, const Stat* st, int lane, Joined* end = nullptr) {
   const E* row = a.logits + (int64_t)(q.r0 + i) * a.ld;
   if (!a.parent) {
-    if (i + 1 >= q.n) return -1;
+    if (i + 1 >= q.n) {
+      if (end) *end = join(a, q, row, st, lane);
+      return -1;
+    }
     const int tok = a.tokens[q.r0 + i + 1];
     const bool known = tok >= 0 && tok < a.V;
     const float x = known ? logit_at(row, tok) : -__builtin_inff();
     const double u = unit_of(a.u[q.r0 + i + 1]);
     const double drawn = a.draft && known ? (double)draft_of(a.draft[(int64_t)(q.r0 + i) * a.draft_ld + tok]) : 1.0;
     const Joined r = join(a, q, row, st, lane);
+    if (end) *end = r;
     if (q.greedy) return known && tok == r.best ? i + 1 : -1;
     const double w = weight_of(x, r.top, q);
+    if (end) end->base = r.base + w;
     return w > 0.0 && u * (r.base + w) * drawn < w ? i + 1 : -1;
   }
   // lane l holds rows l, 64 + l, ..: those that are children of i, their tokens and weights
@@ -439,9 +445,11 @@ __global__ void __launch_bounds__(256) draft_level_kernel(Verify<E> a, int level
 // Where sequence b's branch ends, in every thread: row `at` of it, the `count`-th
 // kept. Row by row the levels have found it (levels of them); else WAVES rows are
 // decided at a time, a wave each, from the one that the branch has reached on.
-// `write`: kept and n_kept leave.
+// `write`: kept and n_kept leave. `s_end`: of the rows decided last, the first of
+// which is `spare`.
 template <int WAVES, bool LEVELS, typename E>
-__device__ __forceinline__ Place branch(const Verify<E>& a, const Seq& q, int b, int levels, bool write, int* s_next) {
+__device__ __forceinline__ Place branch(const Verify<E>& a, const Seq& q, int b, int levels, bool write, int* s_next,
+                                        Joined* s_end = nullptr) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   int32_t* const kb = a.kept + (int64_t)b * a.most;
   Place p{0, 1, 0, 0};
@@ -452,10 +460,15 @@ __device__ __forceinline__ Place branch(const Verify<E>& a, const Seq& q, int b,
     if (write && threadIdx.x == 0) kb[0] = 0;
     for (int first = 0;; first = p.at / WAVES * WAVES) {
       if (first + wave < q.n) {
-        const int next = decide(a, q, first + wave, a.stats + (int64_t)(q.r0 + first + wave) * a.chunks, lane);
-        if (lane == 0) s_next[wave] = next;
+        Joined end;
+        const int next = decide(a, q, first + wave, a.stats + (int64_t)(q.r0 + first + wave) * a.chunks, lane, s_end ? &end : nullptr);
+        if (lane == 0) {
+          s_next[wave] = next;
+          if (s_end) s_end[wave] = end;
+        }
       }
       __syncthreads();
+      p.spare = first;
       while (!p.ended && p.at < first + WAVES) {
         const int next = p.count < a.most ? s_next[p.at - first] : -1;
         if (next < 0) {
@@ -485,7 +498,7 @@ __device__ __forceinline__ void no_rows(const Verify<E>& a, int b) {
   }
 }
 
-constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
+constexpr int kPickThreads = 512, kPickWaves = kPickThreads / 64;
 struct PickShared {
   double sum[kPickWaves];
   int hit[kPickWaves], last[kPickWaves];
@@ -493,7 +506,7 @@ struct PickShared {
 
 // The first token up to which more than u of a row's weight lies (-1: nothing
 // weighs). chunk_sum(c) and weight(token) say the weights. Every wave finds the
-// chunk alike; its tokens are two a thread. Call from all threads.
+// chunk alike; its tokens are four a thread. Call from all threads.
 template <typename C, typename W>
 __device__ __forceinline__ int pick(int chunks, int lead, int V, double u, const C& chunk_sum, const W& weight, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -584,7 +597,7 @@ __device__ __forceinline__ int pick_row(const Verify<E>& a, const Seq& q, int b,
       const int t = a.tokens[q.r0 + j];
       if (g * 64 + lane < q.n && up == at && t >= 0 && t < a.V) {
         tok[g] = t;
-        w[g] = weight_of(logit_at(row, t), r.top, q);
+        if (!tried) w[g] = weight_of(logit_at(row, t), r.top, q);
       }
       kids[g] = __ballot(tok[g] >= 0);
     }
@@ -656,6 +669,7 @@ constexpr int kRestWaves = 8;
 template <typename E, bool LEVELS>
 __global__ void __launch_bounds__(kRestWaves * 64) draft_rest_kernel(Verify<E> a, int levels) {
   __shared__ int s_next[kRestWaves];
+  __shared__ Joined s_end[kRestWaves];
   const int b = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const bool first = blockIdx.x == 0;
   const Seq q = seq_of(a, b);
@@ -666,10 +680,17 @@ __global__ void __launch_bounds__(kRestWaves * 64) draft_rest_kernel(Verify<E> a
     }
     return;
   }
-  const Place p = branch<kRestWaves, LEVELS>(a, q, b, levels, first, s_next);
+  const Place p = branch<kRestWaves, LEVELS>(a, q, b, levels, first, s_next, s_end);
   const Stat* st = a.stats + (LEVELS ? (int64_t)((p.count - 1) & 1) * a.B + b : (int64_t)q.r0 + p.at) * a.chunks;
   const E* row = a.logits + (int64_t)(q.r0 + p.at) * a.ld;
-  const Joined r = join(a, q, row, st, lane);
+  Joined r;
+  if (LEVELS) {
+    r = join(a, q, row, st, lane);
+    const int tok = p.at + 1 < q.n ? a.tokens[q.r0 + p.at + 1] : -1;
+    if (tok >= 0 && tok < a.V) r.base += weight_of(logit_at(row, tok), r.top, q);
+  } else {
+    r = s_end[p.at - p.spare];                             // found with the decision
+  }
   if (q.greedy) {
     if (first && threadIdx.x == 0) {
       a.next[b] = r.best;
@@ -678,8 +699,7 @@ __global__ void __launch_bounds__(kRestWaves * 64) draft_rest_kernel(Verify<E> a
     return;
   }
   const bool tried = p.count < a.most && p.at + 1 < q.n;
-  const int tok = p.at + 1 < q.n ? a.tokens[q.r0 + p.at + 1] : -1;
-  const double inv = 1.0 / (r.base + (tok >= 0 && tok < a.V ? weight_of(logit_at(row, tok), r.top, q) : 0.0));
+  const double inv = 1.0 / r.base;
   if (first && threadIdx.x == 0) a.ends[b] = End{q.r0 + p.at, tried, r.top, 0, inv};
   const int chunk = blockIdx.x * kRestWaves + wave, e0 = chunk * kChunk - lead_of(row);
   if (!tried || e0 >= a.V) return;
