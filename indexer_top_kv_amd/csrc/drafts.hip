@@ -60,7 +60,7 @@ struct Verify {
   int32_t *kept, *n_kept, *next;
   // of the workspace
   Stat* stats;                               // all rows: [T][chunks]; row by row: [2][B][chunks], in turn
-  Place* places;                             // row by row: [most][B]
+  Place* places;                             // row by row: [levels][B]
   End* ends;                                 // drawn: [B], and max(p - q, 0) summed by chunks [B][chunks]
   double* rest;
 };
@@ -96,8 +96,9 @@ __device__ __forceinline__ float logit_at(const E* row, int v) {
 // 2^((x - top) / temperature in base 2), relative error 4e-11; 0 for -inf and NaN.
 // The nearest whole number by an addition that rounds there, 2^f of the rest by a
 // minimax polynomial. 64-bit multiply-adds run at the rate of 32-bit ones, and a
-// sum of many rows is bound by these instructions, 18 a value: 64 trees of 60 rows
-// over 128000 tokens, every row, take 93% of the vector unit's cycles.
+// sum of many rows is bound by the instructions, 19 a value, 15 of them here: 64
+// trees of 60 rows over 128000 tokens, every row, take 93% of the vector unit's
+// cycles.
 __device__ __forceinline__ double weight_of(double x, double top, const Seq& q) {
   constexpr double kRound = 6755399441055744.0;            // 1.5 x 2^52
   const double d = fmax(x - top, q.lowest), z = fma(d, q.inv_t, kRound), f = fma(d, q.inv_t, kRound - z);
@@ -753,11 +754,12 @@ __global__ void __launch_bounds__(kPickThreads) draft_pick_kernel(Verify<E> a) {
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 int chunks_of(int V) { return (V + 7 + kChunk - 1) / kChunk; }
 
-// Every row at once takes what all of the T rows' values take (1.5 values a ns) and
-// two or three launches; row by row only the rows of the branches are read, a launch
-// for each of them that a branch may have (5 us). 64 trees of 60 rows, 128000 tokens,
-// branches of up to 10 rows: 337 us at once, 60 row by row; 8 of 26 rows, 50021
-// tokens: 25 and 41.
+// Every row at once reads all of the T rows (1.5 values a ns) in two or three
+// launches; row by row only the rows of the branches are read, at most about three
+// of a sequence's, in a launch (5 us) for each row that a branch may have. Rows of
+// 128000 tokens, trees of 60 rows, branches of up to 11: 64 sequences 58 us row by
+// row, 337 at once; 8 of them 44 and 59, 4 of them 40 and 36. 64 of 26 rows, 50021
+// tokens, branches of up to 10: 56 and 73; 32 of them 49 and 46.
 bool row_by_row(int64_t B, int64_t T, int64_t V, int64_t levels) { return (T - 3 * B) * V > levels * 4000000; }
 struct Way {
   int levels;                                // 0: at once
