@@ -744,22 +744,47 @@ __global__ void __launch_bounds__(256, 1)
       issue_pages(1);
       issue(slot, 0);
     }
+    if constexpr (!TREE) {
 #pragma unroll
-    for (int h = 0; h < QT; ++h) {
-      const int m = m0 + min(16 * h + c16, M - 1), mr = m / H, mh = m - mr * H;   // past the end: the last one again
-      p_row[h] = sr.pos0 + mr;
-      const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + grp * 16;
+      for (int h = 0; h < QT; ++h) {
+        const int m = m0 + min(16 * h + c16, M - 1), mr = m / H, mh = m - mr * H;   // past the end: the last one again
+        p_row[h] = sr.pos0 + mr;
+        const uint8_t* qp = reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs) + grp * 16;
 #pragma unroll
-      for (int s = 0; s < kNKs; ++s) qf[h][s] = ld_bf16x8(qp + s * 64);
-    }
-    if constexpr (TREE) {
+        for (int s = 0; s < kNKs; ++s) qf[h][s] = ld_bf16x8(qp + s * 64);
+      }
+    } else {
+      // Every wave needs all queries: eight a wave go to the buffer of round 1 as rows
+      // do, and come from there as key fragments do. (Gathered by each wave, 147 KiB
+      // through a CU's 27 bytes a cycle: 5.3K of the 15K cycles to start.)
+      constexpr uint32_t kQBuf = kNTile;
+      auto query_at = [&](int x) -> const uint8_t* {       // past the end: the last one again
+        const int m = m0 + min(x, M - 1), mr = m / H, mh = m - mr * H;
+        return reinterpret_cast<const uint8_t*>(q + (int64_t)(sr.first + mr) * q_rs + (int64_t)mh * q_hs);
+      };
+      if (wave * 8 < 16 * QT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lds_load_row(lds0 + kQBuf + (wave * 8 + j) * kVPitch, lane * 16, query_at(wave * 8 + j));
+        const int k = lane >> 3;
+        lds_load_lanes(lds0 + kQBuf + kNTail + wave * 1024, query_at(wave * 8 + k) + kPagedVal * 2 + (((lane & 7) ^ k) * 16));
+      }
       if ((int)threadIdx.x <= r_hi) s_parent[threadIdx.x] = parent_of(up, threadIdx.x);
       __syncthreads();
       if (lane < kNM / 4) {                        // this wave's eight queries
         const int x = wave * (kNM / 4) + lane;
         tree_line(s_line + x * kLinePitch, s_parent, (m0 + min(x, M - 1)) / H, sr.pos0, window, n_sink);
       }
+      __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's queries and rows
       __syncthreads();
+#pragma unroll
+      for (int h = 0; h < QT; ++h) {
+        const int x = 16 * h + c16;
+#pragma unroll
+        for (int s = 0; s < kNKs; ++s)
+          qf[h][s] = ld_bf16x8(tiles + kQBuf + (s < 16 ? x * kVPitch + grp * 16 + s * 64
+                                                       : kNTail + x * 128 + (((4 * (s - 16) + grp) ^ (x & 7)) * 16)));
+      }
+      // every wave has read them before round 0's first barrier, behind which their buffer is written again
     }
     for (int i = 0; i < rounds; ++i) {
       __builtin_amdgcn_s_waitcnt(0x70 | 0xF00);   // vmcnt(0): this wave's rows of round i, the entries of round i + 1
