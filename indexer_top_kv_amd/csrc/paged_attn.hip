@@ -1048,10 +1048,10 @@ int64_t tiles_of(int B, int T, int H, int64_t per_seq, int per) {
 // Trees. Tiles of 32 queries by the narrow kernel also for more queries, where
 // these and the tokens are so few that the start and the partials of a 128-query
 // tile cost more than its rows save: up to kSmall rounds of 64 tokens for each CU.
-// One sequence, 8 rows of 16 heads over 4000 tokens (1 round) 27 us, by the wide
-// kernel 34; 60 rows (7.5) 37 and 43; 16 trees of up to 27 rows, 32 heads, window
-// 1024 (12) 59 and 45.
-constexpr int kSmall = 8;
+// 16 heads over 4000 tokens: one sequence of 8 rows (1 round) 24 us, by the wide
+// kernel 34; 8 sequences of 12 rows (11.8) 42 and 44, of 16 rows (15.8) 49 and 48.
+// A window of 1024, 16 sequences of 10 rows of 32 heads (13.1) 48 and 42.
+constexpr int kSmall = 12;
 struct Split {
   bool narrow;        // at most 32 queries a tile
   bool planned;
