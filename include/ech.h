@@ -638,7 +638,7 @@ int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* seq_len, in
  *  kept   [B, most] int32: the branch's rows, ascending (0 first), then -1.
  *  n_kept [B] int32: how many; next_token [B] int32.
  *  max_rows >= every row0[b+1] - row0[b], at most 256; of a sequence with more
- *  only the first max_rows rows are looked at. V <= 2^24, T ceil((V + 7) / 2048)
+ *  only the first max_rows rows are looked at. V <= 2^24, T ceil((V + 7) / 1024)
  *  < 2^31 - 4.
  *  ws     ech_draft_verify_ws_bytes(...) bytes, 256-byte aligned, uninitialised
  *         OK. Calls that share it must be ordered. May be captured.

@@ -23,8 +23,14 @@ namespace {
 
 constexpr int kDraftMost = 256;              // rows of a tree
 constexpr int kGroups = kDraftMost / 64;     // of a tree's rows, one a lane
-constexpr int kChunk = 2048;                 // tokens that a wave sums: 32 a lane
-constexpr int kPerLane = kChunk / 64;
+// Tokens that a wave sums, in four loads of 16 bytes a lane: 2048 of bf16, 1024 of
+// fp32 (2048 of these take 100 registers and leave four waves for a SIMD: 64 trees of
+// 60 rows, 60000 tokens 62 us, with 1024 57; 11 of 34 rows, 67320 tokens 39.4, 38.3).
+template <typename E>
+constexpr int kChunk = 4 * 64 * 16 / (int)sizeof(E);
+constexpr int kLeast = kChunk<float>;
+template <typename E>
+constexpr int kPerLane = kChunk<E> / 64;
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
@@ -129,7 +135,7 @@ __device__ __forceinline__ int lead_of(const E* row) {
 }
 template <typename E>
 __device__ __forceinline__ int chunks_in(const Verify<E>& a, const E* row) {
-  return (a.V + lead_of(row) + kChunk - 1) / kChunk;
+  return (a.V + lead_of(row) + kChunk<E> - 1) / kChunk<E>;
 }
 
 // Over the wave's lanes in the vector unit: lanes take what is `CTRL` before them,
@@ -178,13 +184,13 @@ __device__ __forceinline__ int lanes_least(int x) {
   return __builtin_amdgcn_readlane(x, 63);
 }
 
-// 2048 values of a row from value e0, a multiple of 16 bytes, on: lane l holds, in
+// A chunk of a row from value e0, a multiple of 16 bytes, on: lane l holds, in
 // pieces of 16 bytes, the values e0 + (64 k + l) kPiece .. of piece k. They stay
-// as they are in memory (16 registers of bf16, which leaves room for more waves);
-// what lies outside of the row is -inf.
+// as they are in memory (16 registers, which leaves room for more waves); what
+// lies outside of the row is -inf.
 template <typename E>
 struct Chunk {
-  static constexpr int kPiece = 16 / sizeof(E), kPieces = kPerLane / kPiece;
+  static constexpr int kPiece = 16 / sizeof(E), kPieces = kPerLane<E> / kPiece;
   u32x4_t raw[kPieces];
   // the j-th value of this lane, and the token it is of
   __device__ __forceinline__ float value(int j) const {
@@ -196,7 +202,7 @@ struct Chunk {
   __device__ __forceinline__ void mend(uint32_t out) {
     constexpr uint32_t kAll = sizeof(E) == 4 ? 0xffffffffu : 0xffffu;
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
+    for (int j = 0; j < kPerLane<E>; ++j) {
       const int sh = sizeof(E) == 2 && (j & 1) ? 16 : 0;
       const uint32_t w = raw[j / kPiece][j % kPiece * (int)sizeof(E) / 4], v = w >> sh & kAll;
       const uint32_t inf = sizeof(E) == 4 ? 0x7f800000u : 0x7f80u, low = inf | (kAll ^ kAll >> 1);
@@ -206,7 +212,7 @@ struct Chunk {
   }
   static __device__ __forceinline__ int token(int e0, int j, int lane) { return e0 + (j / kPiece * 64 + lane) * kPiece + j % kPiece; }
   __device__ __forceinline__ void load(const E* row, int V, int e0, int lane) {
-    const bool inside = e0 >= 0 && e0 + kChunk <= V;
+    const bool inside = e0 >= 0 && e0 + kChunk<E> <= V;
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       const int e = e0 + (k * 64 + lane) * kPiece;
@@ -235,7 +241,7 @@ __device__ __forceinline__ void sum_chunk(const Verify<E>& a, const Seq& q, int 
   using C = Chunk<E>;
   float top = -__builtin_inff();
 #pragma unroll
-  for (int j = 0; j < kPerLane; ++j) top = fmaxf(top, x.value(j));   // passes over NaN
+  for (int j = 0; j < kPerLane<E>; ++j) top = fmaxf(top, x.value(j));   // passes over NaN
   top = lanes_top(top);
   const bool infinite = top == __builtin_inff();
   if (infinite) top = __uint_as_float(kLargest<E>);
@@ -244,7 +250,7 @@ __device__ __forceinline__ void sum_chunk(const Verify<E>& a, const Seq& q, int 
   if (q.greedy) {
     int at = INT32_MAX;
 #pragma unroll
-    for (int j = kPerLane - 1; j >= 0; --j)
+    for (int j = kPerLane<E> - 1; j >= 0; --j)
       if (x.value(j) >= top) at = C::token(e0, j, lane);
     best = top == -__builtin_inff() ? -1 : lanes_least(at);
   } else {
@@ -253,7 +259,7 @@ __device__ __forceinline__ void sum_chunk(const Verify<E>& a, const Seq& q, int 
     for (int j0 = first; j0 < end; j0 += 64) {
       const int j = min(j0 + lane, end - 1), t = a.tokens[q.r0 + j];
       const int tok = j0 + lane < end && (!a.parent || parent_at(a.parent, q.r0, j) == i) ? t : -1;
-      unsigned long long hit = __ballot(tok >= max(e0, 0) && tok < min(e0 + kChunk, a.V));
+      unsigned long long hit = __ballot(tok >= max(e0, 0) && tok < min(e0 + kChunk<E>, a.V));
       while (hit != 0ull) {
         const int rel = __builtin_amdgcn_readlane(tok, __builtin_ctzll(hit)) - e0;
         hit &= hit - 1;
@@ -266,7 +272,7 @@ __device__ __forceinline__ void sum_chunk(const Verify<E>& a, const Seq& q, int 
     for (int k = 0; k < C::kPieces; ++k) asm volatile("" : "+v"(x.raw[k]));   // unpacked again, not kept unpacked
     if (top > -__builtin_inff()) {
 #pragma unroll
-      for (int j = 0; j < kPerLane; ++j) sum += weight_of(x.value(j), top, q);
+      for (int j = 0; j < kPerLane<E>; ++j) sum += weight_of(x.value(j), top, q);
     }
     sum = lanes_sum(sum);
   }
@@ -302,14 +308,18 @@ __device__ __forceinline__ Joined join(const Verify<E>& a, const Seq& q, const E
   return r;
 }
 
-// The child that is accepted at row i of a tree or chain, or -1. By one wave. `end`:
-// a chain's largest logit there and its weight with the child's too.
+// The child that is accepted at row i of a tree or chain, or -1. By one wave. `end`
+// (in LDS, or NULL): a chain's largest logit there and its weight with the child's
+// too, or greedy its first token.
 template <typename E>
 __device__ __forceinline__ int decide(const Verify<E>& a, const Seq& q, int i, const Stat* st, int lane, Joined* end = nullptr) {
   const E* row = a.logits + (int64_t)(q.r0 + i) * a.ld;
   if (!a.parent) {
     if (i + 1 >= q.n) {
-      if (end) *end = join(a, q, row, st, lane);
+      if (end) {
+        const Joined r = join(a, q, row, st, lane);
+        if (lane == 0) *end = r;
+      }
       return -1;
     }
     const int tok = a.tokens[q.r0 + i + 1];
@@ -318,10 +328,9 @@ __device__ __forceinline__ int decide(const Verify<E>& a, const Seq& q, int i, c
     const double u = unit_of(a.u[q.r0 + i + 1]);
     const double drawn = a.draft && known ? (double)draft_of(a.draft[(int64_t)(q.r0 + i) * a.draft_ld + tok]) : 1.0;
     const Joined r = join(a, q, row, st, lane);
-    if (end) *end = r;
+    const double w = q.greedy ? 0.0 : weight_of(x, r.top, q);
+    if (end && lane == 0) *end = Joined{r.top, r.best, r.base + w};
     if (q.greedy) return known && tok == r.best ? i + 1 : -1;
-    const double w = weight_of(x, r.top, q);
-    if (end) end->base = r.base + w;
     return w > 0.0 && u * (r.base + w) * drawn < w ? i + 1 : -1;
   }
   // lane l holds rows l, 64 + l, ..: those that are children of i, their tokens and weights
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(256) draft_stats_kernel(Verify<E> a) {
   if (id >= (int64_t)a.T * a.chunks) return;               // T chunks < 2^31
   const int t = (int)((uint32_t)id / (uint32_t)a.chunks), chunk = (int)((uint32_t)id - (uint32_t)t * (uint32_t)a.chunks);
   const E* row = a.logits + (int64_t)t * a.ld;
-  const int e0 = chunk * kChunk - lead_of(row);            // the chunk's first value (may lie before the row)
+  const int e0 = chunk * kChunk<E> - lead_of(row);            // the chunk's first value (may lie before the row)
   if (e0 >= a.V) return;                                   // a row that begins early needs one chunk less
   Chunk<E> x;
   x.load(row, a.V, e0, lane);                              // on its way while the row's sequence is found
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(256) draft_level_kernel(Verify<E> a, int level
     if (!p.ended) a.kept[(int64_t)b * a.most + level] = p.at;
   }
   const E* row = a.logits + (int64_t)(q.r0 + p.at) * a.ld;
-  const int e0 = chunk * kChunk - lead_of(row);
+  const int e0 = chunk * kChunk<E> - lead_of(row);
   if (p.ended || e0 >= a.V) return;
   Chunk<E> x;
   x.load(row, a.V, e0, lane);
@@ -461,12 +470,9 @@ __device__ __forceinline__ Place branch(const Verify<E>& a, const Seq& q, int b,
     if (write && threadIdx.x == 0) kb[0] = 0;
     for (int first = 0;; first = p.at / WAVES * WAVES) {
       if (first + wave < q.n) {
-        Joined end;
-        const int next = decide(a, q, first + wave, a.stats + (int64_t)(q.r0 + first + wave) * a.chunks, lane, s_end ? &end : nullptr);
-        if (lane == 0) {
-          s_next[wave] = next;
-          if (s_end) s_end[wave] = end;
-        }
+        const int next = decide(a, q, first + wave, a.stats + (int64_t)(q.r0 + first + wave) * a.chunks, lane,
+                                s_end ? s_end + wave : nullptr);
+        if (lane == 0) s_next[wave] = next;
       }
       __syncthreads();
       p.spare = first;
@@ -508,7 +514,7 @@ struct PickShared {
 // The first token up to which more than u of a row's weight lies (-1: nothing
 // weighs). chunk_sum(c) and weight(token) say the weights. Every wave finds the
 // chunk alike; its tokens are four a thread. Call from all threads.
-template <typename C, typename W>
+template <typename E, typename C, typename W>
 __device__ __forceinline__ int pick(int chunks, int lead, int V, double u, const C& chunk_sum, const W& weight, PickShared& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const double x0 = lane < chunks ? chunk_sum(lane) : 0.0, scan0 = lanes_scan(x0);
@@ -530,8 +536,8 @@ __device__ __forceinline__ int pick(int chunks, int lead, int V, double u, const
     base += lane_value(incl, 63);
   }
   const double aim_in = aim - before;
-  constexpr int kEach = kChunk / kPickThreads;
-  const int e0 = chunk * kChunk - lead + tid * kEach;
+  constexpr int kEach = kChunk<E> / kPickThreads;
+  const int e0 = chunk * kChunk<E> - lead + tid * kEach;
   double w[kEach], mine = 0.0;
   int last = -1;
 #pragma unroll
@@ -614,7 +620,7 @@ __device__ __forceinline__ int pick_row(const Verify<E>& a, const Seq& q, int b,
       }
     }
   }
-  return pick(
+  return pick<E>(
       chunks, lead, a.V, unit_of(a.u[q.r0]),
       [&](int c) {
         const Stat s = st[c];
@@ -624,7 +630,7 @@ __device__ __forceinline__ int pick_row(const Verify<E>& a, const Seq& q, int b,
           for (int g = 0; g < kGroups; ++g)
             for (unsigned long long left = kids[g]; left != 0ull; left &= left - 1) {
               const int l = __builtin_ctzll(left);
-              if ((__builtin_amdgcn_readlane(tok[g], l) + lead) / kChunk == c) x += lane_value(w[g], l);
+              if ((__builtin_amdgcn_readlane(tok[g], l) + lead) / kChunk<E> == c) x += lane_value(w[g], l);
             }
         }
         return x;
@@ -702,7 +708,7 @@ __global__ void __launch_bounds__(kRestWaves * 64) draft_rest_kernel(Verify<E> a
   const bool tried = p.count < a.most && p.at + 1 < q.n;
   const double inv = 1.0 / r.base;
   if (first && threadIdx.x == 0) a.ends[b] = End{q.r0 + p.at, tried, r.top, 0, inv};
-  const int chunk = blockIdx.x * kRestWaves + wave, e0 = chunk * kChunk - lead_of(row);
+  const int chunk = blockIdx.x * kRestWaves + wave, e0 = chunk * kChunk<E> - lead_of(row);
   if (!tried || e0 >= a.V) return;
   constexpr int kPiece = Chunk<E>::kPiece;
   Chunk<E> x;
@@ -710,16 +716,16 @@ __global__ void __launch_bounds__(kRestWaves * 64) draft_rest_kernel(Verify<E> a
   if (r.top == __uint_as_float(kLargest<E>)) x.mend(0u);
   const float* draft = a.draft + (int64_t)(q.r0 + p.at) * a.draft_ld;
   double sum = 0.0;
-  if (e0 >= 0 && e0 + kChunk <= a.V && (reinterpret_cast<uintptr_t>(draft + e0) & 15u) == 0) {
+  if (e0 >= 0 && e0 + kChunk<E> <= a.V && (reinterpret_cast<uintptr_t>(draft + e0) & 15u) == 0) {
 #pragma unroll
-    for (int k = 0; k < kPerLane / 4; ++k) {
+    for (int k = 0; k < kPerLane<E> / 4; ++k) {
       const f32x4_t d = *reinterpret_cast<const f32x4_t*>(draft + e0 + ((k * 4 / kPiece) * 64 + lane) * kPiece + k * 4 % kPiece);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum += rest_of<E>(q, x.value(k * 4 + j), d[j], r.top, inv);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kPerLane; ++j) {
+    for (int j = 0; j < kPerLane<E>; ++j) {
       const int v = Chunk<E>::token(e0, j, lane);
       if (v >= 0 && v < a.V) sum += rest_of<E>(q, x.value(j), draft[v], r.top, inv);
     }
@@ -740,7 +746,7 @@ __global__ void __launch_bounds__(kPickThreads) draft_pick_kernel(Verify<E> a) {
   const float* draft = a.draft + (int64_t)e.row * a.draft_ld;
   int got = -1;
   if (e.tried)
-    got = pick(
+    got = pick<E>(
         chunks_in(a, row), lead_of(row), a.V, unit_of(a.u[q.r0]), [&](int c) { return a.rest[(int64_t)b * a.chunks + c]; },
         [&](int v) { return rest_of<E>(q, logit_at(row, v), draft[v], e.top, e.inv); }, sh);
   if (got < 0) {                                           // nothing was tried, or q is nowhere below p
@@ -752,9 +758,9 @@ __global__ void __launch_bounds__(kPickThreads) draft_pick_kernel(Verify<E> a) {
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
-int chunks_of(int V) { return (V + 7 + kChunk - 1) / kChunk; }
+int chunks_of(int V, int chunk = kLeast) { return (V + 7 + chunk - 1) / chunk; }
 
-// Every row at once reads all of the T rows (1.5 values a ns) in two or three
+// Every row at once reads all of the T rows (1500 values a ns) in two or three
 // launches; row by row only the rows of the branches are read, at most about three
 // of a sequence's, in a launch (5 us) for each row that a branch may have. Rows of
 // 128000 tokens, trees of 60 rows, branches of up to 11: 64 sequences 58 us row by
@@ -836,7 +842,7 @@ extern "C" int ech_draft_verify(const void* logits, int ltype, int64_t ld, int V
   char* wp = static_cast<char*>(ws);
   auto call = [&](auto* x) {
     using E = std::remove_const_t<std::remove_pointer_t<decltype(x)>>;
-    const Verify<E> a{x, ld, V, chunks_of(V), tokens, parent, draft, draft_ld, u, temperature, row0, B, T, max_rows, most, kept,
+    const Verify<E> a{x, ld, V, chunks_of(V, kChunk<E>), tokens, parent, draft, draft_ld, u, temperature, row0, B, T, max_rows, most, kept,
                       n_kept, next_token, reinterpret_cast<Stat*>(wp), reinterpret_cast<Place*>(wp + w.places),
                       reinterpret_cast<End*>(wp + w.ends), reinterpret_cast<double*>(wp + w.rest)};
     return w.levels ? verify_call<E, true>(a, w.levels, s) : verify_call<E, false>(a, 0, s);
