@@ -1055,7 +1055,8 @@ class PagedLayer:
         self._accept_host(counts, *self._accept_launch(kept, n_kept, stream))
 
     def fork(self, src: int, dst) -> None:
-        """The empty sequences dst (a number or several) go on from src's tokens."""
+        """The empty sequences dst (a number or several) go on from src's tokens:
+        those that launches before it wrote (not between a place and its launch)."""
         self._not_captured()
         self._no_drafts()
         dst = [int(b) for b in np.atleast_1d(dst)]

@@ -87,6 +87,19 @@ SHAPES = [
     ([128], [700], 2, 64, 31, 130, 'random'),
     ([256], [300], 1, 24, 90, 2, 'chain'),
     ([6], [2000], 128, 64, 4096, 4, 'random'),                  # a window longer than the sequence
+    # tiles of 128 queries: more than 256 of 32
+    ([64, 60, 0, 64, 90], [100, 3, 9, 31, 200], 64, 16, 0, 0, 'random'),
+    ([70, 64, 64], [500, 0, 64], 63, 24, 0, 0, 'forest'),
+    ([256], [333], 40, 64, 0, 0, 'chain'),
+    ([256], [31], 33, 7, 0, 0, 'binary'),
+    ([100, 100], [700, 30], 64, 16, 90, 5, 'random'),
+    ([250], [40], 48, 16, 30, 60, 'chain'),                     # first tokens inside the tree
+    ([128, 80], [400, 64], 48, 24, 1, 0, 'random'),
+    ([256, 200], [20, 150], 128, 16, 0, 0, 'random'),           # and more of these than CUs
+    ([256, 200], [300, 50], 100, 64, 40, 3, 'forest'),
+    # of 32, as many rounds as they are used for, and more
+    ([16, 9, 16, 16], [3000, 3800, 3500, 2900], 16, 64, 0, 0, 'random'),
+    ([16, 16, 16, 16, 16, 16, 16, 16], [6400] * 8, 16, 64, 0, 0, 'star'),
 ]
 
 
@@ -111,14 +124,14 @@ def test_rows_of_no_sequence_and_parents_that_are_none():
     """Rows before the first and behind the last sequence stay as they were;
     parents that do not precede their row count as none."""
     need_gpu()
-    for ctx, H in ((40, 16), (1500, 16), (5, 1)):
-        c = TreeCase([9, 4], [ctx, 3], H, 16, seed=3, lead=2, tail=3)
+    for ctx, H, more in ((40, 16, 0), (1500, 16, 0), (5, 1, 0), (50, 128, 80)):
+        c = TreeCase([9, 4 + more], [ctx, 3], H, 16, seed=3, lead=2, tail=3)
         bad = c.parent.copy()
         bad[2:15] = [0, 1, 2, -5, 4, 2 ** 31 - 1, -2 ** 31, 300, 3, 0, 0, 2, 9]
         check_attn(c.attn(parent=bad), c.ref(parent=bad), c.max_len, f'{ctx}')
 
 
-@pytest.mark.parametrize('rows,H', [([6], 4), ([40], 16)])
+@pytest.mark.parametrize('rows,H', [([6], 4), ([40], 16), ([150], 64)])
 def test_values_that_are_not_finite_outside_of_a_line(rows, H):
     """Infinities and NaN in rows of other branches, and in rows without a page,
     stay out of a row's output; in its own line they reach it."""
@@ -138,11 +151,12 @@ def test_values_that_are_not_finite_outside_of_a_line(rows, H):
     assert not np.isfinite(out[hit]).all(axis=(1, 2)).any()
 
 
-def test_absent_pages_and_short_lengths():
+@pytest.mark.parametrize('rows,H', [([20, 12], 16), ([100, 60], 60)])
+def test_absent_pages_and_short_lengths(rows, H):
     """Nodes whose page is missing count as absent; a length below the number
     of rows leaves rows without a slot."""
     need_gpu()
-    c = TreeCase([20, 12], [30, 40], 16, 8, seed=6)
+    c = TreeCase(rows, [30, 40], H, 8, seed=6)
     table = c.table.copy()
     table[0, 4], table[0, 5], table[1, 2] = -1, c.n_slots, 2 ** 31 - 1
     check_attn(c.attn(table=dev(table)), c.ref(table=table), c.max_len)
@@ -150,7 +164,7 @@ def test_absent_pages_and_short_lengths():
     check_attn(c.attn(), c.ref(), c.max_len)
 
 
-@pytest.mark.parametrize('rows,H', [([5], 4), ([9], 16), ([40], 128)])
+@pytest.mark.parametrize('rows,H', [([5], 4), ([9], 16), ([100], 128)])
 def test_pages_behind_4_gib_of_pool(rows, H):
     """The cached rows and the tree at the end of a pool of more than 2^32 bytes."""
     need_gpu()
@@ -186,7 +200,7 @@ def test_two_calls_at_once():
 def test_strided_queries():
     """Rows and heads of a wider tensor."""
     need_gpu()
-    for rows, H in (([12], 16), ([3], 8), ([40], 24)):
+    for rows, H in (([12], 16), ([3], 8), ([200], 48)):
         c = TreeCase(rows, [100], H, 16, seed=13)
         wide = torch.full((c.T, H + 2, 640), float('nan'), dtype=torch.bfloat16, device='cuda')
         wide[:, 1:-1, 8:584] = dev(c.q).view(torch.bfloat16)

@@ -234,3 +234,18 @@ def test_calls_on_several_streams():
     assert got[0][0] == got[1][0]
     for x, y in zip(got[0][1], got[1][1]):
         np.testing.assert_array_equal(x, y)
+
+
+def test_a_step_without_rows():
+    """No sequence brings a row: nothing changes, nothing is kept."""
+    need_gpu()
+    layer = PagedLayer(2, 16, n_pages=20, max_len=100, max_rows=40, page_size=16)
+    x = dev(some(np.random.default_rng(1), 5, 576)).view(torch.bfloat16)
+    layer.step(torch.zeros((5, 16, 576), dtype=torch.bfloat16, device='cuda'), x, [5, 0])
+    none = dict(dtype=torch.int32, device='cuda')
+    out, lse = layer.draft(torch.zeros((0, 16, 576), dtype=torch.bfloat16, device='cuda'), x[:0], torch.zeros(0, **none), [0, 0])
+    assert out.shape == (0, 16, 512)
+    got = DraftStep([layer], 3).finish(torch.zeros((0, 50), device='cuda'), torch.zeros(0, **none), torch.zeros(0, device='cuda'),
+                                       parent=torch.zeros(0, **none))
+    assert got.counts.tolist() == [0, 0] and got.next_token.tolist() == [-1, -1] and (got.kept == -1).all()
+    assert layer.lens.tolist() == [5, 0] and host(layer.seq_len).tolist() == [5, 0]
