@@ -159,11 +159,11 @@ __device__ __forceinline__ void store_columns(uint16_t* out, const uint8_t* t, i
 __device__ __forceinline__ f32x4_t* part_at(float* part, int wg, int row_tiles, int r, int wave) {
   return reinterpret_cast<f32x4_t*>(part) + (((int64_t)wg * row_tiles + r) * 4 + wave) * 1024;
 }
-__device__ __forceinline__ void store_part(float* part, int wg, int row_tiles, const f32x16_t (&acc)[4][4], int wave,
-                                           int lane) {
+__device__ __forceinline__ void store_part(float* part, int wg, int row_tiles, int have, const f32x16_t (&acc)[4][4],
+                                           int wave, int lane) {   // `have` of them hold queries
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    if (r < row_tiles) {
+    if (r < have) {
       f32x4_t* o = part_at(part, wg, row_tiles, r, wave) + lane;
 #pragma unroll
       for (int ct = 0; ct < 4; ++ct)
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(256, 1)
   if (eg == 0) s_l[wave * 32 + ecol] = l;
   if (nsp > 1) {
     if (eg == 0) my_ml[wave * 32 + ecol] = make_float2(mx, l);
-    store_part(part_o, wg, row_tiles, acc, wave, elane);
+    store_part(part_o, wg, row_tiles, TREE ? min(row_tiles, (M - m0 + 31) / 32) : row_tiles, acc, wave, elane);
     return;
   }
   __syncthreads();                   // every wave's sums; and every wave is done with the step buffers
