@@ -1122,7 +1122,8 @@ class DraftStep:
         self._out = torch.empty(n, dtype=torch.int32, device=self.device)
         self._host = torch.empty(n, dtype=torch.int32, pin_memory=self.device.type == 'cuda')
         self.kept, self.n_kept, self.next_token = self._split(self._out)
-        self._ws, self._last = None, None
+        # the buffers may be memory that this stream still uses
+        self._ws, self._last = None, torch.cuda.current_stream(self.device) if self.device.type == 'cuda' else None
 
     def _split(self, x: torch.Tensor):
         B = self.B
@@ -1139,15 +1140,15 @@ class DraftStep:
             raise ValueError(f'{first._placed} rows were placed, logits has shape {tuple(logits.shape)}')
         T, V = logits.shape
         s = torch.cuda.current_stream(self.device)
-        if self._last is not None and self._last != s:
+        if self._last != s:
             s.wait_stream(self._last)       # the buffers' last use
+            self._out.record_stream(s)
+            if self._ws is not None:
+                self._ws.record_stream(s)
+            self._last = s
         need = ech_draft_verify_ws_bytes(self.B, T, V, first._most, self.most)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        if self._last != s:
-            self._out.record_stream(s)
-            self._ws.record_stream(s)
-        self._last = s
         for x in self.layers:               # the first one's offsets are read: behind its own last call
             x._enter()
         ech_draft_verify(logits, tokens, first.row0, first._most, u, self.kept, self.n_kept, self.next_token, parent=parent,

@@ -15,6 +15,7 @@ from indexer_top_kv_amd.pipeline import DraftStep, PagedLayer
 from test_gpu_tree_attn import trees
 from test_gpu_paged import SCALE, check_attn
 from test_gpu_paged_layer import Model
+from test_gpu_paged_streams import WAIT
 
 pytestmark = pytest.mark.gpu
 V = 3000
@@ -249,3 +250,28 @@ def test_a_step_without_rows():
                                        parent=torch.zeros(0, **none))
     assert got.counts.tolist() == [0, 0] and got.next_token.tolist() == [-1, -1] and (got.kept == -1).all()
     assert layer.lens.tolist() == [5, 0] and host(layer.seq_len).tolist() == [5, 0]
+
+
+def test_buffers_made_on_a_stream_that_is_busy():
+    """A DraftStep's buffers may be memory that the stream it was made on still
+    writes: the first finish on another stream comes behind that."""
+    need_gpu()
+    layer = PagedLayer(1, 16, n_pages=20, max_len=100, max_rows=40, page_size=16)
+    r, side, ended = np.random.default_rng(3), torch.cuda.Stream(), torch.cuda.Event()
+    q, x = (dev(some(r, *s)).view(torch.bfloat16) for s in ((3, 16, 576), (3, 576)))
+    logits = torch.zeros((3, 50), device='cuda')
+    logits[:, 7] = 100.
+    tokens, u = torch.full((3,), 7, dtype=torch.int32, device='cuda'), torch.full((3,), 0.5, device='cuda')
+    layer.draft(q, x, None, [3])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        old = torch.empty(64, dtype=torch.int32, device='cuda')
+        torch.cuda._sleep(WAIT)
+        old.fill_(-7)
+        del old
+        ds = DraftStep([layer], 4)
+        ended.record()
+    got = ds.finish(logits, tokens, u)
+    assert ended.query()
+    assert got.counts.tolist() == [3] and got.kept.tolist() == [[0, 1, 2, -1]] and got.next_token.tolist() == [7]
+    np.testing.assert_array_equal(rows_of(layer, 0), host(x.view(torch.int16)).view(np.uint16))
