@@ -1045,13 +1045,17 @@ class PagedLayer:
     def accept(self, kept: torch.Tensor, n_kept: torch.Tensor, counts, stream=None) -> None:
         """The placed drafts' accepted rows stay, the others leave the cache: kept
         [B, most], n_kept [B] int32 on the device, as ech_draft_verify writes
-        them; counts [B]: n_kept's numbers, on the host."""
+        them; counts [B]: n_kept's numbers, on the host, at most `most` each."""
         if self._drafts is None:
             raise RuntimeError('no drafts are placed')
         self._not_captured(stream)
+        if kept.dim() != 2 or kept.shape[0] != self.B:
+            raise ValueError(f'kept: shape {tuple(kept.shape)}, expected ({self.B}, most)')
         counts = np.asarray(counts, np.int64)
-        if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > self._drafts):
-            raise ValueError(f'counts must be {self.B} numbers from 0 to the rows placed')
+        # the device cuts n_kept at both bounds: beyond them its lengths are not the host's
+        if counts.shape != (self.B,) or np.any(counts < 0) or np.any(counts > np.minimum(self._drafts, kept.shape[1])):
+            raise ValueError(f'counts must be {self.B} numbers from 0 to the rows placed, and to the {kept.shape[1]} that '
+                             f'kept holds')
         self._accept_host(counts, *self._accept_launch(kept, n_kept, stream))
 
     def fork(self, src: int, dst) -> None:

@@ -225,3 +225,21 @@ def test_layer_refuses_what_drafts_do_not_allow():
             layer.fork(src, dst)
     layer.fork(0, [1, 2])
     assert layer.lens.tolist() == [20, 20, 20, 5] and layer.pages.more.sum() == 2
+
+
+def test_accept_refuses_counts_that_kept_does_not_hold():
+    """The device cuts n_kept at kept's width: a host that counts more would
+    have lengths with rows that never moved."""
+    from indexer_top_kv_amd.pipeline import PagedLayer
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    layer = PagedLayer(2, 4, n_pages=20, max_len=200, max_rows=30, page_size=16, device='cpu')
+    layer.place([20, 5])
+    layer.place([6, 3], drafts=True)
+    image = layer._image.copy()
+    for kept, counts in ((z(2, 2), [3, 0]), (z(2, 2), [0, 3]), (z(2, 1), [2, 1]), (z(2), [1, 1]), (z(1, 6), [1, 1])):
+        with pytest.raises(ValueError, match='kept|counts'):
+            layer.accept(kept, z(2), counts)
+        assert layer._drafts.tolist() == [6, 3] and layer.lens.tolist() == [26, 8]
+        np.testing.assert_array_equal(layer._image, image)
+    with pytest.raises(ValueError, match='GPU'):                # nothing wrong but that these are host tensors
+        layer.accept(z(2, 2), z(2), [2, 2])
