@@ -1115,7 +1115,11 @@ class DraftStep:
     what follows each row, the rows' tokens and random numbers (as in
     ech_draft_verify), and waits for the decision: the next step's tokens are
     the host's. The layers' rows move while it waits. `most`: rows that a branch
-    may keep (its depth + 1)."""
+    may keep (its depth + 1). Of a chain of more than 256 rows the first 256 are
+    looked at: a branch that has them all ends there, and the token that follows
+    is the target's."""
+
+    MOST = 256      # rows of a sequence that ech_draft_verify looks at
 
     def __init__(self, layers, most: int):
         self.layers = list(layers)
@@ -1143,6 +1147,11 @@ class DraftStep:
         if logits.dim() != 2 or logits.shape[0] < first._placed:
             raise ValueError(f'{first._placed} rows were placed, logits has shape {tuple(logits.shape)}')
         T, V = logits.shape
+        rows = min(first._most, self.MOST)
+        need = ech_draft_verify_ws_bytes(self.B, T, V, rows, self.most)
+        if need == 0:                       # before a layer or a buffer is touched
+            raise ValueError(f'{T} rows of {V} tokens cannot be verified: 1 to 2^24 tokens, and rows times ceil((tokens + 7) '
+                             f'/ 1024) below 2^31 - 4')
         s = torch.cuda.current_stream(self.device)
         if self._last != s:
             s.wait_stream(self._last)       # the buffers' last use
@@ -1150,12 +1159,11 @@ class DraftStep:
             if self._ws is not None:
                 self._ws.record_stream(s)
             self._last = s
-        need = ech_draft_verify_ws_bytes(self.B, T, V, first._most, self.most)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         for x in self.layers:               # the first one's offsets are read: behind its own last call
             x._enter()
-        ech_draft_verify(logits, tokens, first.row0, first._most, u, self.kept, self.n_kept, self.next_token, parent=parent,
+        ech_draft_verify(logits, tokens, first.row0, rows, u, self.kept, self.n_kept, self.next_token, parent=parent,
                          draft=draft, temperature=temperature, ws=self._ws)
         self._host.copy_(self._out, non_blocking=True)
         done = torch.cuda.Event()

@@ -243,3 +243,21 @@ def test_accept_refuses_counts_that_kept_does_not_hold():
         np.testing.assert_array_equal(layer._image, image)
     with pytest.raises(ValueError, match='GPU'):                # nothing wrong but that these are host tensors
         layer.accept(z(2, 2), z(2), [2, 2])
+
+
+def test_finish_refuses_what_cannot_be_verified_before_anything_moves():
+    from indexer_top_kv_amd.pipeline import DraftStep, PagedLayer
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    layers = [PagedLayer(2, 4, n_pages=60, max_len=400, max_rows=300, page_size=16, device='cpu') for _ in range(2)]
+    for layer in layers:
+        layer.place([6, 3], drafts=True)
+    entered = []
+    for layer in layers:
+        layer._enter = lambda stream=None: entered.append(stream)
+    step = DraftStep(layers, 4)
+    for V in ((1 << 24) + 1, 0):
+        with pytest.raises(ValueError, match='2\\^24'):
+            step.finish(torch.zeros(1, 1).expand(9, V), z(9), torch.zeros(9))
+    with pytest.raises(ValueError, match='placed'):
+        step.finish(torch.zeros(8, 50), z(8), torch.zeros(8))
+    assert not entered and all(x._drafts.tolist() == [6, 3] for x in layers)

@@ -1,0 +1,58 @@
+"""Steps of drafts at the limits of their calls (DraftStep, PagedLayer.accept):
+what is kept, the rows and the next tokens have to be the oracle's."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_util import dev, host, need_gpu
+from indexer_top_kv_amd.pipeline import DraftStep, PagedLayer
+from test_gpu_tree_layer import rows_of, some
+
+pytestmark = pytest.mark.gpu
+
+
+def long_chains(drawn, seed=1):
+    """Chains that pass 256 rows: tokens, logits, draft, u and temperatures of three sequences."""
+    r = np.random.default_rng(seed)
+    counts, V = [300, 257, 4], 100
+    T, row0 = sum(counts), np.concatenate([[0], np.cumsum(counts)])
+    x = r.standard_normal((T, V)).astype(np.float32)
+    x[np.arange(T), r.integers(0, V, T)] += 30.0           # all but certain: whole chains pass
+    tokens = np.concatenate([[3], x.argmax(1)[:-1]]).astype(np.int32)
+    q = None
+    if drawn:
+        q = np.exp(0.9 * x.astype(np.float64))
+        q = (q / q.sum(1, keepdims=True)).astype(np.float32)
+    return counts, row0, x, tokens, q, r.random(T).astype(np.float32), np.array([0.0, 0.8, 1.0], np.float32)
+
+
+def decided(row0, counts, x, tokens, q, u, temps, most):
+    """The oracle over the first 256 rows of each sequence."""
+    kept, nxt, near = [], [], []
+    for b, n in enumerate(counts):
+        k, t, d = oracle.drafts.verify(x, tokens, [row0[b], row0[b] + min(n, 256)], u, most, None, q, temps[b:b + 1])
+        kept, nxt, near = kept + k, nxt + t, near + d
+    return kept, nxt, min(near)
+
+
+@pytest.mark.parametrize('drawn', [False, True])
+def test_chains_of_more_rows_than_are_verified(drawn):
+    need_gpu()
+    counts, row0, x, tokens, q, u, temps = long_chains(drawn)
+    r = np.random.default_rng(2)
+    layers = [PagedLayer(3, 4, n_pages=120, max_len=700, max_rows=300, page_size=16) for _ in range(2)]
+    news = [some(r, sum(counts), 576) for _ in layers]
+    ds = DraftStep(layers, 300)
+    for layer, new in zip(layers, news):
+        layer.draft(dev(some(r, sum(counts), 4, 576)).view(torch.bfloat16), dev(new).view(torch.bfloat16), None, counts)
+    got = ds.finish(dev(x), dev(tokens), dev(u), draft=None if q is None else dev(q), temperature=dev(temps))
+    kept, nxt, near = decided(row0, counts, x, tokens, q, u, temps, 300)
+    assert near > 1e-9 and [len(k) for k in kept] == [256, 256, 4]
+    assert got.counts.tolist() == [256, 256, 4] and got.next_token.tolist() == nxt
+    assert got.kept.tolist() == [k + [-1] * (300 - len(k)) for k in kept]
+    for layer, new in zip(layers, news):
+        assert layer.lens.tolist() == [256, 256, 4] and host(layer.seq_len).tolist() == [256, 256, 4]
+        for b in range(3):
+            np.testing.assert_array_equal(rows_of(layer, b), new[row0[b]:row0[b] + len(kept[b])])
+        layer.place([1, 1, 1])                              # the step is over
