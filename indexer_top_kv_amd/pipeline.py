@@ -1123,6 +1123,8 @@ class DraftStep:
 
     def __init__(self, layers, most: int):
         self.layers = list(layers)
+        if not self.layers or len({id(x) for x in self.layers}) < len(self.layers):
+            raise ValueError('layers: at least one, each once')
         self.B, self.most, self.device = self.layers[0].B, int(most), self.layers[0].device
         if any(x.B != self.B or x.device != self.device for x in self.layers) or self.most < 1:
             raise ValueError('the layers hold the same sequences on one device; most is at least 1')

@@ -261,3 +261,14 @@ def test_finish_refuses_what_cannot_be_verified_before_anything_moves():
     with pytest.raises(ValueError, match='placed'):
         step.finish(torch.zeros(8, 50), z(8), torch.zeros(8))
     assert not entered and all(x._drafts.tolist() == [6, 3] for x in layers)
+
+
+def test_a_step_names_each_layer_once():
+    """Twice in the list, a layer's rows would move twice."""
+    from indexer_top_kv_amd.pipeline import DraftStep, PagedLayer
+    mk = lambda B=2: PagedLayer(B, 4, n_pages=8, max_len=64, max_rows=16, page_size=16, device='cpu')  # noqa: E731
+    a, b = mk(), mk()
+    assert len(DraftStep([a, b], 3).layers) == 2
+    for layers in ([a, a], [a, b, a], [], [a, mk(3)]):
+        with pytest.raises(ValueError, match='layers'):
+            DraftStep(layers, 3)
