@@ -1134,6 +1134,13 @@ class DraftStep:
         self.kept, self.n_kept, self.next_token = self._split(self._out)
         # the buffers may be memory that this stream still uses
         self._ws, self._last = None, torch.cuda.current_stream(self.device) if self.device.type == 'cuda' else None
+        self._mark()
+
+    def _mark(self) -> None:
+        """The buffers' last use so far. A stream that is not torch's own may be
+        destroyed before the next step: it is marked now."""
+        s = self._last
+        self._done = s.record_event() if s is not None and s.cuda_stream and s.stream_id == s.cuda_stream else None
 
     def _split(self, x: torch.Tensor):
         B = self.B
@@ -1155,12 +1162,16 @@ class DraftStep:
             raise ValueError(f'{T} rows of {V} tokens cannot be verified: 1 to 2^24 tokens, and rows times ceil((tokens + 7) '
                              f'/ 1024) below 2^31 - 4')
         s = torch.cuda.current_stream(self.device)
-        if self._last != s:
-            s.wait_stream(self._last)       # the buffers' last use
+        if self._last != s:                 # behind the buffers' last use
+            if self._done is not None:
+                s.wait_event(self._done)
+            else:
+                s.wait_stream(self._last)
             self._out.record_stream(s)
             if self._ws is not None:
                 self._ws.record_stream(s)
             self._last = s
+        self._done = None
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.device)
         for x in self.layers:               # the first one's offsets are read: behind its own last call
@@ -1175,6 +1186,7 @@ class DraftStep:
         kept, counts, nxt = (x.numpy().copy() for x in self._split(self._host))
         for x, w in zip(self.layers, under_way):
             x._accept_host(counts.astype(np.int64), *w)
+        self._mark()
         return Accepted(counts, kept, nxt)
 
 

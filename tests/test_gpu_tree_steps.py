@@ -56,3 +56,41 @@ def test_chains_of_more_rows_than_are_verified(drawn):
         for b in range(3):
             np.testing.assert_array_equal(rows_of(layer, b), new[row0[b]:row0[b] + len(kept[b])])
         layer.place([1, 1, 1])                              # the step is over
+
+
+@pytest.mark.parametrize('made_on_it', [False, True])
+def test_a_foreign_stream_is_not_touched_after_its_step(made_on_it, monkeypatch):
+    """A stream that torch does not own may be gone when the next step comes:
+    nothing is recorded on it then, and the steps' results are those of one stream."""
+    need_gpu()
+    side = torch.cuda.Stream()
+    foreign = torch.cuda.ExternalStream(side.cuda_stream)
+    layer, r = PagedLayer(1, 16, n_pages=20, max_len=100, max_rows=40, page_size=16), np.random.default_rng(3)
+    logits = torch.zeros((3, 50), device='cuda')
+    logits[:, 7] = 100.
+    tokens, u = torch.full((3,), 7, dtype=torch.int32, device='cuda'), torch.full((3,), 0.5, device='cuda')
+    news = [some(r, 3, 576) for _ in range(3)]
+    torch.cuda.synchronize()
+
+    def step(ds, new):
+        layer.draft(dev(some(r, 3, 16, 576)).view(torch.bfloat16), dev(new).view(torch.bfloat16), None, [3])
+        if ds is not None:
+            got = ds.finish(logits, tokens, u)
+            assert got.counts.tolist() == [3] and got.kept.tolist() == [[0, 1, 2, -1]] and got.next_token.tolist() == [7]
+    with torch.cuda.stream(foreign if made_on_it else torch.cuda.current_stream()):
+        ds = DraftStep([layer], 4)
+    if not made_on_it:
+        with torch.cuda.stream(foreign):
+            step(ds, news[0])
+    named, record = [], torch.cuda.Stream.record_event
+
+    def seen(self, event=None):
+        named.append(self.cuda_stream)
+        return record(self, event)
+    monkeypatch.setattr(torch.cuda.Stream, 'record_event', seen)
+    for new in news[1:]:
+        step(ds, new)
+    assert side.cuda_stream not in named
+    monkeypatch.undo()
+    want = np.concatenate(news[1:] if made_on_it else news)
+    np.testing.assert_array_equal(rows_of(layer, 0), want)
