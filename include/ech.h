@@ -535,7 +535,8 @@ int ech_paged_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, c
  * may follow the cached tokens.
  *  parent [T] int32, device, -1 <= parent[row0[b] + i] < i; anything else counts
  *         as -1. Rows of no sequence are not read.
- *  max_rows at most 256 (ECH_EINVAL). Everything else as in ech_paged_attn.
+ *  max_rows at most 256 (ECH_EINVAL). Everything else as in ech_paged_attn, its
+ *  rounding too: the softmax weights enter the value product as bf16.
  */
 size_t ech_paged_tree_attn_ws_bytes(int B, int T, int H, int max_rows, int max_len, int window, int n_sink);
 int ech_paged_tree_attn(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* pool, int64_t n_slots,
@@ -620,7 +621,9 @@ int ech_paged_evict(const float* acc, int64_t acc_ld, const int32_t* seq_len, in
  * left of p (all of it where no child was tried).
  * A sequence at temperature 0 (or below, or NaN) is greedy: the child whose token
  * is the row's largest logit (the lowest such token) is accepted, and the next
- * token is that token; u and draft play no part. Sums are in 64 bits.
+ * token is that token; u and draft play no part. Sums are in 64 bits, of
+ * exponentials within 4e-11 of the formula's (relatively): a decision whose sides
+ * differ by less than 1e-10 of them may fall either way.
  *  logits [T, V], ltype ECH_LOGIT_BF16 or _F32, rows ld values apart (ld >= V).
  *         NaN counts as -inf, +inf as the type's largest finite value. A row whose
  *         logits are all -inf accepts nothing and has the next token -1.

@@ -102,8 +102,8 @@ __device__ __forceinline__ float logit_at(const E* row, int v) {
 // 2^((x - top) / temperature in base 2), relative error 4e-11; 0 for -inf and NaN.
 // The nearest whole number by an addition that rounds there, 2^f of the rest by a
 // minimax polynomial. 64-bit multiply-adds run at the rate of 32-bit ones, and a
-// sum of many rows is bound by the instructions, 19 a value, 15 of them here: 64
-// trees of 60 rows over 128000 tokens, every row, take 93% of the vector unit's
+// sum of many rows is bound by the instructions, 24 a value, 15 of them here: 3840
+// rows of 128000 bf16 logits, every row, take 436 us and 83% of the vector units'
 // cycles.
 __device__ __forceinline__ double weight_of(double x, double top, const Seq& q) {
   constexpr double kRound = 6755399441055744.0;            // 1.5 x 2^52

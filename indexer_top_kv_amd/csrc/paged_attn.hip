@@ -85,8 +85,11 @@ __device__ __forceinline__ void zero_not_finite(uint8_t* piece) {   // 16 bytes 
 // parent[i] < i, and row i, at the position c + (how many rows it descends from)
 // behind the c cached tokens, sees those and its own line. A tile's queries each
 // keep their line as bits in LDS, made once a workgroup by following parents
-// there; the steps that hold cached tokens alone do not read it, so a tree costs
-// what a chunk of as many rows does.
+// there, one after another (with a window twice); the steps that hold cached
+// tokens alone do not read it, so a tree of short lines costs what a chunk of as
+// many rows does, and one of long lines more. 256 rows of 16 heads over 4000
+// tokens: a chunk 66 us, a tree at random 63, one chain 79; with a window of 512:
+// 38, 32 and 65.
 constexpr int kTreeMost = 256;               // rows of a tree
 constexpr int kLineWords = kTreeMost / 32;
 constexpr int kLinePitch = kLineWords + 1;   // the position behind the bits; odd: banks
@@ -1050,7 +1053,10 @@ int64_t tiles_of(int B, int T, int H, int64_t per_seq, int per) {
 // tile cost more than its rows save: up to kSmall rounds of 64 tokens for each CU.
 // 16 heads over 4000 tokens: one sequence of 8 rows (1 round) 24 us, by the wide
 // kernel 34; 8 sequences of 12 rows (11.8) 42 and 44, of 16 rows (15.8) 49 and 48.
-// A window of 1024, 16 sequences of 10 rows of 32 heads (13.1) 48 and 42.
+// A window of 1024, 16 sequences of 10 rows of 32 heads (13.1) 48 and 42. (A
+// window's tokens count as the largest tree's, kTreeMost more than the window,
+// whatever max_rows is: a bound, which with short windows keeps some small trees
+// from the tiles of 32.)
 constexpr int kSmall = 12;
 struct Split {
   bool narrow;        // at most 32 queries a tile

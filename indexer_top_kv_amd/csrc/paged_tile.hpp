@@ -118,9 +118,11 @@ __device__ __forceinline__ int lanes_max(int x) {           // x >= 0
 // over 8K to 16K tokens 165 us, with this 153 us. A tile per CU, not split: 881
 // us, and 12 chunks of 77 rows at 16 heads over up to 5K tokens 282 us against
 // 73 us.) All tiles of a sequence
-// count as its last and longest. Every wave computes it alike, a sequence (of
-// each 64) per lane. ALL: one tile per sequence, over all of its tokens, new
-// rows or none.
+// count as its last and longest; a tree's as a chunk's, though with a window they
+// begin up to the tree's rows earlier: that costs balance alone, since a kernel
+// divides the steps that it runs. Every wave computes it alike, a sequence (of
+// each 64) per lane. ALL: one tile per sequence, over all of its tokens, new rows
+// or none.
 template <int PER, int STEP, bool ALL = false>
 __device__ __forceinline__ Work plan_work(const int32_t* row0, const int32_t* seq_len, const Pages& pg, int B, int T,
                                           int H, int max_rows, int max_len, int window, int n_sink, int wg) {
