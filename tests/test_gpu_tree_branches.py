@@ -115,3 +115,19 @@ def test_row_by_row_in_a_graph_with_a_shared_workspace():
         check()
         calls()
         check()
+
+
+@pytest.mark.parametrize('drawn', [False, True])
+def test_more_rows_than_the_bound(drawn):
+    """Only the first max_rows rows of a sequence are looked at."""
+    need_gpu()
+    c = Deep([300, 5, 280], 60001, None, drawn=drawn, seed=41, temps=[0.9, 0.0], most=4, peak=14.0)
+    for bound in (3, 256):
+        got = [oracle.drafts.verify(c.x, c.tokens, [r, r + min(n, bound)], c.u, 4, None, c.draft, c.temps[b:b + 1])
+               for b, (r, n) in enumerate(zip(c.row0, [300, 5, 280]))]
+        assert min(d for x in got for d in x[2]) > 1e-9
+        c.rows = [bound]                                   # of this, buffers and run take the largest
+        assert c.row_by_row()
+        kept, n_kept, nxt = c.run()
+        assert n_kept.tolist() == [len(x[0][0]) for x in got] and nxt.tolist() == [x[1][0] for x in got]
+        assert kept.tolist() == [x[0][0] + [-1] * (4 - len(x[0][0])) for x in got]

@@ -7,6 +7,9 @@ import torch
 import oracle
 from gpu_util import dev, host, need_gpu
 from indexer_top_kv_amd.pipeline import DraftStep, PagedLayer
+from test_gpu_paged import SCALE, check_attn
+from test_gpu_paged_layer import Model
+from test_gpu_tree_attn import trees
 from test_gpu_tree_layer import rows_of, some
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +97,43 @@ def test_a_foreign_stream_is_not_touched_after_its_step(made_on_it, monkeypatch)
     monkeypatch.undo()
     want = np.concatenate(news[1:] if made_on_it else news)
     np.testing.assert_array_equal(rows_of(layer, 0), want)
+
+
+@pytest.mark.parametrize('window,sink', [(0, 0), (20, 3)])
+def test_replayed_draft_launches_against_the_oracle(window, sink):
+    """A captured launch of trees, replayed for steps of other sizes, within the
+    bounds that test_gpu_paged.py derives; the steps' rows stay or leave between."""
+    need_gpu()
+    r, H, most = np.random.default_rng(11), 32, 24
+    layer, m = PagedLayer(2, H, n_pages=80, max_len=500, max_rows=most, page_size=16, window=window, n_sink=sink), Model(2)
+    first = some(r, 20, 576)
+    layer.step(dev(some(r, 20, H, 576)).view(torch.bfloat16), dev(first).view(torch.bfloat16), [13, 7])
+    m.rows = [first[:13], first[13:]]
+    q = torch.zeros((most, H, 576), dtype=torch.bfloat16, device='cuda')
+    x, parent = torch.zeros((most, 576), dtype=torch.bfloat16, device='cuda'), torch.full((most,), -1, dtype=torch.int32, device='cuda')
+    g = torch.cuda.CUDAGraph()
+    layer.place([0, 0], max_rows=most, drafts=True)
+    with torch.cuda.graph(g):
+        out, lse = layer.launch(q, x, parent=parent)
+    none = torch.zeros((2, 1), dtype=torch.int32, device='cuda')
+    layer.accept(none, none[:, 0].contiguous(), [0, 0])
+    for step, (counts, kind) in enumerate([([10, 10], 'random'), ([24, 0], 'chain'), ([1, 9], 'star'), ([0, 24], 'forest'), ([11, 13], 'binary')]):
+        T, row0 = sum(counts), np.concatenate([[0], np.cumsum(counts)])
+        qb, xb, par = some(r, T, H, 576), some(r, T, 576), trees(kind, counts, step)
+        for to, new in ((q, dev(qb).view(torch.bfloat16)), (x, dev(xb).view(torch.bfloat16)), (parent, dev(par))):
+            to[:T].copy_(new)
+        layer.place(counts, max_rows=most, drafts=True)
+        g.replay()
+        before = m.rows
+        m.rows = [np.concatenate([m.rows[b], xb[row0[b]:row0[b + 1]]]) for b in range(2)]
+        pool, table, page, lens = m.dense()
+        ref = oracle.drafts.attention(qb, pool, table, page, row0, lens, par, SCALE, window, sink)
+        check_attn((out[:T].float().cpu().numpy(), host(lse[:T])), ref, int(lens.max()), f'step {step}')
+        keep = [[i for i in range(n) if r.random() < 0.5] for n in counts]
+        kept = np.full((2, max(1, *map(len, keep))), -1, np.int32)
+        for b, k in enumerate(keep):
+            kept[b, :len(k)] = k
+        layer.accept(dev(kept), dev(np.array([len(k) for k in keep], np.int32)), [len(k) for k in keep])
+        m.rows = [np.concatenate([before[b], xb[row0[b]:row0[b + 1]][keep[b]]]) for b in range(2)]
+        for b in range(2):
+            np.testing.assert_array_equal(rows_of(layer, b), m.rows[b])
